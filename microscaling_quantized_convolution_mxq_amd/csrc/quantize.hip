@@ -21,6 +21,7 @@
 
 #include "mx_common.h"
 #include "mqconv_internal.h"
+#include "philox.h"
 
 namespace mq {
 
@@ -45,24 +46,6 @@ namespace mq {
 // seed's two halves as key (the generator of Salmon et al., SC'11: ten rounds
 // of two 32 x 32 -> 64-bit products and key increments).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void philox4x32_10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
-                                              uint32_t k1, uint32_t (&o)[4]) {
-#pragma unroll
-  for (int r = 0; r < 10; r++) {
-    if (r > 0) {
-      k0 += 0x9E3779B9u;
-      k1 += 0xBB67AE85u;
-    }
-    const uint32_t hi0 = __umulhi(0xD2511F53u, c0), lo0 = 0xD2511F53u * c0;
-    const uint32_t hi1 = __umulhi(0xCD9E8D57u, c2), lo1 = 0xCD9E8D57u * c2;
-    c0 = hi1 ^ c1 ^ k0;
-    c1 = lo1;
-    c2 = hi0 ^ c3 ^ k1;
-    c3 = lo0;
-  }
-  o[0] = c0; o[1] = c1; o[2] = c2; o[3] = c3;
-}
-
 // The 16 values x of half a block run (channels c0 .. c0 + 15 of memory row
 // `row`, c0 a multiple of 16), divided by the block scale 2^(S - 127) and
 // rounded stochastically onto the element grid; the results are grid points
