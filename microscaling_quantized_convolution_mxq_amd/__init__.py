@@ -430,3 +430,11 @@ def mqconv_nvfp_quantize(src, role: int, fmt: int, dims, codes, block_scales, te
                                       _buf(block_scales, mqconv_nvfp_scales_bytes(role, *d), "uint8", "block_scales"),
                                       _f32(tensor_scale, 1, "tensor_scale"), p, n, _stream(stream)),
            "mqconv_nvfp_quantize")
+
+
+# ---- operators around the convolutions (include/mqconv_block.h) ---------------------
+from .block import (ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, CACHE_COUNT_MAX, EXPORTED_BLOCK, NORM_BWD,  # noqa: E402,F401
+                    NORM_FWD, MxCache, mq_drop, mq_norm, mqconv_cache_codes_bytes, mqconv_cache_read,
+                    mqconv_cache_read_mx, mqconv_cache_scales_bytes, mqconv_cache_write, mqconv_dropout,
+                    mqconv_dropout_mx, mqconv_group_norm, mqconv_group_norm_backward, mqconv_group_norm_backward_mx,
+                    mqconv_group_norm_mx, mqconv_group_norm_workspace_bytes)

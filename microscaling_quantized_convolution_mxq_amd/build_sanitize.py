@@ -19,7 +19,8 @@ import sys
 
 from microscaling_quantized_convolution_mxq_amd import build as b
 
-SANITIZED = ["mqconv_api.hip", "quantize.hip", "layout.hip", "naive.hip", "nvfp.hip"]
+SANITIZED = ["mqconv_api.hip", "quantize.hip", "layout.hip", "naive.hip", "nvfp.hip",
+             "block_api.hip", "dropout.hip", "norm.hip", "norm_mx.hip", "cache.hip"]
 OUT = os.path.join(b.BUILD, "sanitize")
 LIB = os.path.join(OUT, "libmqconv_sanitize.so")
 # host-only sanitizer flags: each one after -Xarch_host

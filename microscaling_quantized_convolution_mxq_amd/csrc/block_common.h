@@ -1,0 +1,145 @@
+// block_common.h -- device-side pieces of the group norm, dropout and replay
+// cache kernels: channel octets of fp32 rows, activations and their slopes,
+// and the dropout factor of an element.
+//
+// Values that two kernels must agree on to the bit (an fp32 result and the MX
+// codes of the same result) are written with explicit fused multiply-adds and
+// contraction off, so that no kernel rounds them in its own way.
+#pragma once
+#include "mx_common.h"
+#include "mqconv_internal.h"
+#include "philox.h"
+
+namespace mq {
+
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+
+// Four floats at any 4-byte aligned address (one 16-byte access: global
+// memory accesses need no more than dword alignment).
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// cnt (of 8, or of 16) consecutive values at p; zeros past cnt.
+template <int K>
+__device__ __forceinline__ void load_run(const float* p, int cnt, float (&v)[K]) {
+  if (cnt >= K) {
+#pragma unroll
+    for (int i = 0; i < K; i += 4) {
+      const f4u t = *reinterpret_cast<const f4u*>(p + i);
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[i + j] = t[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < K; i++) v[i] = i < cnt ? p[i] : 0.0f;
+  }
+}
+template <int K>
+__device__ __forceinline__ void store_run(float* p, int cnt, const float (&v)[K]) {
+  if (cnt >= K) {
+#pragma unroll
+    for (int i = 0; i < K; i += 4) {
+      f4u t;
+#pragma unroll
+      for (int j = 0; j < 4; j++) t[j] = v[i + j];
+      *reinterpret_cast<f4u*>(p + i) = t;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < K; i++)
+      if (i < cnt) p[i] = v[i];
+  }
+}
+
+// exp(-u): 2^t of the rounded product t = -u log2(e), corrected to first
+// order by what the product lost. u is held to [-87, 87], where both the
+// exponential and its reciprocal are normal numbers; a sigmoid is 0 or 1 to
+// fp32 well before that.
+__device__ __forceinline__ float exp_neg(float u) {
+#pragma clang fp contract(off)
+  constexpr float L = -1.4426950408889634f, Ll = (float)(-1.4426950408889634 - (double)L);
+  u = __builtin_amdgcn_fmed3f(u, -87.0f, 87.0f);
+  const float t = u * L;
+  const float r = __builtin_fmaf(u, Ll, __builtin_fmaf(u, L, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * 0.69314718f, e);
+}
+__device__ __forceinline__ float sigmoid(float u) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(u)); }
+__device__ __forceinline__ float normal_cdf(float u) {
+#pragma clang fp contract(off)
+  return 0.5f * (1.0f + erff(u * 0.70710678f));
+}
+
+// The activation of every value of u, in place (act is uniform).
+template <int K>
+__device__ __forceinline__ void act_values(int act, float (&u)[K]) {
+#pragma clang fp contract(off)
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < K; i++) u[i] = u[i] * sigmoid(u[i]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < K; i++) u[i] = u[i] < 0.0f ? 0.0f : u[i];
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < K; i++) u[i] = u[i] * normal_cdf(u[i]);
+  }
+}
+// g *= act'(u).
+template <int K>
+__device__ __forceinline__ void act_slopes(int act, const float (&u)[K], float (&g)[K]) {
+#pragma clang fp contract(off)
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < K; i++) {
+      const float s = sigmoid(u[i]);
+      g[i] = g[i] * (s * __builtin_fmaf(u[i], 1.0f - s, 1.0f));
+    }
+  } else if (act == kActRelu) {
+    // (a product, not a select: a NaN in u or g stays one)
+#pragma unroll
+    for (int i = 0; i < K; i++) g[i] = u[i] != u[i] ? u[i] : g[i] * (u[i] > 0.0f ? 1.0f : 0.0f);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < K; i++)
+      g[i] = g[i] * __builtin_fmaf(u[i] * 0.39894228f, exp_neg(0.5f * u[i] * u[i]), normal_cdf(u[i]));
+  }
+}
+
+// Dropout of one call: elements whose 16-bit number is below q are dropped
+// (q = 0: none are), the others multiplied by scale.
+struct DropArgs {
+  uint64_t seed;
+  const uint64_t* step;
+  uint32_t q;
+  float scale;
+};
+struct DropKey {
+  uint32_t k0, k1;
+};
+__device__ __forceinline__ DropKey drop_key(const DropArgs& d) {
+  if (d.q == 0) return DropKey{0, 0};
+  const uint64_t s = d.seed + (d.step ? *d.step : 0);
+  return DropKey{(uint32_t)s, (uint32_t)(s >> 32)};
+}
+// Dropout of channels c0 .. c0 + K - 1 (c0 a multiple of 8) of a row: one
+// Philox block, eight 16-bit numbers, for each octet of channels. 32 bits an
+// element would double the generator's work (20 64-bit products a block, about
+// as long as the memory takes to bring the eight values) for a probability
+// that is finer than 1.5e-5.
+template <int K>
+__device__ __forceinline__ void drop_values(const DropArgs& d, const DropKey& k, uint32_t row, uint32_t c0,
+                                            float (&v)[K]) {
+  if (d.q == 0) return;
+#pragma unroll
+  for (int b = 0; b < K / 8; b++) {
+    uint32_t o[4];
+    philox4x32_10(row, (c0 >> 3) + b, 1u, 0u, k.k0, k.k1, o);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint32_t r = (i & 1) ? o[i >> 1] >> 16 : o[i >> 1] & 0xffffu;
+      v[8 * b + i] = r < d.q ? 0.0f : v[8 * b + i] * d.scale;
+    }
+  }
+}
+
+}  // namespace mq

@@ -1,0 +1,858 @@
+// norm.hip -- group normalization with an activation, channels last, and its
+// gradient: statistics, sums, and the elementwise passes with fp32 output.
+//
+// All of it is memory bound (10-30 operations for each value of 4 to 12
+// bytes). A pixel's row holds every sample and channel side by side, so a
+// thread takes an octet of neighbouring channels of one sample and walks over
+// the pixels: loads are whole lines, and what belongs to its columns stays in
+// registers.
+//   One pass: where a slab of whole groups over all pixels fits the registers
+//     of a workgroup, that workgroup reads it once, joins the statistics in
+//     LDS and writes the result from its registers: one launch, no workspace.
+//   Streaming: partial statistics (a mean and a sum of squares around it) or
+//     sums of chunks of pixels, joined per group by a second kernel in a fixed
+//     order, and an elementwise pass that reads x (and dy) again.
+// Sums of values are fp64 (two operations a value, hidden behind the loads),
+// so a mean is its fp32 rounding, whatever cancels in it; squares are summed
+// in fp32 around means of the values themselves, so a mean far from zero
+// costs no digits, and joined in fp64.
+#include <algorithm>
+
+#include "norm.h"
+
+namespace mq {
+
+namespace {
+
+constexpr int kOneR = 8;  // most pixels a thread of the one-pass kernels holds
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+}  // namespace
+
+NormGeo norm_geo(const NormShape& s, bool backward) {
+  NormGeo g{};
+  g.P = s.P; g.N = s.N; g.C = s.C; g.G = s.G;
+  g.D = s.C / s.G;
+  g.NO = ceil_div(s.C, 8);
+  g.TO = s.N * g.NO;
+  g.UW = backward ? 1 : gcd(g.D, 8);  // the backward sums columns (dgamma, dbeta)
+  g.e = g.D / g.UW;
+  g.dNO = make_fastdiv((unsigned)g.NO);
+  g.dD = make_fastdiv((unsigned)g.D);
+
+  // a slab is a run of octets that ends where a group does: multiples of
+  // lcm(D, 8) channels where they divide C, else whole samples
+  const long long L = (long long)g.D / gcd(g.D, 8) * 8;
+  const bool within = s.C % L == 0;
+  const int unit = within ? (int)(L / 8) : g.NO;
+  const int tmax = backward || g.UW == 1 ? 512 : 1024;
+  if (unit <= tmax) {
+    // at least a cache line's 32 channels, and enough octets that a
+    // workgroup of few pixels has 256 threads
+    long long so = unit * (long long)ceil_div(4, unit);
+    so = std::max(so, unit * (long long)ceil_div(256, (long long)std::min(s.P, 256) * unit));
+    so = std::min(so, (long long)tmax / unit * unit);
+    so = std::min(so, (long long)ceil_div(g.TO, unit) * unit);
+    for (int t = 256; t <= tmax && !g.one; t *= 2) {
+      if (so > t) continue;
+      const int ty = std::min(s.P, t / (int)so);
+      // (1,024 threads have 128 registers each, room for half as many pixels)
+      if (ceil_div(s.P, ty) > (t > 512 ? kOneR / 2 : kOneR)) continue;
+      g.one = true;
+      g.so = (int)so;
+      g.ty1 = ty;
+      g.T1 = ceil_div((long long)so * ty, 64) * 64;
+      g.nslab = ceil_div(g.TO, so);
+      g.nseg = within ? (int)(so * 8 / g.D) : (int)(so / g.NO) * g.G;
+    }
+  }
+
+  // streaming tiles: the split of a row into column tiles that leaves the
+  // fewest of 256 threads idle
+  double best = 0;
+  const int n0 = ceil_div(g.TO, 256);
+  for (int nt = n0; nt < n0 + 4; nt++) {
+    const int tx = ceil_div(g.TO, nt), ty = 256 / tx;
+    const double use = (double)g.TO / nt * ty / 256;
+    if (use > best * 1.05) {
+      best = use;
+      g.ntile = nt; g.tx = tx; g.ty = std::min(ty, s.P);
+    }
+  }
+  // about four workgroups per compute unit, of at least four pixels a thread
+  const int want = std::max(1, std::min(1024 / std::min(1024, g.ntile), ceil_div(s.P, 4 * g.ty)));
+  g.ppc = ceil_div(ceil_div(s.P, want), g.ty) * g.ty;
+  g.nchunk = ceil_div(s.P, g.ppc);
+  return g;
+}
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// shared pieces
+// ---------------------------------------------------------------------------
+// a thread's octet
+struct Oct {
+  int n, c0, cnt;
+  long long col;  // n * C + c0
+};
+__device__ __forceinline__ Oct octet(const NormGeo& g, int o, bool active) {
+  Oct t;
+  t.n = (int)fdiv((unsigned)(active ? o : 0), g.dNO);
+  t.c0 = ((active ? o : 0) - t.n * g.NO) * 8;
+  t.cnt = active ? min(8, g.C - t.c0) : 0;
+  t.col = (long long)t.n * g.C + t.c0;
+  return t;
+}
+
+// gamma (1 where there is none) and beta of an octet
+__device__ __forceinline__ void affine(const NormArgs& a, const Oct& t, float (&ga)[8], float (&be)[8]) {
+  load_run<8>(a.beta + t.c0, a.beta ? t.cnt : 0, be);
+  load_run<8>(a.gamma + t.c0, a.gamma ? t.cnt : 0, ga);
+  if (!a.gamma) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) ga[i] = i < t.cnt ? 1.0f : 0.0f;
+  }
+}
+
+// Statistics of some values: a mean m + lo (m is its fp32 rounding) and the
+// sum q of squared deviations from m. With c values their sum is c (m + lo)
+// and the sum of their squares q + c m (m + 2 lo).
+using Part = NormPart;
+struct Sums {
+  double s = 0, sq = 0;
+  __device__ void add(const Part& p, double c) {
+    s += c * ((double)p.m + p.lo);
+    sq += (double)p.q + c * p.m * ((double)p.m + 2.0 * p.lo);
+  }
+};
+__device__ __forceinline__ Part part_of(double sum, double n, float m, float q) {
+  return Part{m, (float)(sum / n - (double)m), q};
+}
+
+// Joins `n` values of mean m and squared deviations q into (mean, m2) of
+// `have` ones.
+__device__ __forceinline__ void join(float& mean, float& m2, float have, float m, float q, float n) {
+  const float f = n / (have + n);
+  const float d = m - mean;
+  mean = __builtin_fmaf(d, f, mean);
+  m2 = m2 + __builtin_fmaf(d * d, have * f, q);
+}
+
+// sum, mean (rounded) and sum of squared deviations of the UW values of every
+// unit of an octet over the first `rows` of R rows (the others hold zeros)
+template <int R, int UW>
+__device__ __forceinline__ void unit_stats(const float (&v)[R][8], int rows, double (&sum)[8 / UW],
+                                           float (&mean)[8 / UW], float (&m2)[8 / UW]) {
+  const float inv = 1.0f / (float)(rows * UW);
+#pragma unroll
+  for (int u = 0; u < 8 / UW; u++) {
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < R; k++)
+#pragma unroll
+      for (int i = 0; i < UW; i++) s += (double)v[k][u * UW + i];
+    sum[u] = s;
+    const float m = (float)s * inv;
+    float q = 0.0f;
+#pragma unroll
+    for (int k = 0; k < R; k++)
+#pragma unroll
+      for (int i = 0; i < UW; i++) {
+        const float d = v[k][u * UW + i] - m;
+        q += k < rows ? d * d : 0.0f;
+      }
+    mean[u] = m;
+    m2[u] = q;
+  }
+}
+
+// mean and rstd of M values
+__device__ __forceinline__ float2 finish_stats(const Sums& t, double M, float eps) {
+  const double mean = t.s / M;
+  double var = t.sq / M - mean * mean;
+  if (var < 0.0) var = 0.0;
+  return make_float2((float)mean, (float)(1.0 / sqrt(var + (double)eps)));
+}
+
+__device__ __forceinline__ double group_sum(double v, int lanes) {  // aligned groups of lanes (a power of two)
+  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// lanes that reduce one segment together: a power of two up to 64
+__device__ __forceinline__ int seg_lanes(int threads, int nseg) {
+  int t = 1;
+  while (t < 64 && 2 * t * nseg <= threads) t <<= 1;
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// forward, one pass
+// ---------------------------------------------------------------------------
+template <int R, int UW>
+__global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_kernel(const NormArgs a) {
+  constexpr int UN = 8 / UW;
+  extern __shared__ float2 sh[];
+  const NormGeo& g = a.g;
+  const int W = g.so * UN;           // units of the slab
+  float2* const sseg = sh;           // [nseg]
+  Part* const su = reinterpret_cast<Part*>(sh + g.nseg);  // [ty1][W]
+  const int ox = (int)threadIdx.x % g.so, py = (int)threadIdx.x / g.so;
+  const int o0 = blockIdx.x * g.so;
+  const bool active = py < g.ty1 && o0 + ox < g.TO;
+  const Oct t = octet(g, o0 + ox, active);
+  const long long stride = (long long)g.N * g.C;
+  const int rows = active ? (g.P - py + g.ty1 - 1) / g.ty1 : 0;  // pixels py, py + ty1, ...
+  float v[R][8];
+#pragma unroll
+  for (int k = 0; k < R; k++) load_run<8>(a.x + (py + k * g.ty1) * stride + t.col, k < rows ? t.cnt : 0, v[k]);
+  if (active) {
+    double sum[UN];
+    float mean[UN], m2[UN];
+    unit_stats<R, UW>(v, rows, sum, mean, m2);
+#pragma unroll
+    for (int u = 0; u < UN; u++) su[py * W + ox * UN + u] = part_of(sum[u], (double)(rows * UW), mean[u], m2[u]);
+  }
+  __syncthreads();
+  // segments (sample, group) of the slab: e units each, over ty1 rows
+  const int n0 = (int)fdiv((unsigned)o0, g.dNO);
+  const int S0 = n0 * g.G + (o0 - n0 * g.NO) * 8 / g.D;
+  {
+    const int lanes = seg_lanes((int)blockDim.x, g.nseg);
+    const int j = (int)threadIdx.x & (lanes - 1);
+    const double M = (double)g.P * g.D;
+    for (int s = (int)threadIdx.x / lanes; s < g.nseg && S0 + s < g.N * g.G; s += (int)blockDim.x / lanes) {
+      const int S = S0 + s, n = S / g.G, gr = S - n * g.G;
+      const int pos = (n * g.NO - o0) * UN + gr * g.e;
+      Sums sum;
+      for (int i = j; i < g.ty1 * g.e; i += lanes) {
+        const int row = i / g.e;
+        sum.add(su[row * W + pos + (i - row * g.e)], (double)(((g.P - row + g.ty1 - 1) / g.ty1) * UW));
+      }
+      sum.s = group_sum(sum.s, lanes);
+      sum.sq = group_sum(sum.sq, lanes);
+      if (j == 0) {
+        const float2 st = finish_stats(sum, M, a.eps);
+        sseg[s] = st;
+        if (a.mean) a.mean[S] = st.x;
+        if (a.rstd) a.rstd[S] = st.y;
+      }
+    }
+  }
+  __syncthreads();
+  if (!active) return;
+  float mean[8], ga[8], be[8];
+  affine(a, t, ga, be);
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int s = t.n * g.G + (int)fdiv((unsigned)(t.c0 + (i < t.cnt ? i : 0)), g.dD) - S0;
+    const float2 st = sseg[s];
+    mean[i] = i < t.cnt ? st.x : 0.0f;
+    ga[i] = i < t.cnt ? st.y * ga[i] : 0.0f;
+  }
+  if (a.out) {
+    const DropKey key = drop_key(a.drop);
+#pragma unroll
+    for (int k = 0; k < R; k++)
+      if (k < rows) {
+        const int p = py + k * g.ty1;
+        float u[8];
+        norm_values<8>(mean, ga, be, v[k], u);
+        act_values<8>(a.act, u);
+        drop_values<8>(a.drop, key, (uint32_t)p * g.N + t.n, t.c0, u);
+        store_run<8>(a.out + p * stride + t.col, t.cnt, u);
+      }
+  } else if (py == 0) {
+    store_run<8>(a.col.mean + t.col, t.cnt, mean);
+    store_run<8>(a.col.a + t.col, t.cnt, ga);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// forward, streaming
+// ---------------------------------------------------------------------------
+constexpr int kBatch = 4;  // pixels a thread has in flight
+
+template <int UW>
+__global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
+  constexpr int UN = 8 / UW;
+  __shared__ Part su[256 * UN];
+  const NormGeo& g = a.g;
+  const int chunk = (int)blockIdx.x / g.ntile, tile = (int)blockIdx.x - chunk * g.ntile;
+  const int ox = (int)threadIdx.x % g.tx, py = (int)threadIdx.x / g.tx;
+  const int o = tile * g.tx + ox;
+  const bool active = py < g.ty && o < g.TO;
+  const Oct t = octet(g, o, active);
+  const long long stride = (long long)g.N * g.C;
+  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
+  double sum[UN];
+  float mean[UN], m2[UN], have = 0.0f;
+#pragma unroll
+  for (int u = 0; u < UN; u++) sum[u] = mean[u] = m2[u] = 0.0f;
+  if (active) {
+    const float* src = a.x + t.col;
+    for (int p = p0 + py; p < p1; p += kBatch * g.ty) {
+      const int rows = min(kBatch, (p1 - p + g.ty - 1) / g.ty);
+      float v[kBatch][8], bm[UN], bq[UN];
+      double bs[UN];
+#pragma unroll
+      for (int k = 0; k < kBatch; k++)
+        load_run<8>(src + (p + (long long)k * g.ty) * stride, k < rows ? t.cnt : 0, v[k]);
+      unit_stats<kBatch, UW>(v, rows, bs, bm, bq);
+      const float n = (float)(rows * UW);
+#pragma unroll
+      for (int u = 0; u < UN; u++) {
+        sum[u] += bs[u];
+        join(mean[u], m2[u], have, bm[u], bq[u], n);
+      }
+      have += n;
+    }
+  }
+  const int W = g.tx * UN;
+  if (py < g.ty)
+#pragma unroll
+    for (int u = 0; u < UN; u++) su[py * W + ox * UN + u] = part_of(sum[u], (double)have, mean[u], m2[u]);
+  __syncthreads();
+  // units of the tile, joined over the rows of pixels
+  const int NU = g.N * g.C / UW;
+  for (int i = (int)threadIdx.x; i < W; i += 256) {
+    const int oo = tile * g.tx + i / UN, u = i % UN;
+    if (oo >= g.TO) continue;
+    const Oct q = octet(g, oo, true);
+    if (u * UW >= q.cnt) continue;
+    Sums s;
+    for (int r = 0; r < g.ty && p0 + r < p1; r++)
+      s.add(su[r * W + i], (double)(((p1 - p0 - r + g.ty - 1) / g.ty) * UW));
+    const double c = (double)(p1 - p0) * UW, m = s.s / c;
+    a.part[(long long)chunk * NU + (q.col / UW + u)] = part_of(s.s, c, (float)m, (float)(s.sq - m * s.s));
+  }
+}
+
+// Segments of a workgroup of the joining kernels: neighbouring ones, at least
+// 16 units side by side.
+__host__ __device__ inline int join_segs(int e) { return e >= 16 ? 1 : 16 / e; }
+
+// Joins the chunks' statistics of every (sample, group) and spreads them over
+// its columns.
+__global__ __launch_bounds__(256) void norm_join_kernel(const NormArgs a) {
+  __shared__ double rs[256], rq[256];
+  __shared__ float2 sseg[16];
+  const NormGeo& g = a.g;
+  const int NS = g.N * g.G, spw = join_segs(g.e);
+  const int S0 = (int)blockIdx.x * spw, ns = min(spw, NS - S0);
+  const int W = ns * g.e;  // units of this workgroup
+  const int NU = g.N * g.C / g.UW;
+  const Part* part = a.part + (long long)S0 * g.e;
+  const int tid = (int)threadIdx.x;
+  const int wide = W < 256 ? W : 256, rows = 256 / wide;
+  const int r = tid / wide;
+  Sums s;
+  if (r < rows)
+    for (int u = tid - r * wide; u < W; u += wide)
+      for (int k = r; k < g.nchunk; k += rows)
+        s.add(part[(long long)k * NU + u], (double)(min(g.P, (k + 1) * g.ppc) - k * g.ppc) * g.UW);
+  rs[tid] = s.s;
+  rq[tid] = s.sq;
+  __syncthreads();
+  if (tid < ns) {
+    Sums t;
+    const int e = min(g.e, wide);
+    for (int k = 0; k < rows; k++)
+      for (int i = 0; i < e; i++) {
+        t.s += rs[k * wide + tid * e + i];
+        t.sq += rq[k * wide + tid * e + i];
+      }
+    const float2 st = finish_stats(t, (double)g.P * g.D, a.eps);
+    sseg[tid] = st;
+    if (a.mean) a.mean[S0 + tid] = st.x;
+    if (a.rstd) a.rstd[S0 + tid] = st.y;
+  }
+  __syncthreads();
+  const long long col0 = (long long)S0 * g.D;
+  for (int i = tid; i < ns * g.D; i += 256) {
+    const float2 st = sseg[i / g.D];
+    const int c = (int)((col0 + i) % g.C);
+    a.col.mean[col0 + i] = st.x;
+    a.col.a[col0 + i] = st.y * (a.gamma ? a.gamma[c] : 1.0f);
+  }
+}
+
+__global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
+  const NormGeo& g = a.g;
+  const int chunk = (int)blockIdx.x / g.ntile, tile = (int)blockIdx.x - chunk * g.ntile;
+  const int ox = (int)threadIdx.x % g.tx, py = (int)threadIdx.x / g.tx;
+  const int o = tile * g.tx + ox;
+  if (py >= g.ty || o >= g.TO) return;
+  const Oct t = octet(g, o, true);
+  const long long stride = (long long)g.N * g.C;
+  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
+  float mean[8], ga[8], be[8];
+  load_run<8>(a.col.mean + t.col, t.cnt, mean);
+  load_run<8>(a.col.a + t.col, t.cnt, ga);
+  load_run<8>(a.beta + t.c0, a.beta ? t.cnt : 0, be);
+  const DropKey key = drop_key(a.drop);
+  for (int p = p0 + py; p < p1; p += kBatch * g.ty) {
+    float v[kBatch][8];
+#pragma unroll
+    for (int k = 0; k < kBatch; k++) {
+      const int q = p + k * g.ty;
+      load_run<8>(a.x + q * stride + t.col, q < p1 ? t.cnt : 0, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; k++) {
+      const int q = p + k * g.ty;
+      if (q >= p1) break;
+      float u[8];
+      norm_values<8>(mean, ga, be, v[k], u);
+      act_values<8>(a.act, u);
+      drop_values<8>(a.drop, key, (uint32_t)q * g.N + t.n, t.c0, u);
+      store_run<8>(a.out + q * stride + t.col, t.cnt, u);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+// mean and gamma * rstd of an octet from the forward's statistics
+__device__ __forceinline__ void grad_params(const NormArgs& a, const Oct& t, float (&mean)[8], float (&rstd)[8],
+                                            float (&ga)[8], float (&be)[8]) {
+  const NormGeo& g = a.g;
+  affine(a, t, ga, be);
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const bool ok = i < t.cnt;
+    const int s = t.n * g.G + (int)fdiv((unsigned)(t.c0 + (ok ? i : 0)), g.dD);
+    mean[i] = ok ? a.mean_in[s] : 0.0f;
+    rstd[i] = ok ? a.rstd_in[s] : 0.0f;
+    ga[i] = rstd[i] * ga[i];
+  }
+}
+
+// adds g and g * (x - mean) of one pixel to the octet's sums; d and gr are
+// left holding x - mean and g
+__device__ __forceinline__ void grad_terms(const NormArgs& a, const DropKey& key, const Oct& t, int p,
+                                           const float (&mean)[8], const float (&ga)[8], const float (&be)[8],
+                                           float (&d)[8], float (&gr)[8]) {
+  float u[8];
+  norm_values<8>(mean, ga, be, d, u);
+  drop_values<8>(a.drop, key, (uint32_t)p * a.g.N + t.n, t.c0, gr);
+  act_slopes<8>(a.act, u, gr);
+}
+
+// k1 = rstd * mean_M(gamma g) and k2 = rstd^2 * mean_M(gamma g xh) of a group
+// from the sums of gamma g and gamma g xh
+__device__ __forceinline__ float2 grad_means(double s1, double s2, double M, float rstd) {
+  return make_float2((float)((double)rstd * s1 / M), (float)((double)rstd * rstd * s2 / M));
+}
+
+template <int R>
+__global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a) {
+  extern __shared__ float2 sh[];
+  const NormGeo& g = a.g;
+  const int W = g.so * 8;             // columns of the slab (some past a sample's last channel)
+  float2* const su = sh;              // [ty1][W], then the columns' sums in its first row
+  float2* const sseg = sh + g.ty1 * W;
+  const int ox = (int)threadIdx.x % g.so, py = (int)threadIdx.x / g.so;
+  const int o0 = blockIdx.x * g.so;
+  const bool active = py < g.ty1 && o0 + ox < g.TO;
+  const Oct t = octet(g, o0 + ox, active);
+  const long long stride = (long long)g.N * g.C;
+  const int rows = active ? (g.P - py + g.ty1 - 1) / g.ty1 : 0;
+  float d[R][8], gr[R][8];
+#pragma unroll
+  for (int k = 0; k < R; k++) {
+    const int cnt = k < rows ? t.cnt : 0;
+    load_run<8>(a.x + (py + k * g.ty1) * stride + t.col, cnt, d[k]);
+    load_run<8>(a.dy + (py + k * g.ty1) * stride + t.col, cnt, gr[k]);
+  }
+  float mean[8], rstd[8], ga[8], be[8];
+  const DropKey key = drop_key(a.drop);
+  if (active) {
+    grad_params(a, t, mean, rstd, ga, be);
+    float s1[8], s2[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) s1[i] = s2[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < R; k++)
+      if (k < rows) {
+        grad_terms(a, key, t, py + k * g.ty1, mean, ga, be, d[k], gr[k]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          s1[i] += gr[k][i];
+          s2[i] = __builtin_fmaf(gr[k][i], d[k][i], s2[i]);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 8; i++) su[py * W + ox * 8 + i] = make_float2(s1[i], s2[i] * rstd[i]);
+  }
+  __syncthreads();
+  // the columns' sums over the rows
+  for (int i = (int)threadIdx.x; i < W; i += (int)blockDim.x) {
+    const int oo = o0 + (i >> 3);
+    if (oo >= g.TO) continue;
+    const Oct q = octet(g, oo, true);
+    if ((i & 7) >= q.cnt) continue;
+    double s1 = 0, s2 = 0;
+    for (int r = 0; r < g.ty1; r++) {
+      s1 += su[r * W + i].x;
+      s2 += su[r * W + i].y;
+    }
+    const float2 tot = make_float2((float)s1, (float)s2);
+    su[i] = tot;
+    a.tot[q.col + (i & 7)] = tot;
+  }
+  __syncthreads();
+  const int n0 = (int)fdiv((unsigned)o0, g.dNO);
+  const int S0 = n0 * g.G + (o0 - n0 * g.NO) * 8 / g.D;
+  {
+    const int lanes = seg_lanes((int)blockDim.x, g.nseg);
+    const int j = (int)threadIdx.x & (lanes - 1);
+    const double M = (double)g.P * g.D;
+    for (int s = (int)threadIdx.x / lanes; s < g.nseg && S0 + s < g.N * g.G; s += (int)blockDim.x / lanes) {
+      const int S = S0 + s, n = S / g.G, grp = S - n * g.G;
+      const int pos = (n * g.NO - o0) * 8 + grp * g.D;
+      double s1 = 0, s2 = 0;
+      for (int i = j; i < g.D; i += lanes) {
+        const float2 w = su[pos + i];
+        const double gm = a.gamma ? (double)a.gamma[grp * g.D + i] : 1.0;
+        s1 += gm * w.x;
+        s2 += gm * w.y;
+      }
+      s1 = group_sum(s1, lanes);
+      s2 = group_sum(s2, lanes);
+      if (j == 0) sseg[s] = grad_means(s1, s2, M, a.rstd_in[S]);
+    }
+  }
+  __syncthreads();
+  if (!active) return;
+  float k1[8], k2[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const bool ok = i < t.cnt;
+    const float2 k = sseg[t.n * g.G + (int)fdiv((unsigned)(t.c0 + (ok ? i : 0)), g.dD) - S0];
+    k1[i] = ok ? k.x : 0.0f;
+    k2[i] = ok ? k.y : 0.0f;
+  }
+  if (a.out) {
+#pragma unroll
+    for (int k = 0; k < R; k++)
+      if (k < rows) {
+        float dx[8];
+        norm_grad_values<8>(ga, k1, k2, d[k], gr[k], dx);
+        store_run<8>(a.out + (py + k * g.ty1) * stride + t.col, t.cnt, dx);
+      }
+  } else if (py == 0) {
+    store_run<8>(a.col.mean + t.col, t.cnt, mean);
+    store_run<8>(a.col.a + t.col, t.cnt, ga);
+    store_run<8>(a.col.k1 + t.col, t.cnt, k1);
+    store_run<8>(a.col.k2 + t.col, t.cnt, k2);
+  }
+}
+
+// dgamma and dbeta behind the one-pass kernel
+__global__ __launch_bounds__(256) void norm_channel_kernel(const NormArgs a) { norm_channel_sums(a, blockIdx.x); }
+
+__global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
+  __shared__ float2 su[256 * 8];
+  const NormGeo& g = a.g;
+  const int chunk = (int)blockIdx.x / g.ntile, tile = (int)blockIdx.x - chunk * g.ntile;
+  const int ox = (int)threadIdx.x % g.tx, py = (int)threadIdx.x / g.tx;
+  const int o = tile * g.tx + ox;
+  const bool active = py < g.ty && o < g.TO;
+  const Oct t = octet(g, o, active);
+  const long long stride = (long long)g.N * g.C;
+  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
+  float s1[8], s2[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) s1[i] = s2[i] = 0.0f;
+  if (active) {
+    float mean[8], rstd[8], ga[8], be[8];
+    grad_params(a, t, mean, rstd, ga, be);
+    const DropKey key = drop_key(a.drop);
+    constexpr int B = kBatch / 2;  // two tensors
+    for (int p = p0 + py; p < p1; p += B * g.ty) {
+      float d[B][8], gr[B][8];
+#pragma unroll
+      for (int k = 0; k < B; k++) {
+        const int q = p + k * g.ty, cnt = q < p1 ? t.cnt : 0;
+        load_run<8>(a.x + q * stride + t.col, cnt, d[k]);
+        load_run<8>(a.dy + q * stride + t.col, cnt, gr[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < B; k++) {
+        const int q = p + k * g.ty;
+        if (q >= p1) break;
+        grad_terms(a, key, t, q, mean, ga, be, d[k], gr[k]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          s1[i] += gr[k][i];
+          s2[i] = __builtin_fmaf(gr[k][i], d[k][i], s2[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) s2[i] *= rstd[i];
+  }
+  const int W = g.tx * 8;
+  if (py < g.ty)
+#pragma unroll
+    for (int i = 0; i < 8; i++) su[py * W + ox * 8 + i] = make_float2(s1[i], s2[i]);
+  __syncthreads();
+  const long long NC = stride;
+  for (int i = (int)threadIdx.x; i < W; i += 256) {
+    const int oo = tile * g.tx + (i >> 3);
+    if (oo >= g.TO) continue;
+    const Oct q = octet(g, oo, true);
+    if ((i & 7) >= q.cnt) continue;
+    double a1 = 0, a2 = 0;
+    for (int r = 0; r < g.ty; r++) {
+      a1 += su[r * W + i].x;
+      a2 += su[r * W + i].y;
+    }
+    a.psum[chunk * NC + q.col + (i & 7)] = make_float2((float)a1, (float)a2);
+  }
+}
+
+// Joins the chunks' sums of every column, and the columns of every (sample,
+// group), whose two means are spread over its columns.
+__global__ __launch_bounds__(256) void norm_join_backward_kernel(const NormArgs a) {
+  __shared__ double r1[256], r2[256];
+  __shared__ float2 sseg[16];
+  const NormGeo& g = a.g;
+  const int NS = g.N * g.G, spw = join_segs(g.D);
+  const int S0 = (int)blockIdx.x * spw, ns = min(spw, NS - S0);
+  const int W = ns * g.D;
+  const long long NC = (long long)g.N * g.C, col0 = (long long)S0 * g.D;
+  const float2* part = a.psum + col0;
+  const int tid = (int)threadIdx.x;
+  const int wide = W < 256 ? W : 256, rows = 256 / wide;
+  const int r = tid / wide, u0 = tid - r * wide;
+  // per pass of `wide` columns: sums over the chunks, joined over the rows of
+  // threads, scaled by gamma and gathered per segment
+  double g1 = 0, g2 = 0;  // this thread's share of its segment (r == 0)
+  for (int u = u0; u - u0 < W; u += wide) {
+    double s1 = 0, s2 = 0;
+    if (r < rows && u < W)
+      for (int k = r; k < g.nchunk; k += rows) {
+        const float2 w = part[k * NC + u];
+        s1 += w.x;
+        s2 += w.y;
+      }
+    r1[tid] = s1;
+    r2[tid] = s2;
+    __syncthreads();
+    if (r == 0 && u < W) {
+      for (int k = 1; k < rows; k++) {
+        s1 += r1[k * wide + tid];
+        s2 += r2[k * wide + tid];
+      }
+      a.tot[col0 + u] = make_float2((float)s1, (float)s2);
+      const int c = (int)((col0 + u) % g.C);
+      const double gm = a.gamma ? (double)a.gamma[c] : 1.0;
+      g1 += gm * s1;
+      g2 += gm * s2;
+    }
+    __syncthreads();
+  }
+  r1[tid] = g1;
+  r2[tid] = g2;
+  __syncthreads();
+  if (tid < ns) {
+    double s1 = 0, s2 = 0;
+    const int e = min(g.D, wide);
+    for (int i = 0; i < e; i++) {
+      s1 += r1[tid * e + i];
+      s2 += r2[tid * e + i];
+    }
+    sseg[tid] = grad_means(s1, s2, (double)g.P * g.D, a.rstd_in[S0 + tid]);
+  }
+  __syncthreads();
+  for (int i = tid; i < W; i += 256) {
+    const int s = i / g.D, c = (int)((col0 + i) % g.C);
+    a.col.mean[col0 + i] = a.mean_in[S0 + s];
+    a.col.a[col0 + i] = a.rstd_in[S0 + s] * (a.gamma ? a.gamma[c] : 1.0f);
+    a.col.k1[col0 + i] = sseg[s].x;
+    a.col.k2[col0 + i] = sseg[s].y;
+  }
+}
+
+__global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs a) {
+  const NormGeo& g = a.g;
+  if ((int)blockIdx.x >= g.ntile * g.nchunk) {
+    norm_channel_sums(a, (int)blockIdx.x - g.ntile * g.nchunk);
+    return;
+  }
+  const int chunk = (int)blockIdx.x / g.ntile, tile = (int)blockIdx.x - chunk * g.ntile;
+  const int ox = (int)threadIdx.x % g.tx, py = (int)threadIdx.x / g.tx;
+  const int o = tile * g.tx + ox;
+  if (py >= g.ty || o >= g.TO) return;
+  const Oct t = octet(g, o, true);
+  const long long stride = (long long)g.N * g.C;
+  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
+  float mean[8], ga[8], be[8], k1[8], k2[8];
+  load_run<8>(a.col.mean + t.col, t.cnt, mean);
+  load_run<8>(a.col.a + t.col, t.cnt, ga);
+  load_run<8>(a.col.k1 + t.col, t.cnt, k1);
+  load_run<8>(a.col.k2 + t.col, t.cnt, k2);
+  load_run<8>(a.beta + t.c0, a.beta ? t.cnt : 0, be);
+  const DropKey key = drop_key(a.drop);
+  constexpr int B = kBatch / 2;
+  for (int p = p0 + py; p < p1; p += B * g.ty) {
+    float d[B][8], gr[B][8];
+#pragma unroll
+    for (int k = 0; k < B; k++) {
+      const int q = p + k * g.ty, cnt = q < p1 ? t.cnt : 0;
+      load_run<8>(a.x + q * stride + t.col, cnt, d[k]);
+      load_run<8>(a.dy + q * stride + t.col, cnt, gr[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < B; k++) {
+      const int q = p + k * g.ty;
+      if (q >= p1) break;
+      grad_terms(a, key, t, q, mean, ga, be, d[k], gr[k]);
+      float dx[8];
+      norm_grad_values<8>(ga, k1, k2, d[k], gr[k], dx);
+      store_run<8>(a.out + q * stride + t.col, t.cnt, dx);
+    }
+  }
+}
+
+size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+// The workspace's parts: the columns' parameters, the backward's sums, and
+// the chunks' partial statistics.
+struct NormWs {
+  size_t cols, tot, part, bytes;
+};
+NormWs norm_ws(const NormGeo& g, bool backward) {
+  NormWs w{};
+  const size_t nc = (size_t)g.N * g.C;
+  w.cols = align256(nc * sizeof(float));
+  w.tot = w.cols * (backward ? 4 : 2);
+  w.part = w.tot + (backward ? align256(nc * sizeof(float2)) : 0);
+  const size_t each = backward ? sizeof(float2) : sizeof(Part);
+  w.bytes = w.part + (g.one ? 0 : (size_t)g.nchunk * (nc / g.UW) * each);
+  return w;
+}
+
+void bind_ws(NormArgs& a, void* ws, bool backward) {
+  const NormWs w = norm_ws(a.g, backward);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  a.col.mean = reinterpret_cast<float*>(b);
+  a.col.a = reinterpret_cast<float*>(b + w.cols);
+  if (backward) {
+    a.col.k1 = reinterpret_cast<float*>(b + 2 * w.cols);
+    a.col.k2 = reinterpret_cast<float*>(b + 3 * w.cols);
+    a.tot = reinterpret_cast<float2*>(b + w.tot);
+    a.psum = reinterpret_cast<float2*>(b + w.part);
+  } else {
+    a.part = reinterpret_cast<Part*>(b + w.part);
+  }
+}
+
+template <int UW>
+void launch_one(const NormArgs& a, hipStream_t st) {
+  const NormGeo& g = a.g;
+  const int R = ceil_div(g.P, g.ty1);
+  const size_t lds = (size_t)(g.ty1 * g.so * (8 / UW)) * sizeof(Part) + (size_t)g.nseg * sizeof(float2);
+  const dim3 grid((unsigned)g.nslab), wg((unsigned)g.T1);
+  if (R <= 1) hipLaunchKernelGGL((norm_one_kernel<1, UW>), grid, wg, lds, st, a);
+  else if (R <= 2) hipLaunchKernelGGL((norm_one_kernel<2, UW>), grid, wg, lds, st, a);
+  else if (R <= 4) hipLaunchKernelGGL((norm_one_kernel<4, UW>), grid, wg, lds, st, a);
+  else hipLaunchKernelGGL((norm_one_kernel<kOneR, UW>), grid, wg, lds, st, a);
+}
+
+}  // namespace
+
+size_t norm_workspace_bytes(const NormShape& s, int op) { return norm_ws(norm_geo(s, op == 1), op == 1).bytes; }
+
+hipError_t launch_group_norm(const NormShape& s, const float* x, const float* gamma, const float* beta,
+                             const DropSpec& drop, float* y, const MxOutView& yq, float* mean, float* rstd, void* ws,
+                             hipStream_t st) {
+  NormArgs a{};
+  a.g = norm_geo(s, false);
+  a.x = x; a.gamma = gamma; a.beta = beta; a.mean = mean; a.rstd = rstd; a.out = y;
+  a.act = s.act; a.eps = s.eps; a.drop = drop_args(drop);
+  bind_ws(a, ws, false);
+  const NormGeo& g = a.g;
+  hipError_t e;
+  if (g.one) {
+    switch (g.UW) {
+      case 1: launch_one<1>(a, st); break;
+      case 2: launch_one<2>(a, st); break;
+      case 4: launch_one<4>(a, st); break;
+      default: launch_one<8>(a, st); break;
+    }
+    e = launch_check();
+    if (e != hipSuccess || y) return e;
+  } else {
+    const dim3 grid((unsigned)(g.ntile * g.nchunk));
+    switch (g.UW) {
+      case 1: hipLaunchKernelGGL(norm_stats_kernel<1>, grid, dim3(256), 0, st, a); break;
+      case 2: hipLaunchKernelGGL(norm_stats_kernel<2>, grid, dim3(256), 0, st, a); break;
+      case 4: hipLaunchKernelGGL(norm_stats_kernel<4>, grid, dim3(256), 0, st, a); break;
+      default: hipLaunchKernelGGL(norm_stats_kernel<8>, grid, dim3(256), 0, st, a); break;
+    }
+    e = launch_check();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)ceil_div((long long)g.N * g.G, join_segs(g.e))), dim3(256), 0,
+                       st, a);
+    e = launch_check();
+    if (e != hipSuccess) return e;
+    if (y) {
+      hipLaunchKernelGGL(norm_apply_kernel, grid, dim3(256), 0, st, a);
+      return launch_check();
+    }
+  }
+  return launch_norm_mx(a, yq, st);
+}
+
+hipError_t launch_group_norm_backward(const NormShape& s, const float* dy, const float* x, const float* gamma,
+                                      const float* beta, const float* mean, const float* rstd, const DropSpec& drop,
+                                      float* dx, const MxOutView& dxq, float* dgamma, float* dbeta, void* ws,
+                                      hipStream_t st) {
+  NormArgs a{};
+  a.g = norm_geo(s, true);
+  a.x = x; a.dy = dy; a.gamma = gamma; a.beta = beta; a.mean_in = mean; a.rstd_in = rstd; a.out = dx;
+  a.dgamma = dgamma; a.dbeta = dbeta;
+  a.act = s.act; a.eps = s.eps; a.drop = drop_args(drop);
+  bind_ws(a, ws, true);
+  const NormGeo& g = a.g;
+  const int extra = dgamma || dbeta ? ceil_div(g.C, 256) : 0;
+  hipError_t e;
+  if (g.one) {
+    const int R = ceil_div(g.P, g.ty1);
+    const size_t lds = ((size_t)g.ty1 * g.so * 8 + g.nseg) * sizeof(float2);
+    const dim3 grid((unsigned)g.nslab), wg((unsigned)g.T1);
+    if (R <= 1) hipLaunchKernelGGL(norm_one_backward_kernel<1>, grid, wg, lds, st, a);
+    else if (R <= 2) hipLaunchKernelGGL(norm_one_backward_kernel<2>, grid, wg, lds, st, a);
+    else if (R <= 4) hipLaunchKernelGGL(norm_one_backward_kernel<4>, grid, wg, lds, st, a);
+    else hipLaunchKernelGGL(norm_one_backward_kernel<kOneR>, grid, wg, lds, st, a);
+    e = launch_check();
+    if (e != hipSuccess) return e;
+    if (dx) {
+      if (!extra) return e;
+      hipLaunchKernelGGL(norm_channel_kernel, dim3((unsigned)extra), dim3(256), 0, st, a);
+      return launch_check();
+    }
+  } else {
+    const dim3 grid((unsigned)(g.ntile * g.nchunk));
+    hipLaunchKernelGGL(norm_sums_kernel, grid, dim3(256), 0, st, a);
+    e = launch_check();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(norm_join_backward_kernel, dim3((unsigned)ceil_div((long long)g.N * g.G, join_segs(g.D))),
+                       dim3(256), 0, st, a);
+    e = launch_check();
+    if (e != hipSuccess) return e;
+    if (dx) {
+      hipLaunchKernelGGL(norm_apply_backward_kernel, dim3(grid.x + (unsigned)extra), dim3(256), 0, st, a);
+      return launch_check();
+    }
+  }
+  return launch_norm_backward_mx(a, dxq, extra, st);
+}
+
+}  // namespace mq

@@ -1,0 +1,360 @@
+"""Group norm with an activation and its gradient on the GPU: fp32 results
+element by element against the fp64 oracle, MX results bit for bit against
+the quantization of the fp32 ones, non-finite values, in-place calls, streams,
+graphs and injected failures.
+
+Bounds are derived, with e = 2^-24 and K = 64 roundings' room for statistics
+(chunks of sums joined in fp64) and the elementwise steps:
+  |u - u'|  <= K e (|a| (|x| + |mean|) + |beta|) =: du,  a = gamma * rstd
+  |y - y'|  <= factor * (1.2 du + K e |y|)               (|act'| <= 1.13)
+  |g - g'|  <= |dy| factor (0.9 du + K e)                (|act''| <= 0.8)
+  |xh - xh'| <= K e rstd (|x| + |mean|) =: dxh
+and the same carried through the formula of dx. ReLU's slope jumps at 0:
+dy is 0 where u lies within du of it."""
+import numpy as np
+import pytest
+import torch
+
+import microscaling_quantized_convolution_mxq_amd as mq
+from oracle import block
+from gpu_common import dev, host, say, workspace
+
+pytestmark = pytest.mark.gpu
+E, K, EPS = 2.0 ** -24, 64, 1e-5
+
+# (H, W, N, C, groups): single values, one pixel (tokens), odd extents and
+# channel counts, groups smaller and larger than an octet, one-pass and
+# streaming sizes, a group too large for one workgroup
+SHAPES = [
+    (1, 1, 1, 1, 1), (1, 1, 1, 8, 2), (1, 1, 300, 64, 1), (1, 1, 7, 1000, 1), (1, 1, 33, 40, 40), (16, 16, 2, 32, 8),
+    (5, 3, 33, 45, 9), (19, 23, 5, 90, 9), (20, 20, 8, 64, 8), (31, 33, 2, 24, 24), (40, 40, 3, 96, 4),
+    (64, 48, 3, 30, 3), (80, 80, 4, 64, 16), (9, 7, 1, 9008, 1), (33, 31, 2, 2048, 1), (75, 75, 1, 3, 1),
+    (57, 61, 17, 33, 11),
+]
+
+
+def _inputs(shape, seed, offset=0.3):
+    h, w, n, c, _ = shape
+    rng = np.random.default_rng(seed)
+    x = (rng.standard_normal((h, w, n, c)) * (0.5 + rng.random(c)) + offset * rng.standard_normal(c)).astype(np.float32)
+    dy = rng.standard_normal((h, w, n, c)).astype(np.float32)
+    gamma = (1 + 0.2 * rng.standard_normal(c)).astype(np.float32)
+    beta = (0.3 * rng.standard_normal(c)).astype(np.float32)
+    return x, dy, gamma, beta
+
+
+def _forward(shape, x, gamma, beta, act, drop=None, mx=None, y=None, stream=None, eps=EPS):
+    h, w, n, c, g = shape
+    gn = mq.mq_norm(h, w, n, c, g, act, eps)
+    mean = torch.full((n, g), float("nan"), device="cuda")
+    rstd = torch.full((n, g), float("nan"), device="cuda")
+    ws = workspace(mq.mqconv_group_norm_workspace_bytes(gn, mq.NORM_FWD))
+    if mx is None:
+        if y is None:
+            y = torch.full((h, w, n, c), float("nan"), device="cuda")
+        mq.mqconv_group_norm(gn, x, gamma, beta, y, mean, rstd, ws, drop=drop, stream=stream)
+        return y, mean, rstd
+    t = mq.MxTensor.empty(mq.ROLE_ACT, mx[0], mx[1], (h, w, n, c))
+    t.codes.fill_(0xAB)
+    t.scales.fill_(0xAB)
+    mq.mqconv_group_norm_mx(gn, x, gamma, beta, t, mean, rstd, ws, drop=drop, stream=stream)
+    return t, mean, rstd
+
+
+def _backward(shape, dy, x, gamma, beta, mean, rstd, act, drop=None, mx=None, dx=None):
+    h, w, n, c, g = shape
+    gn = mq.mq_norm(h, w, n, c, g, act, EPS)
+    dg = torch.full((c,), float("nan"), device="cuda")
+    db = torch.full((c,), float("nan"), device="cuda")
+    ws = workspace(mq.mqconv_group_norm_workspace_bytes(gn, mq.NORM_BWD))
+    if mx is None:
+        if dx is None:
+            dx = torch.full((h, w, n, c), float("nan"), device="cuda")
+        mq.mqconv_group_norm_backward(gn, dy, x, gamma, beta, mean, rstd, dx, dg, db, ws, drop=drop)
+        return dx, dg, db
+    t = mq.MxTensor.empty(mq.ROLE_GRAD, mx[0], mx[1], (h, w, n, c))
+    t.codes.fill_(0xAB)
+    t.scales.fill_(0xAB)
+    mq.mqconv_group_norm_backward_mx(gn, dy, x, gamma, beta, mean, rstd, t, dg, db, ws, drop=drop)
+    return t, dg, db
+
+
+def _close(name, got, ref, tol):
+    got = np.asarray(got, np.float64)
+    assert np.isfinite(got).all(), f"{name}: non-finite"
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), (f"{name}: {bad.sum()} of {bad.size} beyond the bound, first at {tuple(np.argwhere(bad)[0])}: "
+                           f"{got[bad][0]!r} for {ref[bad][0]!r}, bound {np.broadcast_to(tol, ref.shape)[bad][0]:.3e}")
+
+
+def _spread(v, d):
+    return np.repeat(v, d, axis=1)
+
+
+def _check_forward(shape, x, gamma, beta, act, got, factor, y=None):
+    g, d = shape[4], shape[3] // shape[4]
+    ga = np.ones(shape[3]) if gamma is None else gamma.astype(np.float64)
+    be = np.zeros(shape[3]) if beta is None else beta.astype(np.float64)
+    ref, mean, rstd, u = block.group_norm(x, ga, be, g, act, EPS, factor)
+    xa = np.abs(x.astype(np.float64))
+    gmean = lambda v: v.reshape(-1, shape[2], g, d).mean(axis=(0, 3))  # noqa: E731
+    _close("mean", host(got[1]), mean, K * E * gmean(xa) + 1e-30)
+    # rstd: d(rstd)/rstd = d(var)/2(var + eps); var's error is that of its mean and of its sum
+    _close("rstd", host(got[2]), rstd, K * E * rstd * (1 + rstd * np.sqrt(gmean(xa * xa))))
+    m, r = _spread(mean, d), _spread(rstd, d)
+    du = K * E * (np.abs(ga) * r * (xa + np.abs(m)) * (1 + r * _spread(np.sqrt(gmean(xa * xa)), d) * E) + np.abs(be))
+    _close("y", host(got[0]), ref, factor * (1.2 * du + K * E * np.abs(ref)) + 1e-30)
+
+
+def _factor(shape, p, seed):
+    return block.drop_factor(shape[:4], p, seed) if p else np.ones(shape[:4])
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward_and_backward_fp32(shape):
+    for act, p, affine in ((mq.ACT_SILU, 0.0, True), (mq.ACT_NONE, 0.3, True), (mq.ACT_GELU, 0.1, False),
+                           (mq.ACT_RELU, 0.0, True)):
+        say(f"norm {shape} act={act} p={p} affine={affine}")
+        x, dy, gamma, beta = _inputs(shape, sum(shape) + act)
+        if not affine:
+            gamma = beta = None
+        seed = 0xABCDEF0123456789 + act
+        drop = mq.mq_drop(p, seed) if p else None
+        factor = _factor(shape, p, seed)
+        X, DY = dev(x), dev(dy)
+        G, B = (None, None) if gamma is None else (dev(gamma), dev(beta))
+        got = _forward(shape, X, G, B, act, drop)
+        _check_forward(shape, x, gamma, beta, act, got, factor)
+        if act == mq.ACT_RELU:
+            _, m, r, u = block.group_norm(x, gamma, beta, shape[4], act, EPS)
+            m, r = _spread(m, shape[3] // shape[4]), _spread(r, shape[3] // shape[4])
+            dy[np.abs(u) <= 2 * K * E * (np.abs(gamma) * r * (np.abs(x) + np.abs(m)) + np.abs(beta))] = 0
+            DY = dev(dy)
+
+        # backward, from the statistics that the forward pass kept
+        mean, rstd = host(got[1]), host(got[2])
+        ga = np.ones(shape[3]) if gamma is None else gamma.astype(np.float64)
+        be = np.zeros(shape[3]) if beta is None else beta.astype(np.float64)
+        dx, dgamma, dbeta, q = block.group_norm_backward(dy, x, ga, be, mean, rstd, shape[4], act, factor)
+        d = shape[3] // shape[4]
+        m, r = _spread(mean.astype(np.float64), d), _spread(rstd.astype(np.float64), d)
+        dxh = K * E * r * (np.abs(x) + np.abs(m))
+        du = np.abs(ga) * dxh + K * E * np.abs(be)
+        assert act != mq.ACT_RELU or (dy[np.abs(q["u"]) <= du] == 0).all()
+        dg = np.abs(dy) * factor * (0.9 * du + K * E)
+        a, fold, xh, gg = np.abs(ga), q["fold"], np.abs(q["xh"]), np.abs(q["g"] * ga)
+        B1 = np.abs(fold(q["g"] * ga * q["xh"]))
+        tol = r * (a * dg + fold(a * dg) + xh * fold(a * dg * xh + gg * dxh) + dxh * B1 +
+                   K * E * (gg + fold(gg) + xh * fold(gg * xh)))
+        out = _backward(shape, DY, X, G, B, got[1], got[2], act, drop)
+        _close("dx", host(out[0]), dx, tol + 1e-30)
+        _close("dgamma", host(out[1]), dgamma, (dg * xh + np.abs(q["g"]) * dxh + K * E * np.abs(q["g"]) * xh).sum(axis=(0, 1, 2)) + 1e-30)
+        _close("dbeta", host(out[2]), dbeta, (dg + K * E * np.abs(q["g"])).sum(axis=(0, 1, 2)) + 1e-30)
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 2, 32, 8), (57, 61, 3, 33, 11)], ids=str)
+def test_gradient_against_differences(shape):
+    """dL/ds of L = sum(dy * y) along a direction, by fp64 differences of the forward formula. The fp32 gradient's error along
+    a direction is at most its elementwise error; 1e-4 of the sum of its terms' sizes is far above that and far below a
+    wrong term."""
+    say(f"norm gradient by differences {shape}")
+    x, dy, gamma, beta = _inputs(shape, 5)
+    factor = _factor(shape, 0.2, 99)
+    drop = mq.mq_drop(0.2, 99)
+    _, mean, rstd = _forward(shape, dev(x), dev(gamma), dev(beta), mq.ACT_SILU, drop)
+    dx, dg, db = (host(t).astype(np.float64) for t in _backward(shape, dev(dy), dev(x), dev(gamma), dev(beta), mean, rstd, mq.ACT_SILU, drop))
+    rng = np.random.default_rng(6)
+    v, vg, vb = rng.standard_normal(x.shape), rng.standard_normal(shape[3]), rng.standard_normal(shape[3])
+    f = lambda s: (block.group_norm(x + s * v, gamma + s * vg, beta + s * vb, shape[4], mq.ACT_SILU, EPS, factor)[0] * dy).sum()  # noqa: E731
+    h = 1e-4
+    terms = (dx * v, dg * vg, db * vb)
+    assert abs((f(h) - f(-h)) / (2 * h) - sum(t.sum() for t in terms)) <= 1e-4 * sum(np.abs(t).sum() for t in terms)
+
+
+MX_SHAPES = [(1, 1, 1, 1, 1), (1, 1, 300, 64, 1), (5, 3, 33, 45, 9), (19, 23, 5, 90, 9), (20, 20, 32, 64, 8),
+             (40, 24, 16, 64, 16), (31, 33, 2, 300, 3), (7, 6, 40, 320, 20), (75, 75, 1, 3, 1), (57, 61, 17, 33, 11)]
+
+
+def _same_codes(t, ref, label):
+    np.testing.assert_array_equal(host(t.scales), host(ref.scales), err_msg=f"scales {label}")
+    np.testing.assert_array_equal(host(t.codes), host(ref.codes), err_msg=f"codes {label}")
+
+
+@pytest.mark.parametrize("shape", MX_SHAPES, ids=str)
+@pytest.mark.parametrize("fmt", range(5))
+def test_mx_results_are_the_quantized_fp32_results(shape, fmt):
+    x, dy, gamma, beta = (dev(a) for a in _inputs(shape, 40 + fmt))
+    for bp, act, p in ((32, mq.ACT_SILU, 0.25), (1, mq.ACT_NONE, 0.0), (1, mq.ACT_RELU, 0.1), (32, mq.ACT_GELU, 0.0)):
+        say(f"norm mx {shape} fmt={fmt} bp={bp} act={act} p={p}")
+        drop = mq.mq_drop(p, 31) if p else None
+        y, mean, rstd = _forward(shape, x, gamma, beta, act, drop)
+        t, mean2, rstd2 = _forward(shape, x, gamma, beta, act, drop, mx=(fmt, bp))
+        assert torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+        ref = mq.MxTensor.empty(mq.ROLE_ACT, fmt, bp, shape[:4])
+        mq.mqconv_quantize(y, ref)
+        _same_codes(t, ref, f"y {shape} {act}")
+        dx, dg, db = _backward(shape, dy, x, gamma, beta, mean, rstd, act, drop)
+        t, dg2, db2 = _backward(shape, dy, x, gamma, beta, mean, rstd, act, drop, mx=(fmt, bp))
+        assert torch.equal(dg, dg2) and torch.equal(db, db2)
+        ref = mq.MxTensor.empty(mq.ROLE_GRAD, fmt, bp, shape[:4])
+        mq.mqconv_quantize(dx, ref)
+        _same_codes(t, ref, f"dx {shape} {act}")
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 4, 32, 8), (80, 80, 4, 64, 16)], ids=str)
+def test_a_mean_far_from_zero_keeps_its_digits(shape):
+    """x = 1000 + noise: sums of squares around zero would lose every digit of the variance."""
+    say(f"norm far mean {shape}")
+    x, _, gamma, beta = _inputs(shape, 8)
+    x = (x + np.float32(1000)).astype(np.float32)
+    got = _forward(shape, dev(x), dev(gamma), dev(beta), mq.ACT_NONE)
+    _check_forward(shape, x, gamma, beta, mq.ACT_NONE, got, np.ones(shape[:4]))
+    _, mean, rstd, _ = block.group_norm(x, gamma, beta, shape[4], 0, EPS)
+    # around local means the variance keeps 2^-24 (mean / std) relative to its square root's scale
+    assert (np.abs(host(got[2]) - rstd) / rstd).max() < 1e-4
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 4, 32, 8), (64, 64, 4, 64, 16)], ids=str)
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+def test_non_finite_values_stay_in_their_group(shape, value):
+    say(f"norm non-finite {shape} {value}")
+    x, dy, gamma, beta = _inputs(shape, 12)
+    d = shape[3] // shape[4]
+    clean = _forward(shape, dev(x), dev(gamma), dev(beta), mq.ACT_SILU)
+    ref = _backward(shape, dev(dy), dev(x), dev(gamma), dev(beta), clean[1], clean[2], mq.ACT_SILU)
+    x[3, 5, 2, d] = value  # sample 2, group 1
+    got = _forward(shape, dev(x), dev(gamma), dev(beta), mq.ACT_SILU)
+    out = _backward(shape, dev(dy), dev(x), dev(gamma), dev(beta), got[1], got[2], mq.ACT_SILU)
+    inside = np.zeros(shape[:4], bool)
+    inside[:, :, 2, d:2 * d] = True
+    for name, a, b in (("y", got[0], clean[0]), ("dx", out[0], ref[0])):
+        a, b = host(a), host(b)
+        assert np.isnan(a[inside]).all(), name
+        np.testing.assert_array_equal(a[~inside], b[~inside], err_msg=name)
+    assert np.isnan(host(got[2])[2, 1]) and np.isfinite(np.delete(host(got[2]).reshape(-1), 2 * shape[4] + 1)).all()
+    t, _, _ = _forward(shape, dev(x), dev(gamma), dev(beta), mq.ACT_SILU, mx=(0, 32))
+    q = mq.MxTensor.empty(mq.ROLE_ACT, 0, 32, shape[:4])
+    mq.mqconv_quantize(got[0], q)
+    _same_codes(t, q, "non-finite")
+
+
+def test_constant_groups_and_zero_gradients():
+    """A group of equal values has variance 0: xh = 0, y = act(beta); eps = 0 makes it NaN as the formula does; a zero gradient
+    gives zeros."""
+    shape = (6, 5, 3, 16, 4)
+    x = np.full(shape[:4], 2.5, np.float32)
+    _, dy, gamma, beta = _inputs(shape, 3)
+    y, mean, rstd = _forward(shape, dev(x), dev(gamma), dev(beta), mq.ACT_NONE)
+    assert (host(mean) == 2.5).all()
+    np.testing.assert_array_equal(host(y), np.broadcast_to(beta, shape[:4]))
+    dx, dg, db = _backward(shape, dev(np.zeros_like(x)), dev(x), dev(gamma), dev(beta), mean, rstd, mq.ACT_NONE)
+    assert not host(dx).any() and not host(dg).any() and not host(db).any()
+    y, _, rstd = _forward(shape, dev(x), dev(gamma), dev(beta), mq.ACT_NONE, eps=0.0)
+    assert np.isinf(host(rstd)).all() and np.isnan(host(y)).all()
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 4, 32, 8), (64, 64, 4, 64, 16)], ids=str)
+def test_in_place_optional_outputs_and_another_stream(shape):
+    say(f"norm in place {shape}")
+    h, w, n, c, g = shape
+    x, dy, gamma, beta = (dev(a) for a in _inputs(shape, 21))
+    y, mean, rstd = _forward(shape, x, gamma, beta, mq.ACT_SILU)
+    dx, dg, db = _backward(shape, dy, x, gamma, beta, mean, rstd, mq.ACT_SILU)
+    z = x.clone()
+    _forward(shape, z, gamma, beta, mq.ACT_SILU, y=z)
+    assert torch.equal(z, y)
+    z = dy.clone()
+    _backward(shape, z, x, gamma, beta, mean, rstd, mq.ACT_SILU, dx=z)
+    assert torch.equal(z, dx)
+    z = x.clone()
+    _backward(shape, dy, z, gamma, beta, mean, rstd, mq.ACT_SILU, dx=z)
+    assert torch.equal(z, dx)
+    gn = mq.mq_norm(h, w, n, c, g, mq.ACT_SILU, EPS)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y2, dx2 = torch.empty_like(y), torch.empty_like(dx)
+    w0 = workspace(mq.mqconv_group_norm_workspace_bytes(gn, 0))
+    w1 = workspace(mq.mqconv_group_norm_workspace_bytes(gn, 1))
+    mq.mqconv_group_norm(gn, x, gamma, beta, y2, ws=w0, stream=s)
+    mq.mqconv_group_norm_backward(gn, dy, x, gamma, beta, mean, rstd, dx2, ws=w1, stream=s)
+    s.synchronize()
+    assert torch.equal(y2, y) and torch.equal(dx2, dx)
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 4, 32, 8), (64, 64, 4, 64, 16)], ids=str)
+def test_graph_replays_draw_a_new_mask_each_step(shape):
+    """A captured forward and backward with a step counter: every replay equals the eager calls at its step, and steps differ."""
+    say(f"norm graph {shape}")
+    h, w, n, c, g = shape
+    x, dy, gamma, beta = (dev(a) for a in _inputs(shape, 30))
+    gn = mq.mq_norm(h, w, n, c, g, mq.ACT_SILU, EPS)
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    drop = mq.mq_drop(0.5, 2**64 - 2, step)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(n, g, device="cuda"), torch.empty(n, g, device="cuda")
+    dg, db = torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    yq = mq.MxTensor.empty(mq.ROLE_ACT, 0, 32, shape[:4])
+    ws = workspace(max(mq.mqconv_group_norm_workspace_bytes(gn, k) for k in (0, 1)))
+    outs = (y, mean, rstd, dx, dg, db, yq.codes, yq.scales)
+
+    def path():
+        mq.mqconv_group_norm(gn, x, gamma, beta, y, mean, rstd, ws, drop=drop)
+        mq.mqconv_group_norm_mx(gn, x, gamma, beta, yq, ws=ws, drop=drop)
+        mq.mqconv_group_norm_backward(gn, dy, x, gamma, beta, mean, rstd, dx, dg, db, ws, drop=drop)
+
+    eager = []
+    for k in range(4):  # the seed passes 2^64 on the way
+        step.fill_(k)
+        path()
+        eager.append([t.clone() for t in outs])
+    assert not torch.equal(eager[0][0], eager[1][0]) and not torch.equal(eager[2][3], eager[3][3])
+    seeds = [(2**64 - 2 + k) % 2**64 for k in range(4)]
+    for k in (0, 3):
+        assert (host(eager[k][0]) == 0).sum() >= (block.drop_factor(shape[:4], 0.5, seeds[k]) == 0).sum()
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        path()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            path()
+    torch.cuda.synchronize()
+    for k in (2, 0, 3, 1, 1):
+        for t in outs:
+            t.fill_(0x5A if t.dtype == torch.uint8 else float("nan"))
+        step.fill_(k)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.synchronize()
+        for i, (t, e) in enumerate(zip(outs, eager[k])):
+            assert torch.equal(t, e), f"replay at step {k}: output {i} differs"
+        path()
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 4, 32, 8), (64, 64, 4, 64, 16)], ids=str)
+def test_injected_failures_then_recovery(shape):
+    say(f"norm injected failures {shape}")
+    x, dy, gamma, beta = (dev(a) for a in _inputs(shape, 33))
+    y, mean, rstd = _forward(shape, x, gamma, beta, mq.ACT_SILU, mx=(0, 32))
+    dx, dg, db = _backward(shape, dy, x, gamma, beta, mean, rstd, mq.ACT_SILU, mx=(1, 32))
+    calls = (lambda: _forward(shape, x, gamma, beta, mq.ACT_SILU, mx=(0, 32)),
+             lambda: _backward(shape, dy, x, gamma, beta, mean, rstd, mq.ACT_SILU, mx=(1, 32)))
+    try:
+        for call, ref in zip(calls, ((y, mean, rstd), (dx, dg, db))):
+            failed = 0
+            for k in range(1, 6):
+                mq.mqconv_inject_launch_failure(k)
+                try:
+                    got = call()
+                except mq.MqConvError as e:
+                    assert e.status == -7
+                    failed += 1
+                    continue
+                mq.mqconv_inject_launch_failure(0)
+                _same_codes(got[0], ref[0], "after failures")
+                assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
+                break
+            assert failed == (2 if shape[0] == 16 else 3)
+    finally:
+        mq.mqconv_inject_launch_failure(0)
