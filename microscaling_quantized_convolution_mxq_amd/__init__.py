@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional, Sequence, Tuple, Union
 
@@ -183,10 +184,23 @@ def _ny(shape):
     return ho * wo * n * cout
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream: torch's own lookup where it has one (3 us less a call than by a Stream object)."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
+    if not _raw_stream:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -234,10 +248,12 @@ def mqconv_status_string(status: int) -> str:
     return _status_string(status)
 
 
+@functools.lru_cache(maxsize=1024)
 def mqconv_codes_bytes(role: int, fmt: int, d0: int, d1: int, d2: int, d3: int) -> int:
     return lib().mqconv_codes_bytes(role, fmt, d0, d1, d2, d3)
 
 
+@functools.lru_cache(maxsize=1024)
 def mqconv_scales_bytes(role: int, bp: int, d0: int, d1: int, d2: int, d3: int) -> int:
     return lib().mqconv_scales_bytes(role, bp, d0, d1, d2, d3)
 

@@ -12,16 +12,25 @@
 
 namespace mq {
 
-enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+// kActAny (as a template argument): the kernel takes the activation from its
+// arguments. GELU's erf costs registers that the other activations' kernels
+// need for values in flight, so whole-octet tensors take kernels of their own
+// activation.
+enum { kActAny = -1, kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 
 // Four floats at any 4-byte aligned address (one 16-byte access: global
 // memory accesses need no more than dword alignment).
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 
-// cnt (of 8, or of 16) consecutive values at p; zeros past cnt.
-template <int K>
+// cnt (of 8, or of 16) consecutive values at p; zeros past cnt. FULL: all K
+// whatever cnt is, so p must be readable. Channel counts that are multiples
+// of K take such kernels, whose loads stand under no condition (their callers
+// move an address out of range to one in range and leave its values out): the
+// compiler can then count which loads are under way, and waits for a pixel's
+// values only, not for those it has just requested.
+template <int K, bool FULL = false>
 __device__ __forceinline__ void load_run(const float* p, int cnt, float (&v)[K]) {
-  if (cnt >= K) {
+  if (FULL || cnt >= K) {
 #pragma unroll
     for (int i = 0; i < K; i += 4) {
       const f4u t = *reinterpret_cast<const f4u*>(p + i);
@@ -33,9 +42,9 @@ __device__ __forceinline__ void load_run(const float* p, int cnt, float (&v)[K])
     for (int i = 0; i < K; i++) v[i] = i < cnt ? p[i] : 0.0f;
   }
 }
-template <int K>
+template <int K, bool FULL = false>
 __device__ __forceinline__ void store_run(float* p, int cnt, const float (&v)[K]) {
-  if (cnt >= K) {
+  if (FULL ? cnt > 0 : cnt >= K) {
 #pragma unroll
     for (int i = 0; i < K; i += 4) {
       f4u t;
@@ -43,7 +52,7 @@ __device__ __forceinline__ void store_run(float* p, int cnt, const float (&v)[K]
       for (int j = 0; j < 4; j++) t[j] = v[i + j];
       *reinterpret_cast<f4u*>(p + i) = t;
     }
-  } else {
+  } else if constexpr (!FULL) {
 #pragma unroll
     for (int i = 0; i < K; i++)
       if (i < cnt) p[i] = v[i];
@@ -70,9 +79,10 @@ __device__ __forceinline__ float normal_cdf(float u) {
 }
 
 // The activation of every value of u, in place (act is uniform).
-template <int K>
+template <int ACT, int K>
 __device__ __forceinline__ void act_values(int act, float (&u)[K]) {
 #pragma clang fp contract(off)
+  if constexpr (ACT != kActAny) act = ACT;
   if (act == kActSilu) {
 #pragma unroll
     for (int i = 0; i < K; i++) u[i] = u[i] * sigmoid(u[i]);
@@ -85,9 +95,10 @@ __device__ __forceinline__ void act_values(int act, float (&u)[K]) {
   }
 }
 // g *= act'(u).
-template <int K>
+template <int ACT, int K>
 __device__ __forceinline__ void act_slopes(int act, const float (&u)[K], float (&g)[K]) {
 #pragma clang fp contract(off)
+  if constexpr (ACT != kActAny) act = ACT;
   if (act == kActSilu) {
 #pragma unroll
     for (int i = 0; i < K; i++) {

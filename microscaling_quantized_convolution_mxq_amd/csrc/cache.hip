@@ -15,16 +15,17 @@ __device__ __forceinline__ float scale_value(uint32_t S) {
   return __uint_as_float(S == 0u ? 0x00400000u : S == 255u ? 0x7fc00000u : S << 23);
 }
 
-// The value of a 6-bit code: its magnitude bits placed at the top of an fp32
-// mantissa and exponent and multiplied by 2^(127 - bias), which makes
-// subnormal codes right too.
+// The value of the 6-bit code at bit `at` of w: sign-extended from its bit 5
+// and shifted to where its magnitude is fp32 exponent and mantissa bits, with
+// the copies of the sign in between masked out, then multiplied by 2^(127 -
+// bias), which makes subnormal codes right too.
 template <int F>
-__device__ __forceinline__ float value6(uint32_t code) {
+__device__ __forceinline__ float value6(uint32_t w, int at) {
   using T = Fmt<F>;
   constexpr float up = F == 2 ? 0x1p126f : 0x1p124f;  // 2^(127 - bias)
   static_assert(T::bias == (F == 2 ? 1 : 3), "exponent bias");
-  const float a = __uint_as_float((code & 31u) << (23 - T::M)) * up;
-  return __uint_as_float(__float_as_uint(a) | (code & 32u) << 26);
+  const uint32_t code = (uint32_t)((int)(w << (26 - at)) >> 26);
+  return __uint_as_float(code << (23 - T::M) & (0x80000000u | 31u << (23 - T::M))) * up;
 }
 
 // Values of 4 codes packed in the low 4 * bits of w, times sc.
@@ -43,7 +44,7 @@ __device__ __forceinline__ void values4(uint32_t w, float sc, float (&v)[4]) {
     v[0] = a[0] * sc; v[1] = a[1] * sc; v[2] = b[0] * sc; v[3] = b[1] * sc;
   } else if constexpr (F <= 3) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) v[i] = value6<F>((w >> (6 * i)) & 63u) * sc;
+    for (int i = 0; i < 4; i++) v[i] = value6<F>(w, 6 * i) * sc;
   } else {
     const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
     const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
@@ -168,7 +169,7 @@ hipError_t launch_cache_write(const CacheView& c, const float* x, int N, int n0,
 // 1 KB of consecutive bytes. A workgroup's tile is kReadPix pixels x a few
 // samples: the scale bytes of a slot's neighbouring pixels share cache lines,
 // which one workgroup then uses up.
-constexpr int kReadPix = 16;
+constexpr int kReadPix = 16, kReadUnroll = 4;
 struct CacheRead {
   CacheView c;
   const int32_t* slot;
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const CacheRead a) {
   const int p0 = pt * kReadPix, pe = min(kReadPix, a.c.P - p0);
   const int m0 = mt * a.mb;
   const int total = pe * a.mb * a.NQ, C = a.c.C;
-  constexpr int U = 4;
+  constexpr int U = kReadUnroll;
   for (int i0 = (int)threadIdx.x; i0 < total; i0 += 256 * U) {
     uint32_t w[U], S[U];
     float* to[U];
@@ -230,8 +231,7 @@ hipError_t launch_cache_read(const CacheView& c, const int32_t* slot, int count,
   a.c = c; a.slot = slot; a.x = x; a.N = N; a.n0 = n0; a.count = count;
   a.nCB = ceil_div(c.C, 32);
   a.NQ = ceil_div(c.C, 4);
-  // about 4096 quads a workgroup
-  const int rows = 4096 / a.NQ;
+  const int rows = 512 * kReadUnroll / a.NQ;
   a.mb = rows / kReadPix;
   if (a.mb < 1) a.mb = 1;
   if (a.mb > count) a.mb = count;
@@ -262,28 +262,27 @@ struct CacheSrc {
   const int32_t* slot;
   int nCB;
   struct State {
-    long long row0;  // first row of the sample's slot (negative: none)
+    long long row0;  // first row of the sample's slot (of slot 0 where there is none)
+    bool ok;
   };
   struct Raw {
     uint32_t w[FI <= 1 ? 4 : FI <= 3 ? 3 : 2], S;
   };
-  __device__ void init(State& s, int n, int, int cnt) const {
+  __device__ void params(State&, int, int, int) const {}
+  __device__ void rows(State& s, int n, int cnt) const {
     const int k = cnt > 0 ? slot[n] : -1;
-    s.row0 = k >= 0 && k < c.slots ? (long long)k * c.P : -1;
+    s.ok = k >= 0 && k < c.slots;
+    s.row0 = s.ok ? (long long)k * c.P : 0;
   }
-  __device__ void load(const State& s, Raw& r, int p, int, int c0, int cnt) const {
+  __device__ void load(const State& s, Raw& r, int p, int, int c0, int) const {
     constexpr int NW = sizeof(r.w) / 4, RB = run_bytes_of(FI);
-#pragma unroll
-    for (int i = 0; i < NW; i++) r.w[i] = 0;
-    r.S = 0;
-    if (cnt <= 0 || s.row0 < 0) return;
     const long long run = (s.row0 + p) * nCB + (c0 >> 5);
     const uint32_t* d = reinterpret_cast<const uint32_t*>(c.codes + run * RB + ((c0 >> 4) & 1) * (RB / 2));
 #pragma unroll
     for (int i = 0; i < NW; i++) r.w[i] = d[i];
     r.S = c.scales[run];
   }
-  __device__ void values(const State&, const Raw& r, int, int, int c0, float (&v)[16]) const {
+  __device__ void values(const State& s, const Raw& r, int, int, int c0, float (&v)[16]) const {
     const float sc = scale_value(r.S);
     uint32_t w[4];  // four codes each
     if constexpr (FI <= 1) {
@@ -303,7 +302,7 @@ struct CacheSrc {
       float q[4];
       values4<FI>(w[i], sc, q);
 #pragma unroll
-      for (int j = 0; j < 4; j++) v[4 * i + j] = c0 + 4 * i + j < c.C ? q[j] : 0.0f;
+      for (int j = 0; j < 4; j++) v[4 * i + j] = s.ok && c0 + 4 * i + j < c.C ? q[j] : 0.0f;
     }
   }
   __device__ void extra(int) const {}

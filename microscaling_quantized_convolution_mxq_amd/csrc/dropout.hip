@@ -23,7 +23,7 @@ DropArgs drop_args(const DropSpec& d) {
 // A thread takes octets of channels i, i + gridDim.x * 256, ... of the
 // [rows][octets] grid, kDropUnroll of them in flight.
 constexpr int kDropUnroll = 2;
-template <bool RES>
+template <bool RES, bool FULL>
 __global__ __launch_bounds__(256) void dropout_kernel(const float* x, const float* res, float* y, int C, int NO,
                                                       FastDiv dNO, int total, DropArgs d) {
   const DropKey key = drop_key(d);
@@ -35,13 +35,13 @@ __global__ __launch_bounds__(256) void dropout_kernel(const float* x, const floa
     long long at[kDropUnroll];
 #pragma unroll
     for (int u = 0; u < kDropUnroll; u++) {
-      const int i = i0 + u * stride;  // (below 2^30 + 2^20)
-      row[u] = fdiv((unsigned)i, dNO);
-      oct[u] = (uint32_t)i - row[u] * NO;
+      const int i = i0 + u * stride, j = i < total ? i : 0;  // (i is below 2^30 + 2^20)
+      row[u] = fdiv((unsigned)j, dNO);
+      oct[u] = (uint32_t)j - row[u] * NO;
       cnt[u] = i < total ? min(8, C - (int)oct[u] * 8) : 0;
       at[u] = (long long)row[u] * C + oct[u] * 8;
-      load_run<8>(x + at[u], cnt[u], v[u]);
-      if constexpr (RES) load_run<8>(res + at[u], cnt[u], r[u]);
+      load_run<8, FULL>(x + at[u], cnt[u], v[u]);
+      if constexpr (RES) load_run<8, FULL>(res + at[u], cnt[u], r[u]);
     }
 #pragma unroll
     for (int u = 0; u < kDropUnroll; u++) {
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(const float* x, const floa
 #pragma unroll
         for (int j = 0; j < 8; j++) v[u][j] = v[u][j] + r[u][j];
       }
-      store_run<8>(y + at[u], cnt[u], v[u]);
+      store_run<8, FULL>(y + at[u], cnt[u], v[u]);
     }
   }
 }
@@ -64,14 +64,15 @@ hipError_t launch_dropout(const float* x, const float* residual, int rows, int C
   const dim3 grid((unsigned)(need < 2048 ? need : 2048));
   const FastDiv dNO = make_fastdiv((unsigned)NO);
   const DropArgs d = drop_args(drop);
-  if (residual)
-    hipLaunchKernelGGL(dropout_kernel<true>, grid, dim3(256), 0, st, x, residual, y, C, NO, dNO, total, d);
-  else
-    hipLaunchKernelGGL(dropout_kernel<false>, grid, dim3(256), 0, st, x, residual, y, C, NO, dNO, total, d);
+  const bool full = C % 8 == 0;
+  const auto kern = residual ? (full ? dropout_kernel<true, true> : dropout_kernel<true, false>)
+                             : (full ? dropout_kernel<false, true> : dropout_kernel<false, false>);
+  hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, x, residual, y, C, NO, dNO, total, d);
   return launch_check();
 }
 
 // The same values as MX codes.
+template <bool FULL>
 struct DropSrc {
   const float* x;
   int N, C;
@@ -82,9 +83,10 @@ struct DropSrc {
   struct Raw {
     float x[16];
   };
-  __device__ void init(State& s, int, int, int) const { s.key = drop_key(d); }
+  __device__ void rows(State&, int, int) const {}
+  __device__ void params(State& s, int, int, int) const { s.key = drop_key(d); }
   __device__ void load(const State&, Raw& r, int p, int n, int c0, int cnt) const {
-    load_run<16>(x + ((long long)p * N + n) * C + c0, cnt, r.x);
+    load_run<16, FULL>(x + ((long long)p * N + n) * C + c0, cnt, r.x);
   }
   __device__ void values(const State& s, const Raw& r, int p, int n, int c0, float (&v)[16]) const {
 #pragma unroll
@@ -96,8 +98,10 @@ struct DropSrc {
 
 hipError_t launch_dropout_mx(const float* x, int P, int N, int C, const DropSpec& drop, const MxOutView& out,
                              hipStream_t st) {
-  DropSrc s{x, N, C, drop_args(drop)};
-  return launch_mx_rows(out.fmt, s, mx_rows(out, P, N, C), 0, st);
+  const MxRows g = mx_rows(out, P, N, C);
+  const DropArgs d = drop_args(drop);
+  return C % 16 == 0 ? launch_mx_rows(out.fmt, DropSrc<true>{x, N, C, d}, g, 0, st)
+                     : launch_mx_rows(out.fmt, DropSrc<false>{x, N, C, d}, g, 0, st);
 }
 
 }  // namespace mq

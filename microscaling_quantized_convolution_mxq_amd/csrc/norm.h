@@ -19,9 +19,22 @@ struct NormGeo {
   // one workgroup holds a slab of `so` octets of all pixels in registers
   bool one;
   int so, ty1, T1, nslab, nseg;
-  // streaming: tiles of tx octets x chunks of ppc pixels, ty pixels at once
-  int tx, ty, ntile, nchunk, ppc;
+  // streaming: tiles of tx octets; groups of ty neighbouring pixels, of which
+  // chunk k takes groups k, k + nchunk, ... (what runs at one time is then
+  // one stretch of memory, whose lines fall on all channels alike)
+  int tx, ty, ntile, nchunk, ngroup;
 };
+// pixels of row py (of ty) in chunk k
+__device__ __forceinline__ int chunk_rows(const NormGeo& g, int k, int py) {
+  const int n = (g.ngroup - k + g.nchunk - 1) / g.nchunk;
+  const int last = g.ngroup - 1;
+  return n - (last % g.nchunk == k && last * g.ty + py >= g.P ? 1 : 0);
+}
+// pixels of chunk k
+__device__ __forceinline__ int chunk_pixels(const NormGeo& g, int k) {
+  const int n = (g.ngroup - k + g.nchunk - 1) / g.nchunk * g.ty;
+  return n - ((g.ngroup - 1) % g.nchunk == k ? g.ngroup * g.ty - g.P : 0);
+}
 NormGeo norm_geo(const NormShape& s, bool backward);
 
 // Per-column parameters of the elementwise pass, [N * C] floats each: mean
@@ -54,15 +67,40 @@ struct NormArgs {
 hipError_t launch_norm_mx(const NormArgs& a, const MxOutView& out, hipStream_t st);
 hipError_t launch_norm_backward_mx(const NormArgs& a, const MxOutView& out, int extra, hipStream_t st);
 
-// dgamma and dbeta of channels 256 b .. 256 b + 255 from the sums of every
-// sample, in their order.
+// dgamma and dbeta of channels kSumC b .. from the sums of every sample, by a
+// workgroup of up to 512 threads: thread t takes channel t % kSumC of samples
+// t / kSumC, ... (one thread a channel would wait for memory once a sample).
+constexpr int kSumC = 32;
 __device__ __forceinline__ void norm_channel_sums(const NormArgs& a, int b) {
-  for (int c = b * 256 + (int)threadIdx.x; c < min(a.g.C, b * 256 + 256); c += blockDim.x) {
-    double s1 = 0, s2 = 0;
-    for (int n = 0; n < a.g.N; n++) {
-      const float2 t = a.tot[(long long)n * a.g.C + c];
-      s1 += t.x;
-      s2 += t.y;
+  __shared__ double r1[512], r2[512];
+  const int t = (int)threadIdx.x, rows = (int)blockDim.x / kSumC, r = t / kSumC;
+  const int c = b * kSumC + t % kSumC, C = a.g.C, N = a.g.N;
+  double s1 = 0, s2 = 0;
+  if (c < C) {
+    int n = r;
+    for (; n + 3 * rows < N; n += 4 * rows) {
+      float2 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) w[j] = a.tot[(long long)(n + j * rows) * C + c];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        s1 += w[j].x;
+        s2 += w[j].y;
+      }
+    }
+    for (; n < N; n += rows) {
+      const float2 w = a.tot[(long long)n * C + c];
+      s1 += w.x;
+      s2 += w.y;
+    }
+  }
+  r1[t] = s1;
+  r2[t] = s2;
+  __syncthreads();
+  if (r == 0 && c < C) {
+    for (int k = 1; k < rows; k++) {
+      s1 += r1[k * kSumC + t];
+      s2 += r2[k * kSumC + t];
     }
     if (a.dbeta) a.dbeta[c] = (float)s1;
     if (a.dgamma) a.dgamma[c] = (float)s2;

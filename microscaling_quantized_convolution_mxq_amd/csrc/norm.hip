@@ -17,6 +17,7 @@
 // in fp32 around means of the values themselves, so a mean far from zero
 // costs no digits, and joined in fp64.
 #include <algorithm>
+#include <type_traits>
 
 #include "norm.h"
 
@@ -24,7 +25,9 @@ namespace mq {
 
 namespace {
 
-constexpr int kOneR = 8;  // most pixels a thread of the one-pass kernels holds
+constexpr int kOneR = 8;         // most pixels a thread of the one-pass kernels holds
+constexpr int kBatch = 4;        // pixels a thread of the streaming kernels has in flight
+constexpr int kStreamGroups = 1024;  // workgroups of the streaming kernels, about
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
@@ -68,22 +71,24 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
     }
   }
 
-  // streaming tiles: the split of a row into column tiles that leaves the
-  // fewest of 256 threads idle
+  // streaming tiles: about 32 octets (1 KB of a pixel's row) wide, since every
+  // chunk of pixels leaves a partial result of each column, so few wide tiles
+  // would mean many partials; of such widths the one that leaves the fewest
+  // of 256 threads idle
   double best = 0;
-  const int n0 = ceil_div(g.TO, 256);
+  const int n0 = ceil_div(g.TO, 32);
   for (int nt = n0; nt < n0 + 4; nt++) {
     const int tx = ceil_div(g.TO, nt), ty = 256 / tx;
     const double use = (double)g.TO / nt * ty / 256;
-    if (use > best * 1.05) {
+    if (use > best * 1.02) {
       best = use;
       g.ntile = nt; g.tx = tx; g.ty = std::min(ty, s.P);
     }
   }
-  // about four workgroups per compute unit, of at least four pixels a thread
-  const int want = std::max(1, std::min(1024 / std::min(1024, g.ntile), ceil_div(s.P, 4 * g.ty)));
-  g.ppc = ceil_div(ceil_div(s.P, want), g.ty) * g.ty;
-  g.nchunk = ceil_div(s.P, g.ppc);
+  // up to 1,024 workgroups (four per compute unit) of at least four pixels a
+  // thread
+  g.ngroup = ceil_div(s.P, g.ty);
+  g.nchunk = std::max(1, std::min(kStreamGroups / std::min(kStreamGroups, g.ntile), ceil_div(g.ngroup, kBatch)));
   return g;
 }
 
@@ -92,6 +97,14 @@ namespace {
 // ---------------------------------------------------------------------------
 // shared pieces
 // ---------------------------------------------------------------------------
+// Workgroups go to the eight XCDs in turn; this order gives each XCD a
+// contiguous range of the n pieces of work. Neighbouring slabs share DRAM
+// pages, and slabs eight apart would use an eighth of an XCD's L2 channels.
+__device__ __forceinline__ int xcd_order(int b, int n) {
+  const int x = b & 7, i = b >> 3, q = n >> 3, r = n & 7;
+  return x * q + min(x, r) + i;
+}
+
 // a thread's octet
 struct Oct {
   int n, c0, cnt;
@@ -106,14 +119,22 @@ __device__ __forceinline__ Oct octet(const NormGeo& g, int o, bool active) {
   return t;
 }
 
-// gamma (1 where there is none) and beta of an octet
-__device__ __forceinline__ void affine(const NormArgs& a, const Oct& t, float (&ga)[8], float (&be)[8]) {
-  load_run<8>(a.beta + t.c0, a.beta ? t.cnt : 0, be);
-  load_run<8>(a.gamma + t.c0, a.gamma ? t.cnt : 0, ga);
-  if (!a.gamma) {
+// cnt values at p + c0, or `none` where there is no p
+template <bool FULL>
+__device__ __forceinline__ void load_optional(const float* p, int c0, int cnt, float none, float (&v)[8]) {
+  if (p) {
+    load_run<8, FULL>(p + c0, cnt, v);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; i++) ga[i] = i < t.cnt ? 1.0f : 0.0f;
+    for (int i = 0; i < 8; i++) v[i] = i < cnt ? none : 0.0f;
   }
+}
+
+// gamma (1 where there is none) and beta of an octet
+template <bool FULL>
+__device__ __forceinline__ void affine(const NormArgs& a, const Oct& t, float (&ga)[8], float (&be)[8]) {
+  load_optional<FULL>(a.beta, t.c0, t.cnt, 0.0f, be);
+  load_optional<FULL>(a.gamma, t.c0, t.cnt, 1.0f, ga);
 }
 
 // Statistics of some values: a mean m + lo (m is its fp32 rounding) and the
@@ -141,7 +162,7 @@ __device__ __forceinline__ void join(float& mean, float& m2, float have, float m
 }
 
 // sum, mean (rounded) and sum of squared deviations of the UW values of every
-// unit of an octet over the first `rows` of R rows (the others hold zeros)
+// unit of an octet over the first `rows` of R rows
 template <int R, int UW>
 __device__ __forceinline__ void unit_stats(const float (&v)[R][8], int rows, double (&sum)[8 / UW],
                                            float (&mean)[8 / UW], float (&m2)[8 / UW]) {
@@ -152,7 +173,7 @@ __device__ __forceinline__ void unit_stats(const float (&v)[R][8], int rows, dou
 #pragma unroll
     for (int k = 0; k < R; k++)
 #pragma unroll
-      for (int i = 0; i < UW; i++) s += (double)v[k][u * UW + i];
+      for (int i = 0; i < UW; i++) s += k < rows ? (double)v[k][u * UW + i] : 0.0;
     sum[u] = s;
     const float m = (float)s * inv;
     float q = 0.0f;
@@ -191,7 +212,7 @@ __device__ __forceinline__ int seg_lanes(int threads, int nseg) {
 // ---------------------------------------------------------------------------
 // forward, one pass
 // ---------------------------------------------------------------------------
-template <int R, int UW>
+template <int R, int UW, bool FULL, int ACT>
 __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_kernel(const NormArgs a) {
   constexpr int UN = 8 / UW;
   extern __shared__ float2 sh[];
@@ -200,14 +221,15 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
   float2* const sseg = sh;           // [nseg]
   Part* const su = reinterpret_cast<Part*>(sh + g.nseg);  // [ty1][W]
   const int ox = (int)threadIdx.x % g.so, py = (int)threadIdx.x / g.so;
-  const int o0 = blockIdx.x * g.so;
+  const int o0 = xcd_order((int)blockIdx.x, (int)gridDim.x) * g.so;
   const bool active = py < g.ty1 && o0 + ox < g.TO;
   const Oct t = octet(g, o0 + ox, active);
   const long long stride = (long long)g.N * g.C;
   const int rows = active ? (g.P - py + g.ty1 - 1) / g.ty1 : 0;  // pixels py, py + ty1, ...
   float v[R][8];
 #pragma unroll
-  for (int k = 0; k < R; k++) load_run<8>(a.x + (py + k * g.ty1) * stride + t.col, k < rows ? t.cnt : 0, v[k]);
+  for (int k = 0; k < R; k++)
+    load_run<8, FULL>(a.x + (k < rows ? py + k * g.ty1 : 0) * stride + t.col, k < rows ? t.cnt : 0, v[k]);
   if (active) {
     double sum[UN];
     float mean[UN], m2[UN];
@@ -244,7 +266,7 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
   __syncthreads();
   if (!active) return;
   float mean[8], ga[8], be[8];
-  affine(a, t, ga, be);
+  affine<FULL>(a, t, ga, be);
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const int s = t.n * g.G + (int)fdiv((unsigned)(t.c0 + (i < t.cnt ? i : 0)), g.dD) - S0;
@@ -260,22 +282,20 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
         const int p = py + k * g.ty1;
         float u[8];
         norm_values<8>(mean, ga, be, v[k], u);
-        act_values<8>(a.act, u);
+        act_values<ACT, 8>(a.act, u);
         drop_values<8>(a.drop, key, (uint32_t)p * g.N + t.n, t.c0, u);
-        store_run<8>(a.out + p * stride + t.col, t.cnt, u);
+        store_run<8, FULL>(a.out + p * stride + t.col, t.cnt, u);
       }
   } else if (py == 0) {
-    store_run<8>(a.col.mean + t.col, t.cnt, mean);
-    store_run<8>(a.col.a + t.col, t.cnt, ga);
+    store_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
+    store_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
   }
 }
 
 // ---------------------------------------------------------------------------
 // forward, streaming
 // ---------------------------------------------------------------------------
-constexpr int kBatch = 4;  // pixels a thread has in flight
-
-template <int UW>
+template <int UW, bool FULL>
 __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
   constexpr int UN = 8 / UW;
   __shared__ Part su[256 * UN];
@@ -286,20 +306,32 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
   const bool active = py < g.ty && o < g.TO;
   const Oct t = octet(g, o, active);
   const long long stride = (long long)g.N * g.C;
-  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
+  const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;  // pixels p0, p0 + dp, ...
   double sum[UN];
   float mean[UN], m2[UN], have = 0.0f;
 #pragma unroll
   for (int u = 0; u < UN; u++) sum[u] = mean[u] = m2[u] = 0.0f;
   if (active) {
     const float* src = a.x + t.col;
-    for (int p = p0 + py; p < p1; p += kBatch * g.ty) {
-      const int rows = min(kBatch, (p1 - p + g.ty - 1) / g.ty);
+    // (the next pixels are requested before the current ones are summed)
+    float next[kBatch][8];
+    auto load = [&](int p) {
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) {
+        const int q = p + k * dp;
+        load_run<8, FULL>(src + (q < g.P ? q : 0) * stride, q < g.P ? t.cnt : 0, next[k]);
+      }
+    };
+    load(p0);
+    for (int p = p0; p < g.P; p += kBatch * dp) {
+      const int rows = min(kBatch, (g.P - p + dp - 1) / dp);
       float v[kBatch][8], bm[UN], bq[UN];
       double bs[UN];
 #pragma unroll
       for (int k = 0; k < kBatch; k++)
-        load_run<8>(src + (p + (long long)k * g.ty) * stride, k < rows ? t.cnt : 0, v[k]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[k][i] = next[k][i];
+      load(p + kBatch * dp);
       unit_stats<kBatch, UW>(v, rows, bs, bm, bq);
       const float n = (float)(rows * UW);
 #pragma unroll
@@ -323,55 +355,94 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
     const Oct q = octet(g, oo, true);
     if (u * UW >= q.cnt) continue;
     Sums s;
-    for (int r = 0; r < g.ty && p0 + r < p1; r++)
-      s.add(su[r * W + i], (double)(((p1 - p0 - r + g.ty - 1) / g.ty) * UW));
-    const double c = (double)(p1 - p0) * UW, m = s.s / c;
+    for (int r = 0; r < g.ty; r++) {
+      const int rows = chunk_rows(g, chunk, r);
+      if (rows > 0) s.add(su[r * W + i], (double)rows * UW);
+    }
+    const double c = (double)chunk_pixels(g, chunk) * UW, m = s.s / c;
     a.part[(long long)chunk * NU + (q.col / UW + u)] = part_of(s.s, c, (float)m, (float)(s.sq - m * s.s));
   }
 }
 
-// Segments of a workgroup of the joining kernels: neighbouring ones, at least
-// 16 units side by side.
-__host__ __device__ inline int join_segs(int e) { return e >= 16 ? 1 : 16 / e; }
+// ---------------------------------------------------------------------------
+// joining the chunks
+// ---------------------------------------------------------------------------
+// A joining workgroup of T threads takes W neighbouring units or columns
+// (thread t: column t % W of chunks t / W, t / W + T / W, ...). The chunks'
+// partials are few bytes but far apart, so what counts is how many of these
+// reads are under way at once: few columns a workgroup, eight reads a thread.
+constexpr int kJoinT = 256;
 
-// Joins the chunks' statistics of every (sample, group) and spreads them over
-// its columns.
-__global__ __launch_bounds__(256) void norm_join_kernel(const NormArgs a) {
-  __shared__ double rs[256], rq[256];
-  __shared__ float2 sseg[16];
+// s[r * W + u] summed over the rows r of threads into row 0 (thread order)
+__device__ __forceinline__ void join_rows(double* a, double* b, int W, int rows, int r, int t) {
+  int h = 1;
+  while (h < rows) h <<= 1;
+  for (h >>= 1; h > 0; h >>= 1) {
+    __syncthreads();
+    if (r < h && r + h < rows) {
+      a[t] += a[t + h * W];
+      b[t] += b[t + h * W];
+    }
+    rows = min(rows, h);
+  }
+  __syncthreads();
+}
+
+// Joins the chunks' statistics of neighbouring groups (spw of them, or one of
+// more than T units) and spreads them over their columns.
+template <int T>
+__global__ __launch_bounds__(T) void norm_join_kernel(const NormArgs a, int spw) {
+  __shared__ double rs[T], rq[T];
+  __shared__ float2 sseg[kJoinT];
   const NormGeo& g = a.g;
-  const int NS = g.N * g.G, spw = join_segs(g.e);
+  const int NS = g.N * g.G;
   const int S0 = (int)blockIdx.x * spw, ns = min(spw, NS - S0);
-  const int W = ns * g.e;  // units of this workgroup
+  const int units = ns * g.e, W = min(units, T), rows = T / W;
   const int NU = g.N * g.C / g.UW;
   const Part* part = a.part + (long long)S0 * g.e;
-  const int tid = (int)threadIdx.x;
-  const int wide = W < 256 ? W : 256, rows = 256 / wide;
-  const int r = tid / wide;
+  const int t = (int)threadIdx.x, r = t / W;
   Sums s;
   if (r < rows)
-    for (int u = tid - r * wide; u < W; u += wide)
-      for (int k = r; k < g.nchunk; k += rows)
-        s.add(part[(long long)k * NU + u], (double)(min(g.P, (k + 1) * g.ppc) - k * g.ppc) * g.UW);
-  rs[tid] = s.s;
-  rq[tid] = s.sq;
-  __syncthreads();
-  if (tid < ns) {
-    Sums t;
-    const int e = min(g.e, wide);
-    for (int k = 0; k < rows; k++)
-      for (int i = 0; i < e; i++) {
-        t.s += rs[k * wide + tid * e + i];
-        t.sq += rq[k * wide + tid * e + i];
+    for (int u = t - r * W; u < units; u += W) {
+      constexpr int B = 8;
+      for (int k = r; k < g.nchunk; k += B * rows) {
+        Part q[B];
+#pragma unroll
+        for (int j = 0; j < B; j++)
+          if (k + j * rows < g.nchunk) q[j] = part[(long long)(k + j * rows) * NU + u];
+#pragma unroll
+        for (int j = 0; j < B; j++)
+          if (k + j * rows < g.nchunk) s.add(q[j], (double)chunk_pixels(g, k + j * rows) * g.UW);
       }
-    const float2 st = finish_stats(t, (double)g.P * g.D, a.eps);
-    sseg[tid] = st;
-    if (a.mean) a.mean[S0 + tid] = st.x;
-    if (a.rstd) a.rstd[S0 + tid] = st.y;
+    }
+  rs[t] = s.s;
+  rq[t] = s.sq;
+  join_rows(rs, rq, W, rows, r, t);
+  // the units of every segment
+  if (ns == 1) {
+    join_rows(rs, rq, 1, W, t, t);
+  } else if (t < ns) {
+    double S = 0, Q = 0;
+    for (int i = 0; i < g.e; i++) {
+      S += rs[t * g.e + i];
+      Q += rq[t * g.e + i];
+    }
+    __builtin_amdgcn_wave_barrier();
+    rs[t * g.e] = S;
+    rq[t * g.e] = Q;
+  }
+  if (t < ns) {
+    Sums w;
+    w.s = rs[t * g.e];
+    w.sq = rq[t * g.e];
+    const float2 st = finish_stats(w, (double)g.P * g.D, a.eps);
+    sseg[t] = st;
+    if (a.mean) a.mean[S0 + t] = st.x;
+    if (a.rstd) a.rstd[S0 + t] = st.y;
   }
   __syncthreads();
   const long long col0 = (long long)S0 * g.D;
-  for (int i = tid; i < ns * g.D; i += 256) {
+  for (int i = t; i < ns * g.D; i += T) {
     const float2 st = sseg[i / g.D];
     const int c = (int)((col0 + i) % g.C);
     a.col.mean[col0 + i] = st.x;
@@ -379,6 +450,7 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const NormArgs a) {
   }
 }
 
+template <bool FULL, int ACT>
 __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
   const NormGeo& g = a.g;
   const int chunk = (int)blockIdx.x / g.ntile, tile = (int)blockIdx.x - chunk * g.ntile;
@@ -387,28 +459,37 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
   if (py >= g.ty || o >= g.TO) return;
   const Oct t = octet(g, o, true);
   const long long stride = (long long)g.N * g.C;
-  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
-  float mean[8], ga[8], be[8];
-  load_run<8>(a.col.mean + t.col, t.cnt, mean);
-  load_run<8>(a.col.a + t.col, t.cnt, ga);
-  load_run<8>(a.beta + t.c0, a.beta ? t.cnt : 0, be);
+  const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;
+  // (the first pixels are requested before the parameters)
+  float next[kBatch][8], mean[8], ga[8], be[8];
+  auto load = [&](int p) {
+#pragma unroll
+    for (int k = 0; k < kBatch; k++) {
+      const int q = p + k * dp;
+      load_run<8, FULL>(a.x + (q < g.P ? q : 0) * stride + t.col, q < g.P ? t.cnt : 0, next[k]);
+    }
+  };
+  load(p0);
+  load_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
+  load_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
+  load_optional<FULL>(a.beta, t.c0, t.cnt, 0.0f, be);
   const DropKey key = drop_key(a.drop);
-  for (int p = p0 + py; p < p1; p += kBatch * g.ty) {
+  for (int p = p0; p < g.P; p += kBatch * dp) {
     float v[kBatch][8];
 #pragma unroll
-    for (int k = 0; k < kBatch; k++) {
-      const int q = p + k * g.ty;
-      load_run<8>(a.x + q * stride + t.col, q < p1 ? t.cnt : 0, v[k]);
-    }
+    for (int k = 0; k < kBatch; k++)
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[k][i] = next[k][i];
+    load(p + kBatch * dp);
 #pragma unroll
     for (int k = 0; k < kBatch; k++) {
-      const int q = p + k * g.ty;
-      if (q >= p1) break;
+      const int q = p + k * dp;
+      if (q >= g.P) break;
       float u[8];
       norm_values<8>(mean, ga, be, v[k], u);
-      act_values<8>(a.act, u);
+      act_values<ACT, 8>(a.act, u);
       drop_values<8>(a.drop, key, (uint32_t)q * g.N + t.n, t.c0, u);
-      store_run<8>(a.out + q * stride + t.col, t.cnt, u);
+      store_run<8, FULL>(a.out + q * stride + t.col, t.cnt, u);
     }
   }
 }
@@ -417,10 +498,11 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
 // backward
 // ---------------------------------------------------------------------------
 // mean and gamma * rstd of an octet from the forward's statistics
+template <bool FULL>
 __device__ __forceinline__ void grad_params(const NormArgs& a, const Oct& t, float (&mean)[8], float (&rstd)[8],
                                             float (&ga)[8], float (&be)[8]) {
   const NormGeo& g = a.g;
-  affine(a, t, ga, be);
+  affine<FULL>(a, t, ga, be);
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const bool ok = i < t.cnt;
@@ -433,13 +515,14 @@ __device__ __forceinline__ void grad_params(const NormArgs& a, const Oct& t, flo
 
 // adds g and g * (x - mean) of one pixel to the octet's sums; d and gr are
 // left holding x - mean and g
+template <int ACT>
 __device__ __forceinline__ void grad_terms(const NormArgs& a, const DropKey& key, const Oct& t, int p,
                                            const float (&mean)[8], const float (&ga)[8], const float (&be)[8],
                                            float (&d)[8], float (&gr)[8]) {
   float u[8];
   norm_values<8>(mean, ga, be, d, u);
   drop_values<8>(a.drop, key, (uint32_t)p * a.g.N + t.n, t.c0, gr);
-  act_slopes<8>(a.act, u, gr);
+  act_slopes<ACT, 8>(a.act, u, gr);
 }
 
 // k1 = rstd * mean_M(gamma g) and k2 = rstd^2 * mean_M(gamma g xh) of a group
@@ -448,7 +531,7 @@ __device__ __forceinline__ float2 grad_means(double s1, double s2, double M, flo
   return make_float2((float)((double)rstd * s1 / M), (float)((double)rstd * rstd * s2 / M));
 }
 
-template <int R>
+template <int R, bool FULL, int ACT>
 __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a) {
   extern __shared__ float2 sh[];
   const NormGeo& g = a.g;
@@ -456,7 +539,7 @@ __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a
   float2* const su = sh;              // [ty1][W], then the columns' sums in its first row
   float2* const sseg = sh + g.ty1 * W;
   const int ox = (int)threadIdx.x % g.so, py = (int)threadIdx.x / g.so;
-  const int o0 = blockIdx.x * g.so;
+  const int o0 = xcd_order((int)blockIdx.x, (int)gridDim.x) * g.so;
   const bool active = py < g.ty1 && o0 + ox < g.TO;
   const Oct t = octet(g, o0 + ox, active);
   const long long stride = (long long)g.N * g.C;
@@ -465,20 +548,21 @@ __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a
 #pragma unroll
   for (int k = 0; k < R; k++) {
     const int cnt = k < rows ? t.cnt : 0;
-    load_run<8>(a.x + (py + k * g.ty1) * stride + t.col, cnt, d[k]);
-    load_run<8>(a.dy + (py + k * g.ty1) * stride + t.col, cnt, gr[k]);
+    const long long at = (k < rows ? py + k * g.ty1 : 0) * stride + t.col;
+    load_run<8, FULL>(a.x + at, cnt, d[k]);
+    load_run<8, FULL>(a.dy + at, cnt, gr[k]);
   }
   float mean[8], rstd[8], ga[8], be[8];
   const DropKey key = drop_key(a.drop);
   if (active) {
-    grad_params(a, t, mean, rstd, ga, be);
+    grad_params<FULL>(a, t, mean, rstd, ga, be);
     float s1[8], s2[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) s1[i] = s2[i] = 0.0f;
 #pragma unroll
     for (int k = 0; k < R; k++)
       if (k < rows) {
-        grad_terms(a, key, t, py + k * g.ty1, mean, ga, be, d[k], gr[k]);
+        grad_terms<ACT>(a, key, t, py + k * g.ty1, mean, ga, be, d[k], gr[k]);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
           s1[i] += gr[k][i];
@@ -542,19 +626,20 @@ __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a
       if (k < rows) {
         float dx[8];
         norm_grad_values<8>(ga, k1, k2, d[k], gr[k], dx);
-        store_run<8>(a.out + (py + k * g.ty1) * stride + t.col, t.cnt, dx);
+        store_run<8, FULL>(a.out + (py + k * g.ty1) * stride + t.col, t.cnt, dx);
       }
   } else if (py == 0) {
-    store_run<8>(a.col.mean + t.col, t.cnt, mean);
-    store_run<8>(a.col.a + t.col, t.cnt, ga);
-    store_run<8>(a.col.k1 + t.col, t.cnt, k1);
-    store_run<8>(a.col.k2 + t.col, t.cnt, k2);
+    store_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
+    store_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
+    store_run<8, FULL>(a.col.k1 + t.col, t.cnt, k1);
+    store_run<8, FULL>(a.col.k2 + t.col, t.cnt, k2);
   }
 }
 
 // dgamma and dbeta behind the one-pass kernel
 __global__ __launch_bounds__(256) void norm_channel_kernel(const NormArgs a) { norm_channel_sums(a, blockIdx.x); }
 
+template <bool FULL, int ACT>
 __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
   __shared__ float2 su[256 * 8];
   const NormGeo& g = a.g;
@@ -564,28 +649,41 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
   const bool active = py < g.ty && o < g.TO;
   const Oct t = octet(g, o, active);
   const long long stride = (long long)g.N * g.C;
-  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
+  const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;
   float s1[8], s2[8];
 #pragma unroll
   for (int i = 0; i < 8; i++) s1[i] = s2[i] = 0.0f;
   if (active) {
-    float mean[8], rstd[8], ga[8], be[8];
-    grad_params(a, t, mean, rstd, ga, be);
-    const DropKey key = drop_key(a.drop);
     constexpr int B = kBatch / 2;  // two tensors
-    for (int p = p0 + py; p < p1; p += B * g.ty) {
+    float nd[B][8], ng[B][8];
+    auto load = [&](int p) {
+#pragma unroll
+      for (int k = 0; k < B; k++) {
+        const int q = p + k * dp, cnt = q < g.P ? t.cnt : 0;
+        const long long at = (q < g.P ? q : 0) * stride + t.col;
+        load_run<8, FULL>(a.x + at, cnt, nd[k]);
+        load_run<8, FULL>(a.dy + at, cnt, ng[k]);
+      }
+    };
+    load(p0);
+    float mean[8], rstd[8], ga[8], be[8];
+    grad_params<FULL>(a, t, mean, rstd, ga, be);
+    const DropKey key = drop_key(a.drop);
+    for (int p = p0; p < g.P; p += B * dp) {
       float d[B][8], gr[B][8];
 #pragma unroll
-      for (int k = 0; k < B; k++) {
-        const int q = p + k * g.ty, cnt = q < p1 ? t.cnt : 0;
-        load_run<8>(a.x + q * stride + t.col, cnt, d[k]);
-        load_run<8>(a.dy + q * stride + t.col, cnt, gr[k]);
-      }
+      for (int k = 0; k < B; k++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          d[k][i] = nd[k][i];
+          gr[k][i] = ng[k][i];
+        }
+      load(p + B * dp);
 #pragma unroll
       for (int k = 0; k < B; k++) {
-        const int q = p + k * g.ty;
-        if (q >= p1) break;
-        grad_terms(a, key, t, q, mean, ga, be, d[k], gr[k]);
+        const int q = p + k * dp;
+        if (q >= g.P) break;
+        grad_terms<ACT>(a, key, t, q, mean, ga, be, d[k], gr[k]);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
           s1[i] += gr[k][i];
@@ -616,61 +714,11 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
   }
 }
 
-// Joins the chunks' sums of every column, and the columns of every (sample,
-// group), whose two means are spread over its columns.
-__global__ __launch_bounds__(256) void norm_join_backward_kernel(const NormArgs a) {
-  __shared__ double r1[256], r2[256];
-  __shared__ float2 sseg[16];
+// Two means of a group from its columns' sums, spread over its columns.
+__device__ __forceinline__ void spread_grad(const NormArgs& a, const float2* sseg, int S0, int ns, int t, int T) {
   const NormGeo& g = a.g;
-  const int NS = g.N * g.G, spw = join_segs(g.D);
-  const int S0 = (int)blockIdx.x * spw, ns = min(spw, NS - S0);
-  const int W = ns * g.D;
-  const long long NC = (long long)g.N * g.C, col0 = (long long)S0 * g.D;
-  const float2* part = a.psum + col0;
-  const int tid = (int)threadIdx.x;
-  const int wide = W < 256 ? W : 256, rows = 256 / wide;
-  const int r = tid / wide, u0 = tid - r * wide;
-  // per pass of `wide` columns: sums over the chunks, joined over the rows of
-  // threads, scaled by gamma and gathered per segment
-  double g1 = 0, g2 = 0;  // this thread's share of its segment (r == 0)
-  for (int u = u0; u - u0 < W; u += wide) {
-    double s1 = 0, s2 = 0;
-    if (r < rows && u < W)
-      for (int k = r; k < g.nchunk; k += rows) {
-        const float2 w = part[k * NC + u];
-        s1 += w.x;
-        s2 += w.y;
-      }
-    r1[tid] = s1;
-    r2[tid] = s2;
-    __syncthreads();
-    if (r == 0 && u < W) {
-      for (int k = 1; k < rows; k++) {
-        s1 += r1[k * wide + tid];
-        s2 += r2[k * wide + tid];
-      }
-      a.tot[col0 + u] = make_float2((float)s1, (float)s2);
-      const int c = (int)((col0 + u) % g.C);
-      const double gm = a.gamma ? (double)a.gamma[c] : 1.0;
-      g1 += gm * s1;
-      g2 += gm * s2;
-    }
-    __syncthreads();
-  }
-  r1[tid] = g1;
-  r2[tid] = g2;
-  __syncthreads();
-  if (tid < ns) {
-    double s1 = 0, s2 = 0;
-    const int e = min(g.D, wide);
-    for (int i = 0; i < e; i++) {
-      s1 += r1[tid * e + i];
-      s2 += r2[tid * e + i];
-    }
-    sseg[tid] = grad_means(s1, s2, (double)g.P * g.D, a.rstd_in[S0 + tid]);
-  }
-  __syncthreads();
-  for (int i = tid; i < W; i += 256) {
+  const long long col0 = (long long)S0 * g.D;
+  for (int i = t; i < ns * g.D; i += T) {
     const int s = i / g.D, c = (int)((col0 + i) % g.C);
     a.col.mean[col0 + i] = a.mean_in[S0 + s];
     a.col.a[col0 + i] = a.rstd_in[S0 + s] * (a.gamma ? a.gamma[c] : 1.0f);
@@ -679,43 +727,139 @@ __global__ __launch_bounds__(256) void norm_join_backward_kernel(const NormArgs 
   }
 }
 
-__global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs a) {
+// Joins the chunks' sums of `cols` neighbouring columns; with whole groups of
+// them (GROUPS), also the groups' means. The columns' sums end in fp32 for
+// every plan, so fp32 and MX results see the same.
+template <bool GROUPS>
+__global__ __launch_bounds__(kJoinT) void norm_join_backward_kernel(const NormArgs a, int cols) {
+  __shared__ double r1[kJoinT], r2[kJoinT];
+  __shared__ float2 sseg[kJoinT];
   const NormGeo& g = a.g;
-  if ((int)blockIdx.x >= g.ntile * g.nchunk) {
-    norm_channel_sums(a, (int)blockIdx.x - g.ntile * g.nchunk);
+  const long long NC = (long long)g.N * g.C, col0 = (long long)blockIdx.x * cols;
+  const int W = (int)min((long long)cols, NC - col0), rows = kJoinT / W;
+  const float2* part = a.psum + col0;
+  const int t = (int)threadIdx.x, r = t / W, u = t - r * W;
+  double s1 = 0, s2 = 0;
+  if (r < rows) {
+    constexpr int B = 8;
+    for (int k = r; k < g.nchunk; k += B * rows) {
+      float2 w[B];
+#pragma unroll
+      for (int j = 0; j < B; j++)
+        w[j] = k + j * rows < g.nchunk ? part[(k + j * rows) * NC + u] : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < B; j++) {
+        s1 += w[j].x;
+        s2 += w[j].y;
+      }
+    }
+  }
+  r1[t] = s1;
+  r2[t] = s2;
+  join_rows(r1, r2, W, rows, r, t);
+  if (t < W) {
+    const float2 w = make_float2((float)r1[t], (float)r2[t]);
+    a.tot[col0 + t] = w;
+    if constexpr (GROUPS) {
+      const double gm = a.gamma ? (double)a.gamma[(col0 + t) % g.C] : 1.0;
+      r1[t] = gm * w.x;
+      r2[t] = gm * w.y;
+    }
+  }
+  if constexpr (GROUPS) {
+    // the columns of every group: column i of a group into its first one
+    const int S0 = (int)(col0 / g.D), ns = W / g.D, i = t % g.D;
+    int have = g.D, h = 1;
+    while (h < have) h <<= 1;
+    for (h >>= 1; h > 0; h >>= 1) {
+      __syncthreads();
+      if (t < W && i < h && i + h < have) {
+        r1[t] += r1[t + h];
+        r2[t] += r2[t + h];
+      }
+      have = min(have, h);
+    }
+    __syncthreads();
+    if (t < ns) sseg[t] = grad_means(r1[t * g.D], r2[t * g.D], (double)g.P * g.D, a.rstd_in[S0 + t]);
+    __syncthreads();
+    spread_grad(a, sseg, S0, ns, t, kJoinT);
+  }
+}
+
+// The two means of a group of many columns, from the columns' sums.
+__global__ __launch_bounds__(kJoinT) void norm_fold_backward_kernel(const NormArgs a) {
+  __shared__ double r1[kJoinT], r2[kJoinT];
+  __shared__ float2 sseg[1];
+  const NormGeo& g = a.g;
+  const int S = (int)blockIdx.x, t = (int)threadIdx.x;
+  const int c0 = S % g.G * g.D;
+  double s1 = 0, s2 = 0;
+  for (int i = t; i < g.D; i += kJoinT) {
+    const float2 w = a.tot[(long long)S * g.D + i];
+    const double gm = a.gamma ? (double)a.gamma[c0 + i] : 1.0;
+    s1 += gm * w.x;
+    s2 += gm * w.y;
+  }
+  r1[t] = s1;
+  r2[t] = s2;
+  join_rows(r1, r2, 1, kJoinT, t, t);
+  if (t == 0) sseg[0] = grad_means(r1[0], r2[0], (double)g.P * g.D, a.rstd_in[S]);
+  __syncthreads();
+  spread_grad(a, sseg, S, 1, t, kJoinT);
+}
+
+template <bool FULL, int ACT>
+__global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs a, int extra) {
+  const NormGeo& g = a.g;
+  if ((int)blockIdx.x < extra) {
+    norm_channel_sums(a, (int)blockIdx.x);
     return;
   }
-  const int chunk = (int)blockIdx.x / g.ntile, tile = (int)blockIdx.x - chunk * g.ntile;
+  const int id = (int)blockIdx.x - extra;
+  const int chunk = id / g.ntile, tile = id - chunk * g.ntile;
   const int ox = (int)threadIdx.x % g.tx, py = (int)threadIdx.x / g.tx;
   const int o = tile * g.tx + ox;
   if (py >= g.ty || o >= g.TO) return;
   const Oct t = octet(g, o, true);
   const long long stride = (long long)g.N * g.C;
-  const int p0 = chunk * g.ppc, p1 = min(g.P, p0 + g.ppc);
-  float mean[8], ga[8], be[8], k1[8], k2[8];
-  load_run<8>(a.col.mean + t.col, t.cnt, mean);
-  load_run<8>(a.col.a + t.col, t.cnt, ga);
-  load_run<8>(a.col.k1 + t.col, t.cnt, k1);
-  load_run<8>(a.col.k2 + t.col, t.cnt, k2);
-  load_run<8>(a.beta + t.c0, a.beta ? t.cnt : 0, be);
-  const DropKey key = drop_key(a.drop);
+  const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;
   constexpr int B = kBatch / 2;
-  for (int p = p0 + py; p < p1; p += B * g.ty) {
+  float nd[B][8], ng[B][8];
+  auto load = [&](int p) {
+#pragma unroll
+    for (int k = 0; k < B; k++) {
+      const int q = p + k * dp, cnt = q < g.P ? t.cnt : 0;
+      const long long at = (q < g.P ? q : 0) * stride + t.col;
+      load_run<8, FULL>(a.x + at, cnt, nd[k]);
+      load_run<8, FULL>(a.dy + at, cnt, ng[k]);
+    }
+  };
+  load(p0);
+  float mean[8], ga[8], be[8], k1[8], k2[8];
+  load_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
+  load_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
+  load_run<8, FULL>(a.col.k1 + t.col, t.cnt, k1);
+  load_run<8, FULL>(a.col.k2 + t.col, t.cnt, k2);
+  load_optional<FULL>(a.beta, t.c0, t.cnt, 0.0f, be);
+  const DropKey key = drop_key(a.drop);
+  for (int p = p0; p < g.P; p += B * dp) {
     float d[B][8], gr[B][8];
 #pragma unroll
-    for (int k = 0; k < B; k++) {
-      const int q = p + k * g.ty, cnt = q < p1 ? t.cnt : 0;
-      load_run<8>(a.x + q * stride + t.col, cnt, d[k]);
-      load_run<8>(a.dy + q * stride + t.col, cnt, gr[k]);
-    }
+    for (int k = 0; k < B; k++)
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        d[k][i] = nd[k][i];
+        gr[k][i] = ng[k][i];
+      }
+    load(p + B * dp);
 #pragma unroll
     for (int k = 0; k < B; k++) {
-      const int q = p + k * g.ty;
-      if (q >= p1) break;
-      grad_terms(a, key, t, q, mean, ga, be, d[k], gr[k]);
+      const int q = p + k * dp;
+      if (q >= g.P) break;
+      grad_terms<ACT>(a, key, t, q, mean, ga, be, d[k], gr[k]);
       float dx[8];
       norm_grad_values<8>(ga, k1, k2, d[k], gr[k], dx);
-      store_run<8>(a.out + q * stride + t.col, t.cnt, dx);
+      store_run<8, FULL>(a.out + q * stride + t.col, t.cnt, dx);
     }
   }
 }
@@ -753,16 +897,95 @@ void bind_ws(NormArgs& a, void* ws, bool backward) {
   }
 }
 
-template <int UW>
-void launch_one(const NormArgs& a, hipStream_t st) {
+// f(activation as a compile-time constant)
+template <bool FULL, class F>
+void with_act(int act, F&& f) {
+  if constexpr (FULL) {
+    switch (act) {
+      case kActNone: f(std::integral_constant<int, kActNone>{}); break;
+      case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+      case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+      default: f(std::integral_constant<int, kActGelu>{}); break;
+    }
+  } else {
+    f(std::integral_constant<int, kActAny>{});
+  }
+}
+
+template <int UW, bool FULL>
+void launch_stats(const NormArgs& a, hipStream_t st) {
   const NormGeo& g = a.g;
+  if (!g.one) {
+    hipLaunchKernelGGL((norm_stats_kernel<UW, FULL>), dim3((unsigned)(g.ntile * g.nchunk)), dim3(256), 0, st, a);
+    return;
+  }
   const int R = ceil_div(g.P, g.ty1);
   const size_t lds = (size_t)(g.ty1 * g.so * (8 / UW)) * sizeof(Part) + (size_t)g.nseg * sizeof(float2);
-  const dim3 grid((unsigned)g.nslab), wg((unsigned)g.T1);
-  if (R <= 1) hipLaunchKernelGGL((norm_one_kernel<1, UW>), grid, wg, lds, st, a);
-  else if (R <= 2) hipLaunchKernelGGL((norm_one_kernel<2, UW>), grid, wg, lds, st, a);
-  else if (R <= 4) hipLaunchKernelGGL((norm_one_kernel<4, UW>), grid, wg, lds, st, a);
-  else hipLaunchKernelGGL((norm_one_kernel<kOneR, UW>), grid, wg, lds, st, a);
+  with_act<FULL>(a.act, [&](auto act) {
+    constexpr int A = decltype(act)::value;
+    const auto kern = R <= 1   ? norm_one_kernel<1, UW, FULL, A>
+                      : R <= 2 ? norm_one_kernel<2, UW, FULL, A>
+                      : R <= 4 ? norm_one_kernel<4, UW, FULL, A>
+                               : norm_one_kernel<kOneR, UW, FULL, A>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)g.nslab), dim3((unsigned)g.T1), lds, st, a);
+  });
+}
+template <bool FULL>
+void launch_stats(const NormArgs& a, hipStream_t st) {
+  switch (a.g.UW) {
+    case 1: launch_stats<1, FULL>(a, st); break;
+    case 2: launch_stats<2, FULL>(a, st); break;
+    case 4: launch_stats<4, FULL>(a, st); break;
+    default: launch_stats<8, FULL>(a, st); break;
+  }
+}
+
+// Joins the streaming statistics.
+void launch_join(const NormArgs& a, hipStream_t st) {
+  const NormGeo& g = a.g;
+  const int NS = g.N * g.G;
+  // groups of few units share a workgroup; one of many takes a larger one
+  const int spw = g.e >= 4 ? 1 : 4 / g.e;
+  const dim3 grid((unsigned)ceil_div(NS, spw));
+  if ((long long)g.e * g.nchunk > 8192) hipLaunchKernelGGL(norm_join_kernel<1024>, grid, dim3(1024), 0, st, a, spw);
+  else hipLaunchKernelGGL(norm_join_kernel<kJoinT>, grid, dim3(kJoinT), 0, st, a, spw);
+}
+
+template <bool FULL>
+void launch_sums(const NormArgs& a, hipStream_t st) {
+  const NormGeo& g = a.g;
+  if (!g.one) {
+    with_act<FULL>(a.act, [&](auto act) {
+      hipLaunchKernelGGL((norm_sums_kernel<FULL, decltype(act)::value>), dim3((unsigned)(g.ntile * g.nchunk)),
+                         dim3(256), 0, st, a);
+    });
+    return;
+  }
+  const int R = ceil_div(g.P, g.ty1);
+  const size_t lds = ((size_t)g.ty1 * g.so * 8 + g.nseg) * sizeof(float2);
+  with_act<FULL>(a.act, [&](auto act) {
+    constexpr int A = decltype(act)::value;
+    const auto kern = R <= 1   ? norm_one_backward_kernel<1, FULL, A>
+                      : R <= 2 ? norm_one_backward_kernel<2, FULL, A>
+                      : R <= 4 ? norm_one_backward_kernel<4, FULL, A>
+                               : norm_one_backward_kernel<kOneR, FULL, A>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)g.nslab), dim3((unsigned)g.T1), lds, st, a);
+  });
+}
+
+template <bool FULL>
+void launch_apply(const NormArgs& a, hipStream_t st) {
+  with_act<FULL>(a.act, [&](auto act) {
+    hipLaunchKernelGGL((norm_apply_kernel<FULL, decltype(act)::value>), dim3((unsigned)(a.g.ntile * a.g.nchunk)),
+                       dim3(256), 0, st, a);
+  });
+}
+template <bool FULL>
+void launch_apply_backward(const NormArgs& a, int extra, hipStream_t st) {
+  with_act<FULL>(a.act, [&](auto act) {
+    hipLaunchKernelGGL((norm_apply_backward_kernel<FULL, decltype(act)::value>),
+                       dim3((unsigned)(a.g.ntile * a.g.nchunk + extra)), dim3(256), 0, st, a, extra);
+  });
 }
 
 }  // namespace
@@ -778,32 +1001,18 @@ hipError_t launch_group_norm(const NormShape& s, const float* x, const float* ga
   a.act = s.act; a.eps = s.eps; a.drop = drop_args(drop);
   bind_ws(a, ws, false);
   const NormGeo& g = a.g;
-  hipError_t e;
-  if (g.one) {
-    switch (g.UW) {
-      case 1: launch_one<1>(a, st); break;
-      case 2: launch_one<2>(a, st); break;
-      case 4: launch_one<4>(a, st); break;
-      default: launch_one<8>(a, st); break;
-    }
-    e = launch_check();
-    if (e != hipSuccess || y) return e;
-  } else {
-    const dim3 grid((unsigned)(g.ntile * g.nchunk));
-    switch (g.UW) {
-      case 1: hipLaunchKernelGGL(norm_stats_kernel<1>, grid, dim3(256), 0, st, a); break;
-      case 2: hipLaunchKernelGGL(norm_stats_kernel<2>, grid, dim3(256), 0, st, a); break;
-      case 4: hipLaunchKernelGGL(norm_stats_kernel<4>, grid, dim3(256), 0, st, a); break;
-      default: hipLaunchKernelGGL(norm_stats_kernel<8>, grid, dim3(256), 0, st, a); break;
-    }
-    e = launch_check();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)ceil_div((long long)g.N * g.G, join_segs(g.e))), dim3(256), 0,
-                       st, a);
+  const bool full = g.C % 8 == 0;
+  if (full) launch_stats<true>(a, st);
+  else launch_stats<false>(a, st);
+  hipError_t e = launch_check();
+  if (e != hipSuccess || (g.one && y)) return e;
+  if (!g.one) {
+    launch_join(a, st);
     e = launch_check();
     if (e != hipSuccess) return e;
     if (y) {
-      hipLaunchKernelGGL(norm_apply_kernel, grid, dim3(256), 0, st, a);
+      if (full) launch_apply<true>(a, st);
+      else launch_apply<false>(a, st);
       return launch_check();
     }
   }
@@ -821,36 +1030,38 @@ hipError_t launch_group_norm_backward(const NormShape& s, const float* dy, const
   a.act = s.act; a.eps = s.eps; a.drop = drop_args(drop);
   bind_ws(a, ws, true);
   const NormGeo& g = a.g;
-  const int extra = dgamma || dbeta ? ceil_div(g.C, 256) : 0;
-  hipError_t e;
-  if (g.one) {
-    const int R = ceil_div(g.P, g.ty1);
-    const size_t lds = ((size_t)g.ty1 * g.so * 8 + g.nseg) * sizeof(float2);
-    const dim3 grid((unsigned)g.nslab), wg((unsigned)g.T1);
-    if (R <= 1) hipLaunchKernelGGL(norm_one_backward_kernel<1>, grid, wg, lds, st, a);
-    else if (R <= 2) hipLaunchKernelGGL(norm_one_backward_kernel<2>, grid, wg, lds, st, a);
-    else if (R <= 4) hipLaunchKernelGGL(norm_one_backward_kernel<4>, grid, wg, lds, st, a);
-    else hipLaunchKernelGGL(norm_one_backward_kernel<kOneR>, grid, wg, lds, st, a);
-    e = launch_check();
+  const bool full = g.C % 8 == 0;
+  const int extra = dgamma || dbeta ? ceil_div(g.C, kSumC) : 0;
+  if (full) launch_sums<true>(a, st);
+  else launch_sums<false>(a, st);
+  hipError_t e = launch_check();
+  if (e != hipSuccess) return e;
+  if (!g.one) {
+    // groups of up to 64 columns are joined whole, larger ones in two steps
+    const long long NC = (long long)g.N * g.C;
+    if (g.D <= 64) {
+      const int cols = g.D >= 8 ? g.D : 8 / g.D * g.D;
+      hipLaunchKernelGGL(norm_join_backward_kernel<true>, dim3((unsigned)ceil_div(NC, cols)), dim3(kJoinT), 0, st, a,
+                         cols);
+      e = launch_check();
+    } else {
+      hipLaunchKernelGGL(norm_join_backward_kernel<false>, dim3((unsigned)ceil_div(NC, 16)), dim3(kJoinT), 0, st, a,
+                         16);
+      e = launch_check();
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(norm_fold_backward_kernel, dim3((unsigned)(g.N * g.G)), dim3(kJoinT), 0, st, a);
+      e = launch_check();
+    }
     if (e != hipSuccess) return e;
     if (dx) {
-      if (!extra) return e;
-      hipLaunchKernelGGL(norm_channel_kernel, dim3((unsigned)extra), dim3(256), 0, st, a);
+      if (full) launch_apply_backward<true>(a, extra, st);
+      else launch_apply_backward<false>(a, extra, st);
       return launch_check();
     }
-  } else {
-    const dim3 grid((unsigned)(g.ntile * g.nchunk));
-    hipLaunchKernelGGL(norm_sums_kernel, grid, dim3(256), 0, st, a);
-    e = launch_check();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(norm_join_backward_kernel, dim3((unsigned)ceil_div((long long)g.N * g.G, join_segs(g.D))),
-                       dim3(256), 0, st, a);
-    e = launch_check();
-    if (e != hipSuccess) return e;
-    if (dx) {
-      hipLaunchKernelGGL(norm_apply_backward_kernel, dim3(grid.x + (unsigned)extra), dim3(256), 0, st, a);
-      return launch_check();
-    }
+  } else if (dx) {
+    if (!extra) return e;
+    hipLaunchKernelGGL(norm_channel_kernel, dim3((unsigned)extra), dim3(256), 0, st, a);
+    return launch_check();
   }
   return launch_norm_backward_mx(a, dxq, extra, st);
 }

@@ -6,6 +6,7 @@
 
 namespace mq {
 
+template <bool FULL, int ACT>
 struct NormSrc {
   NormArgs a;
   struct State {
@@ -15,31 +16,33 @@ struct NormSrc {
   struct Raw {
     float x[16];
   };
-  __device__ void init(State& s, int n, int c0, int cnt) const {
+  __device__ void rows(State&, int, int) const {}
+  __device__ void params(State& s, int n, int c0, int cnt) const {
     const long long col = (long long)n * a.g.C + c0;
-    load_run<16>(a.col.mean + col, cnt, s.mean);
-    load_run<16>(a.col.a + col, cnt, s.a);
-    load_run<16>(a.beta + c0, a.beta ? cnt : 0, s.be);
+    load_run<16, FULL>(a.col.mean + col, cnt, s.mean);
+    load_run<16, FULL>(a.col.a + col, cnt, s.a);
+    if (a.beta) load_run<16, FULL>(a.beta + c0, cnt, s.be);
+    else {
+#pragma unroll
+      for (int i = 0; i < 16; i++) s.be[i] = 0.0f;
+    }
     s.key = drop_key(a.drop);
   }
   __device__ void load(const State&, Raw& r, int p, int n, int c0, int cnt) const {
-    load_run<16>(a.x + ((long long)p * a.g.N + n) * a.g.C + c0, cnt, r.x);
+    load_run<16, FULL>(a.x + ((long long)p * a.g.N + n) * a.g.C + c0, cnt, r.x);
   }
   __device__ void values(const State& s, const Raw& r, int p, int n, int c0, float (&v)[16]) const {
     float d[16];
 #pragma unroll
     for (int i = 0; i < 16; i++) d[i] = r.x[i];
     norm_values<16>(s.mean, s.a, s.be, d, v);
-    act_values<16>(a.act, v);
+    act_values<ACT, 16>(a.act, v);
     drop_values<16>(a.drop, s.key, (uint32_t)p * a.g.N + n, c0, v);
   }
   __device__ void extra(int) const {}
 };
 
-hipError_t launch_norm_mx(const NormArgs& a, const MxOutView& out, hipStream_t st) {
-  return launch_mx_rows(out.fmt, NormSrc{a}, mx_rows(out, a.g.P, a.g.N, a.g.C), 0, st);
-}
-
+template <bool FULL, int ACT>
 struct NormGradSrc {
   NormArgs a;
   struct State {
@@ -49,19 +52,24 @@ struct NormGradSrc {
   struct Raw {
     float x[16], dy[16];
   };
-  __device__ void init(State& s, int n, int c0, int cnt) const {
+  __device__ void rows(State&, int, int) const {}
+  __device__ void params(State& s, int n, int c0, int cnt) const {
     const long long col = (long long)n * a.g.C + c0;
-    load_run<16>(a.col.mean + col, cnt, s.mean);
-    load_run<16>(a.col.a + col, cnt, s.a);
-    load_run<16>(a.col.k1 + col, cnt, s.k1);
-    load_run<16>(a.col.k2 + col, cnt, s.k2);
-    load_run<16>(a.beta + c0, a.beta ? cnt : 0, s.be);
+    load_run<16, FULL>(a.col.mean + col, cnt, s.mean);
+    load_run<16, FULL>(a.col.a + col, cnt, s.a);
+    load_run<16, FULL>(a.col.k1 + col, cnt, s.k1);
+    load_run<16, FULL>(a.col.k2 + col, cnt, s.k2);
+    if (a.beta) load_run<16, FULL>(a.beta + c0, cnt, s.be);
+    else {
+#pragma unroll
+      for (int i = 0; i < 16; i++) s.be[i] = 0.0f;
+    }
     s.key = drop_key(a.drop);
   }
   __device__ void load(const State&, Raw& r, int p, int n, int c0, int cnt) const {
     const long long at = ((long long)p * a.g.N + n) * a.g.C + c0;
-    load_run<16>(a.x + at, cnt, r.x);
-    load_run<16>(a.dy + at, cnt, r.dy);
+    load_run<16, FULL>(a.x + at, cnt, r.x);
+    load_run<16, FULL>(a.dy + at, cnt, r.dy);
   }
   __device__ void values(const State& s, const Raw& r, int p, int n, int c0, float (&v)[16]) const {
     float d[16], u[16], g[16];
@@ -72,14 +80,31 @@ struct NormGradSrc {
     }
     norm_values<16>(s.mean, s.a, s.be, d, u);
     drop_values<16>(a.drop, s.key, (uint32_t)p * a.g.N + n, c0, g);
-    act_slopes<16>(a.act, u, g);
+    act_slopes<ACT, 16>(a.act, u, g);
     norm_grad_values<16>(s.a, s.k1, s.k2, d, g, v);
   }
   __device__ void extra(int b) const { norm_channel_sums(a, b); }
 };
 
+namespace {
+template <template <bool, int> class Src>
+hipError_t launch(const NormArgs& a, const MxOutView& out, int extra, hipStream_t st) {
+  const MxRows g = mx_rows(out, a.g.P, a.g.N, a.g.C);
+  if (a.g.C % 16 != 0) return launch_mx_rows(out.fmt, Src<false, kActAny>{a}, g, extra, st);
+  switch (a.act) {
+    case kActNone: return launch_mx_rows(out.fmt, Src<true, kActNone>{a}, g, extra, st);
+    case kActRelu: return launch_mx_rows(out.fmt, Src<true, kActRelu>{a}, g, extra, st);
+    case kActSilu: return launch_mx_rows(out.fmt, Src<true, kActSilu>{a}, g, extra, st);
+    default: return launch_mx_rows(out.fmt, Src<true, kActGelu>{a}, g, extra, st);
+  }
+}
+}  // namespace
+
+hipError_t launch_norm_mx(const NormArgs& a, const MxOutView& out, hipStream_t st) {
+  return launch<NormSrc>(a, out, 0, st);
+}
 hipError_t launch_norm_backward_mx(const NormArgs& a, const MxOutView& out, int extra, hipStream_t st) {
-  return launch_mx_rows(out.fmt, NormGradSrc{a}, mx_rows(out, a.g.P, a.g.N, a.g.C), extra, st);
+  return launch<NormGradSrc>(a, out, extra, st);
 }
 
 }  // namespace mq
