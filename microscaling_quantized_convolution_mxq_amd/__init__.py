@@ -136,6 +136,12 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr() if hasattr(t, "data_ptr") else int(t)
 
 
+@functools.lru_cache(maxsize=None)
+def _dtype(name: str):
+    import torch
+    return getattr(torch, name)
+
+
 def _buf(t, nbytes: int, dtype: Optional[str], what: str) -> Optional[int]:
     """Device address of a buffer handed to the library. A torch tensor must
     be contiguous, of the expected dtype (None: any), hold at least `nbytes`
@@ -145,6 +151,11 @@ def _buf(t, nbytes: int, dtype: Optional[str], what: str) -> Optional[int]:
     it)."""
     if t is None or not hasattr(t, "data_ptr"):
         return _ptr(t)
+    try:  # the usual case in few steps
+        if t.is_cuda and (dtype is None or t.dtype is _dtype(dtype)) and t.nbytes >= nbytes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a torch tensor: one by one below
+        pass
     if dtype is not None and str(t.dtype) != "torch." + dtype:
         raise MqConvError(MQ_ERR_SHAPE, what, f"dtype {t.dtype}, expected torch.{dtype}")
     if not t.is_contiguous():
@@ -313,7 +324,7 @@ def _ws(ws):
         return None, 0
     if not hasattr(ws, "data_ptr"):
         raise MqConvError(MQ_ERR_SHAPE, "ws", "a workspace must be a tensor (its size is passed on)")
-    return _buf(ws, 0, None, "ws"), ws.numel() * ws.element_size()
+    return _buf(ws, 0, None, "ws"), getattr(ws, "nbytes", None) or ws.numel() * ws.element_size()
 
 
 def mqconv_forward(shape, xq: MxTensor, wq: MxTensor, y, ws=None, stream=None) -> None:

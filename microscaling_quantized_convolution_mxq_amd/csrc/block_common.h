@@ -59,19 +59,10 @@ __device__ __forceinline__ void store_run(float* p, int cnt, const float (&v)[K]
   }
 }
 
-// exp(-u): 2^t of the rounded product t = -u log2(e), corrected to first
-// order by what the product lost. u is held to [-87, 87], where both the
-// exponential and its reciprocal are normal numbers; a sigmoid is 0 or 1 to
-// fp32 well before that.
-__device__ __forceinline__ float exp_neg(float u) {
-#pragma clang fp contract(off)
-  constexpr float L = -1.4426950408889634f, Ll = (float)(-1.4426950408889634 - (double)L);
-  u = __builtin_amdgcn_fmed3f(u, -87.0f, 87.0f);
-  const float t = u * L;
-  const float r = __builtin_fmaf(u, Ll, __builtin_fmaf(u, L, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, r * 0.69314718f, e);
-}
+// exp(-u) as 2^(-u log2(e)): the rounding of the product is |u| 2^-24 of the
+// result, which a sigmoid s passes on times s (1 - s); a correction for it took
+// as long as the rest. Overflow to infinity makes a sigmoid 0, as it should.
+__device__ __forceinline__ float exp_neg(float u) { return __builtin_amdgcn_exp2f(u * -1.4426950408889634f); }
 __device__ __forceinline__ float sigmoid(float u) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(u)); }
 __device__ __forceinline__ float normal_cdf(float u) {
 #pragma clang fp contract(off)

@@ -231,7 +231,9 @@ hipError_t launch_cache_read(const CacheView& c, const int32_t* slot, int count,
   a.c = c; a.slot = slot; a.x = x; a.N = N; a.n0 = n0; a.count = count;
   a.nCB = ceil_div(c.C, 32);
   a.NQ = ceil_div(c.C, 4);
-  const int rows = 512 * kReadUnroll / a.NQ;
+  // one round of loads for every thread (two rounds: 64 samples' worth of
+  // 4-bit codes a replay batch, 20 x 20 x 128 x 256, 17 instead of 12 us)
+  const int rows = 256 * kReadUnroll / a.NQ;
   a.mb = rows / kReadPix;
   if (a.mb < 1) a.mb = 1;
   if (a.mb > count) a.mb = count;
@@ -256,7 +258,7 @@ hipError_t launch_cache_read(const CacheView& c, const int32_t* slot, int count,
 // whose lines come back with their own format and scale gets its codes back,
 // because the largest code of a line lies in the format's largest binade (or
 // the line's scale byte is 0, and its values' too).
-template <int FI>
+template <int FI, bool FULL>
 struct CacheSrc {
   CacheView c;
   const int32_t* slot;
@@ -282,42 +284,58 @@ struct CacheSrc {
     for (int i = 0; i < NW; i++) r.w[i] = d[i];
     r.S = c.scales[run];
   }
-  __device__ void values(const State& s, const Raw& r, int, int, int c0, float (&v)[16]) const {
-    const float sc = scale_value(r.S);
-    uint32_t w[4];  // four codes each
+  // (no slot: codes 0 with scale byte 0)
+  __device__ void words(const State& s, const Raw& r, uint32_t (&w)[4], uint32_t& S) const {
+    S = s.ok ? r.S : 0u;
+    uint32_t a[sizeof(r.w) / 4];
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.w) / 4); i++) a[i] = s.ok ? r.w[i] : 0u;
     if constexpr (FI <= 1) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) w[i] = r.w[i];
+      for (int i = 0; i < 4; i++) w[i] = a[i];
     } else if constexpr (FI <= 3) {
-      w[0] = r.w[0];
-      w[1] = r.w[0] >> 24 | r.w[1] << 8;
-      w[2] = r.w[1] >> 16 | r.w[2] << 16;
-      w[3] = r.w[2] >> 8;
+      w[0] = a[0];
+      w[1] = a[0] >> 24 | a[1] << 8;
+      w[2] = a[1] >> 16 | a[2] << 16;
+      w[3] = a[2] >> 8;
     } else {
-      w[0] = r.w[0]; w[1] = r.w[0] >> 16;
-      w[2] = r.w[1]; w[3] = r.w[1] >> 16;
+      w[0] = a[0]; w[1] = a[0] >> 16;
+      w[2] = a[1]; w[3] = a[1] >> 16;
     }
+  }
+  __device__ void values(const State& s, const Raw& r, int, int, int c0, float (&v)[16]) const {
+    uint32_t w[4], S;  // four codes each
+    words(s, r, w, S);
+    const float sc = scale_value(S);
+    const int cnt = c.C - c0;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       float q[4];
       values4<FI>(w[i], sc, q);
 #pragma unroll
-      for (int j = 0; j < 4; j++) v[4 * i + j] = s.ok && c0 + 4 * i + j < c.C ? q[j] : 0.0f;
+      for (int j = 0; j < 4; j++) v[4 * i + j] = FULL || 4 * i + j < cnt ? q[j] : 0.0f;
     }
   }
   __device__ void extra(int) const {}
 };
 
-hipError_t launch_cache_read_mx(const CacheView& c, const int32_t* slot, int N, const MxOutView& out, hipStream_t st) {
-  const MxRows g = mx_rows(out, c.P, N, c.C);
+namespace {
+template <bool FULL>
+hipError_t launch_read_mx(const CacheView& c, const int32_t* slot, const MxRows& g, int fmt, hipStream_t st) {
   const int nCB = ceil_div(c.C, 32);
   switch (c.fmt) {
-    case 0: return launch_mx_rows(out.fmt, CacheSrc<0>{c, slot, nCB}, g, 0, st);
-    case 1: return launch_mx_rows(out.fmt, CacheSrc<1>{c, slot, nCB}, g, 0, st);
-    case 2: return launch_mx_rows(out.fmt, CacheSrc<2>{c, slot, nCB}, g, 0, st);
-    case 3: return launch_mx_rows(out.fmt, CacheSrc<3>{c, slot, nCB}, g, 0, st);
-    default: return launch_mx_rows(out.fmt, CacheSrc<4>{c, slot, nCB}, g, 0, st);
+    case 0: return launch_mx_rows(fmt, CacheSrc<0, FULL>{c, slot, nCB}, g, 0, st);
+    case 1: return launch_mx_rows(fmt, CacheSrc<1, FULL>{c, slot, nCB}, g, 0, st);
+    case 2: return launch_mx_rows(fmt, CacheSrc<2, FULL>{c, slot, nCB}, g, 0, st);
+    case 3: return launch_mx_rows(fmt, CacheSrc<3, FULL>{c, slot, nCB}, g, 0, st);
+    default: return launch_mx_rows(fmt, CacheSrc<4, FULL>{c, slot, nCB}, g, 0, st);
   }
+}
+}  // namespace
+
+hipError_t launch_cache_read_mx(const CacheView& c, const int32_t* slot, int N, const MxOutView& out, hipStream_t st) {
+  const MxRows g = mx_rows(out, c.P, N, c.C);
+  return c.C % 16 == 0 ? launch_read_mx<true>(c, slot, g, out.fmt, st) : launch_read_mx<false>(c, slot, g, out.fmt, st);
 }
 
 }  // namespace mq

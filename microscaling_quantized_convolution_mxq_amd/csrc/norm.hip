@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kOneR = 8;         // most pixels a thread of the one-pass kernels holds
 constexpr int kBatch = 4;        // pixels a thread of the streaming kernels has in flight
-constexpr int kStreamGroups = 1024;  // workgroups of the streaming kernels, about
+constexpr int kStreamGroups = 512;  // workgroups of the streaming kernels, about
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
@@ -50,14 +50,19 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
   const bool within = s.C % L == 0;
   const int unit = within ? (int)(L / 8) : g.NO;
   const int tmax = backward || g.UW == 1 ? 512 : 1024;
-  if (unit <= tmax) {
+  // The backward holds two tensors, too few workgroups of them: up to 2^22
+  // values, where a launch less counts (20 x 20 x 16 x 256: 16.7 against 17.4
+  // us streaming; with 128 samples 52 against 58 us with fp32 results, but 66
+  // against 57 us with MX results, whose sums must be the same ones)
+  const bool small = !backward || (long long)s.P * s.N * s.C <= 1 << 22;
+  if (unit <= tmax && small) {
     // at least a cache line's 32 channels, and enough octets that a
     // workgroup of few pixels has 256 threads
     long long so = unit * (long long)ceil_div(4, unit);
     so = std::max(so, unit * (long long)ceil_div(256, (long long)std::min(s.P, 256) * unit));
     so = std::min(so, (long long)tmax / unit * unit);
     so = std::min(so, (long long)ceil_div(g.TO, unit) * unit);
-    for (int t = 256; t <= tmax && !g.one; t *= 2) {
+    for (int t = backward ? 256 : 512; t <= tmax && !g.one; t *= 2) {
       if (so > t) continue;
       const int ty = std::min(s.P, t / (int)so);
       // (1,024 threads have 128 registers each, room for half as many pixels)
@@ -85,10 +90,10 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
       g.ntile = nt; g.tx = tx; g.ty = std::min(ty, s.P);
     }
   }
-  // up to 1,024 workgroups (four per compute unit) of at least four pixels a
-  // thread
+  // up to 512 workgroups (two per compute unit) of at least four pixels a
+  // thread (gradient of 80 x 80 x 16 x 64: 34 us, 38 with 1,024 workgroups)
   g.ngroup = ceil_div(s.P, g.ty);
-  g.nchunk = std::max(1, std::min(kStreamGroups / std::min(kStreamGroups, g.ntile), ceil_div(g.ngroup, kBatch)));
+  g.nchunk = std::max(1, std::min(kStreamGroups / std::min(kStreamGroups, g.ntile), std::max(ceil_div(g.ngroup, kBatch), std::min(g.ngroup, 256 / std::min(256, g.ntile)))));
   return g;
 }
 
@@ -940,12 +945,16 @@ void launch_stats(const NormArgs& a, hipStream_t st) {
   }
 }
 
+// Columns of a joining workgroup: as many as leave each thread one round of
+// eight reads.
+int join_width(const NormGeo& g) { return std::max(8, std::min(kJoinT, kJoinT * 8 / g.nchunk)); }
+
 // Joins the streaming statistics.
 void launch_join(const NormArgs& a, hipStream_t st) {
   const NormGeo& g = a.g;
   const int NS = g.N * g.G;
   // groups of few units share a workgroup; one of many takes a larger one
-  const int spw = g.e >= 4 ? 1 : 4 / g.e;
+  const int spw = std::max(1, join_width(g) / 2 / g.e);
   const dim3 grid((unsigned)ceil_div(NS, spw));
   if ((long long)g.e * g.nchunk > 8192) hipLaunchKernelGGL(norm_join_kernel<1024>, grid, dim3(1024), 0, st, a, spw);
   else hipLaunchKernelGGL(norm_join_kernel<kJoinT>, grid, dim3(kJoinT), 0, st, a, spw);
@@ -1040,7 +1049,7 @@ hipError_t launch_group_norm_backward(const NormShape& s, const float* dy, const
     // groups of up to 64 columns are joined whole, larger ones in two steps
     const long long NC = (long long)g.N * g.C;
     if (g.D <= 64) {
-      const int cols = g.D >= 8 ? g.D : 8 / g.D * g.D;
+      const int cols = std::max(1, join_width(g) / g.D) * g.D;
       hipLaunchKernelGGL(norm_join_backward_kernel<true>, dim3((unsigned)ceil_div(NC, cols)), dim3(kJoinT), 0, st, a,
                          cols);
       e = launch_check();
