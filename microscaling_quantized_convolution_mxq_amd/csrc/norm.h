@@ -11,10 +11,10 @@ DropArgs drop_args(const DropSpec& d);
 // The row of N * C values of a pixel as octets of channels: octet o holds
 // channels 8 (o % NO) .. of sample o / NO (fewer than 8 in a sample's last
 // one). A unit is UW = gcd(D, 8) neighbouring channels, which one group
-// holds; a group is e = D / UW units.
+// holds.
 struct NormGeo {
   int P, N, C, G, D, NO, TO;  // TO = N * NO octets a pixel
-  int UW, e;
+  int UW;
   FastDiv dNO, dD;
   // one workgroup holds a slab of `so` octets of all pixels in registers
   bool one;
@@ -23,13 +23,12 @@ struct NormGeo {
   // chunk k takes groups k, k + nchunk, ... (what runs at one time is then
   // one stretch of memory, whose lines fall on all channels alike)
   int tx, ty, ntile, nchunk, ngroup;
+  // joining the chunks of a group: its units (backward: columns) of all
+  // chunks by `lanes` neighbouring lanes, or (wide) by a workgroup
+  int e, lanes;
+  bool wide;
+  FastDiv de;
 };
-// pixels of row py (of ty) in chunk k
-__device__ __forceinline__ int chunk_rows(const NormGeo& g, int k, int py) {
-  const int n = (g.ngroup - k + g.nchunk - 1) / g.nchunk;
-  const int last = g.ngroup - 1;
-  return n - (last % g.nchunk == k && last * g.ty + py >= g.P ? 1 : 0);
-}
 // pixels of chunk k
 __device__ __forceinline__ int chunk_pixels(const NormGeo& g, int k) {
   const int n = (g.ngroup - k + g.nchunk - 1) / g.nchunk * g.ty;
@@ -55,8 +54,10 @@ struct NormArgs {
   float *mean, *rstd;              // forward's statistics (may be null)
   float* out;                      // y or dx; null: the columns' parameters instead
   NormPart* part;                  // streaming: chunks' statistics [nchunk][N * C / UW]
-  float2* psum;                    // streaming backward: chunks' sums [nchunk][N * C]
-  float2* tot;                     // backward: sums over the pixels [N * C]
+  float2* psum;                    // backward: sums of g and g xh of the chunks [nchunk][N][C]
+  const float2* sum_src;           // dgamma, dbeta: rows of sums [sum_rows][C]
+  int sum_rows;
+  float2* fold;                    // rows of sums [kFoldRows][C]
   NormCols col;
   float *dgamma, *dbeta;
   int act;
@@ -67,41 +68,48 @@ struct NormArgs {
 hipError_t launch_norm_mx(const NormArgs& a, const MxOutView& out, hipStream_t st);
 hipError_t launch_norm_backward_mx(const NormArgs& a, const MxOutView& out, int extra, hipStream_t st);
 
-// dgamma and dbeta of channels kSumC b .. from the sums of every sample, by a
-// workgroup of up to 512 threads: thread t takes channel t % kSumC of samples
-// t / kSumC, ... (one thread a channel would wait for memory once a sample).
-constexpr int kSumC = 32;
-__device__ __forceinline__ void norm_channel_sums(const NormArgs& a, int b) {
-  __shared__ double r1[512], r2[512];
-  const int t = (int)threadIdx.x, rows = (int)blockDim.x / kSumC, r = t / kSumC;
-  const int c = b * kSumC + t % kSumC, C = a.g.C, N = a.g.N;
-  double s1 = 0, s2 = 0;
+// Sums of rows r0 .. r1 - 1 of `rows` [.][C] over channels c0 .. c0 + W - 1 by
+// a workgroup of up to 512 threads: thread t takes channel t % W of rows r0 +
+// t / W, .... Thread t < W gets its channel's sums.
+template <int W>
+__device__ __forceinline__ void sum_rows(const float2* rows, int C, int c0, int r0, int r1, double& s1, double& s2) {
+  __shared__ double x1[512], x2[512];
+  const int t = (int)threadIdx.x, n = (int)blockDim.x / W, r = t / W, c = c0 + t % W;
+  s1 = s2 = 0;
   if (c < C) {
-    int n = r;
-    for (; n + 3 * rows < N; n += 4 * rows) {
-      float2 w[4];
+    constexpr int B = 8;
+    for (int i = r0 + r; i < r1; i += B * n) {
+      float2 w[B];
 #pragma unroll
-      for (int j = 0; j < 4; j++) w[j] = a.tot[(long long)(n + j * rows) * C + c];
+      for (int j = 0; j < B; j++)
+        w[j] = i + j * n < r1 ? rows[(long long)(i + j * n) * C + c] : make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
+      for (int j = 0; j < B; j++) {
         s1 += w[j].x;
         s2 += w[j].y;
       }
     }
-    for (; n < N; n += rows) {
-      const float2 w = a.tot[(long long)n * C + c];
-      s1 += w.x;
-      s2 += w.y;
-    }
   }
-  r1[t] = s1;
-  r2[t] = s2;
+  x1[t] = s1;
+  x2[t] = s2;
   __syncthreads();
-  if (r == 0 && c < C) {
-    for (int k = 1; k < rows; k++) {
-      s1 += r1[k * kSumC + t];
-      s2 += r2[k * kSumC + t];
+  if (t < W)
+    for (int k = 1; k < n; k++) {
+      s1 += x1[k * W + t];
+      s2 += x2[k * W + t];
     }
+}
+
+// dgamma and dbeta of channels kSumC b ..: eight channels a workgroup, so that
+// its threads share the samples' and chunks' rows between them (a thread a
+// channel had been the tail of the whole gradient).
+constexpr int kSumC = 8;
+constexpr int kFoldRows = 64, kFoldFrom = 1024;  // more rows than kFoldFrom are first summed to kFoldRows
+__device__ __forceinline__ void norm_channel_sums(const NormArgs& a, int b) {
+  double s1, s2;
+  sum_rows<kSumC>(a.sum_src, a.g.C, b * kSumC, 0, a.sum_rows, s1, s2);
+  const int c = b * kSumC + (int)threadIdx.x;
+  if (threadIdx.x < kSumC && c < a.g.C) {
     if (a.dbeta) a.dbeta[c] = (float)s1;
     if (a.dgamma) a.dgamma[c] = (float)s2;
   }

@@ -10,8 +10,11 @@
 //     of a workgroup, that workgroup reads it once, joins the statistics in
 //     LDS and writes the result from its registers: one launch, no workspace.
 //   Streaming: partial statistics (a mean and a sum of squares around it) or
-//     sums of chunks of pixels, joined per group by a second kernel in a fixed
-//     order, and an elementwise pass that reads x (and dy) again.
+//     sums of chunks of pixels, and an elementwise pass that reads x (and dy)
+//     again. The fp32 pass joins the chunks of its own columns' groups first,
+//     in a fixed order (narrow tiles have few chunks, so that is one round of
+//     loads); for MX results, whose tiles span 32 samples, and for groups of
+//     very many columns a kernel in between joins them once.
 // Sums of values are fp64 (two operations a value, hidden behind the loads),
 // so a mean is its fp32 rounding, whatever cancels in it; squares are summed
 // in fp32 around means of the values themselves, so a mean far from zero
@@ -41,6 +44,7 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
   g.TO = s.N * g.NO;
   g.UW = backward ? 1 : gcd(g.D, 8);  // the backward sums columns (dgamma, dbeta)
   g.e = g.D / g.UW;
+  g.de = make_fastdiv((unsigned)g.e);
   g.dNO = make_fastdiv((unsigned)g.NO);
   g.dD = make_fastdiv((unsigned)g.D);
 
@@ -76,12 +80,13 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
     }
   }
 
-  // streaming tiles: about 32 octets (1 KB of a pixel's row) wide, since every
-  // chunk of pixels leaves a partial result of each column, so few wide tiles
-  // would mean many partials; of such widths the one that leaves the fewest
-  // of 256 threads idle
+  // streaming tiles: 16 octets (512 bytes of a pixel's row) wide, 8 where a
+  // row has few: the narrower, the fewer chunks there are of a column, which
+  // the elementwise pass joins; below 512 bytes large tensors read more slowly
+  // (160 x 160 x 32 x 128, both passes: 32 octets 246, 16 233, 8 271, 4 303
+  // us); of such widths the one that leaves the fewest of 256 threads idle
   double best = 0;
-  const int n0 = ceil_div(g.TO, 32);
+  const int n0 = ceil_div(g.TO, g.TO >= 256 ? 16 : 8);
   for (int nt = n0; nt < n0 + 4; nt++) {
     const int tx = ceil_div(g.TO, nt), ty = 256 / tx;
     const double use = (double)g.TO / nt * ty / 256;
@@ -94,6 +99,11 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
   // thread (gradient of 80 x 80 x 16 x 64: 34 us, 38 with 1,024 workgroups)
   g.ngroup = ceil_div(s.P, g.ty);
   g.nchunk = std::max(1, std::min(kStreamGroups / std::min(kStreamGroups, g.ntile), std::max(ceil_div(g.ngroup, kBatch), std::min(g.ngroup, 256 / std::min(256, g.ntile)))));
+  // eight loads a lane
+  const long long entries = (long long)g.e * g.nchunk;
+  g.wide = entries > 2048;
+  g.lanes = 1;
+  while (g.lanes < 64 && g.lanes * 8 < entries) g.lanes *= 2;
   return g;
 }
 
@@ -205,6 +215,31 @@ __device__ __forceinline__ float2 finish_stats(const Sums& t, double M, float ep
 __device__ __forceinline__ double group_sum(double v, int lanes) {  // aligned groups of lanes (a power of two)
   for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor(v, o);
   return v;
+}
+
+// Sums of W columns over rows 0 .. n - 1 by 256 threads: get(row, column, s1,
+// s2) adds a row's values, done(column, s1, s2) takes the sums. Thread t adds
+// rows t / W, t / W + 256 / W, ... of column t % W; then a tree.
+template <class Get, class Done>
+__device__ __forceinline__ void reduce_rows(int W, int n, Get get, Done done) {
+  __shared__ double x1[256], x2[256];
+  const int t = (int)threadIdx.x, r = t / W, u = t - r * W, R = 256 / W;
+  double s1 = 0, s2 = 0;
+  if (r < R)
+    for (int row = r; row < n; row += R) get(row, u, s1, s2);
+  x1[t] = s1;
+  x2[t] = s2;
+  int have = min(R, n), h = 1;
+  while (h < have) h <<= 1;
+  for (h >>= 1; h > 0; h >>= 1) {
+    __syncthreads();
+    if (r < h && r + h < have) {
+      x1[t] += x1[t + h * W];
+      x2[t] += x2[t + h * W];
+    }
+    have = min(have, h);
+  }
+  if (t < W) done(u, x1[t], x2[t]);
 }
 
 // lanes that reduce one segment together: a power of two up to 64
@@ -354,106 +389,215 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
   __syncthreads();
   // units of the tile, joined over the rows of pixels
   const int NU = g.N * g.C / UW;
-  for (int i = (int)threadIdx.x; i < W; i += 256) {
-    const int oo = tile * g.tx + i / UN, u = i % UN;
-    if (oo >= g.TO) continue;
-    const Oct q = octet(g, oo, true);
-    if (u * UW >= q.cnt) continue;
-    Sums s;
-    for (int r = 0; r < g.ty; r++) {
-      const int rows = chunk_rows(g, chunk, r);
-      if (rows > 0) s.add(su[r * W + i], (double)rows * UW);
-    }
-    const double c = (double)chunk_pixels(g, chunk) * UW, m = s.s / c;
-    a.part[(long long)chunk * NU + (q.col / UW + u)] = part_of(s.s, c, (float)m, (float)(s.sq - m * s.s));
-  }
+  const double c = (double)chunk_pixels(g, chunk) * UW;
+  // pixels of row r of the chunk: a group less where the last group is short
+  const int groups = (g.ngroup - chunk + g.nchunk - 1) / g.nchunk, last = g.ngroup - 1;
+  const bool owns_last = last % g.nchunk == chunk;
+  reduce_rows(
+      W, g.ty,
+      [&](int r, int i, double& s1, double& s2) {
+        const int rows = groups - (owns_last && last * g.ty + r >= g.P ? 1 : 0);
+        if (rows == 0) return;
+        Sums q;
+        q.add(su[r * W + i], (double)rows * UW);
+        s1 += q.s;
+        s2 += q.sq;
+      },
+      [&](int i, double s1, double s2) {
+        const int oo = tile * g.tx + i / UN, u = i % UN;
+        if (oo >= g.TO) return;
+        const Oct q = octet(g, oo, true);
+        if (u * UW >= q.cnt) return;
+        const double m = s1 / c;
+        a.part[(long long)chunk * NU + (q.col / UW + u)] = part_of(s1, c, (float)m, (float)(s2 - m * s1));
+      });
 }
 
 // ---------------------------------------------------------------------------
 // joining the chunks
 // ---------------------------------------------------------------------------
-// A joining workgroup of T threads takes W neighbouring units or columns
-// (thread t: column t % W of chunks t / W, t / W + T / W, ...). The chunks'
-// partials are few bytes but far apart, so what counts is how many of these
-// reads are under way at once: few columns a workgroup, eight reads a thread.
-constexpr int kJoinT = 256;
+constexpr int kJoinT = 256, kWideT = 1024;
 
-// s[r * W + u] summed over the rows r of threads into row 0 (thread order)
-__device__ __forceinline__ void join_rows(double* a, double* b, int W, int rows, int r, int t) {
-  int h = 1;
-  while (h < rows) h <<= 1;
-  for (h >>= 1; h > 0; h >>= 1) {
-    __syncthreads();
-    if (r < h && r + h < rows) {
-      a[t] += a[t + h * W];
-      b[t] += b[t + h * W];
-    }
-    rows = min(rows, h);
-  }
-  __syncthreads();
-}
-
-// Joins the chunks' statistics of neighbouring groups (spw of them, or one of
-// more than T units) and spreads them over their columns.
-template <int T>
-__global__ __launch_bounds__(T) void norm_join_kernel(const NormArgs a, int spw) {
-  __shared__ double rs[T], rq[T];
-  __shared__ float2 sseg[kJoinT];
+// Statistics of segment (sample, group) S from its units of all chunks: lane
+// j of `lanes` takes every lanes-th. Every caller's lanes sum in the same
+// order.
+__device__ __forceinline__ Sums segment_stats(const NormArgs& a, int S, int j, int lanes) {
   const NormGeo& g = a.g;
-  const int NS = g.N * g.G;
-  const int S0 = (int)blockIdx.x * spw, ns = min(spw, NS - S0);
-  const int units = ns * g.e, W = min(units, T), rows = T / W;
-  const int NU = g.N * g.C / g.UW;
-  const Part* part = a.part + (long long)S0 * g.e;
-  const int t = (int)threadIdx.x, r = t / W;
+  const int n = g.e * g.nchunk;
+  const long long NU = (long long)g.N * g.C / g.UW;
+  const Part* part = a.part + (long long)S * g.e;
+  constexpr int B = 8;
   Sums s;
-  if (r < rows)
-    for (int u = t - r * W; u < units; u += W) {
-      constexpr int B = 8;
-      for (int k = r; k < g.nchunk; k += B * rows) {
-        Part q[B];
+  for (int i = j; i < n; i += B * lanes) {
+    Part q[B];
+    int k[B];
 #pragma unroll
-        for (int j = 0; j < B; j++)
-          if (k + j * rows < g.nchunk) q[j] = part[(long long)(k + j * rows) * NU + u];
+    for (int b = 0; b < B; b++) {
+      const int at = min(i + b * lanes, n - 1);
+      k[b] = (int)fdiv((unsigned)at, g.de);
+      q[b] = part[k[b] * NU + (at - k[b] * g.e)];
+    }
 #pragma unroll
-        for (int j = 0; j < B; j++)
-          if (k + j * rows < g.nchunk) s.add(q[j], (double)chunk_pixels(g, k + j * rows) * g.UW);
+    for (int b = 0; b < B; b++)
+      if (i + b * lanes < n) s.add(q[b], (double)chunk_pixels(g, k[b]) * g.UW);
+  }
+  return s;
+}
+
+// The same for the backward: sums of gamma g and gamma g xh.
+__device__ __forceinline__ void segment_sums(const NormArgs& a, int S, int j, int lanes, double& s1, double& s2) {
+  const NormGeo& g = a.g;
+  const int n = g.D * g.nchunk, c0 = (S - S / g.G * g.G) * g.D;
+  const long long NC = (long long)g.N * g.C;
+  const float2* part = a.psum + (long long)S * g.D;
+  constexpr int B = 8;
+  s1 = s2 = 0;
+  for (int i = j; i < n; i += B * lanes) {
+    float2 w[B];
+    float gm[B];
+#pragma unroll
+    for (int b = 0; b < B; b++) {
+      const int at = min(i + b * lanes, n - 1);
+      const int k = (int)fdiv((unsigned)at, g.dD), u = at - k * g.D;
+      w[b] = part[k * NC + u];
+      gm[b] = a.gamma ? a.gamma[c0 + u] : 1.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < B; b++)
+      if (i + b * lanes < n) {
+        s1 += (double)gm[b] * w[b].x;
+        s2 += (double)gm[b] * w[b].y;
       }
-    }
-  rs[t] = s.s;
-  rq[t] = s.sq;
-  join_rows(rs, rq, W, rows, r, t);
-  // the units of every segment
-  if (ns == 1) {
-    join_rows(rs, rq, 1, W, t, t);
-  } else if (t < ns) {
-    double S = 0, Q = 0;
-    for (int i = 0; i < g.e; i++) {
-      S += rs[t * g.e + i];
-      Q += rq[t * g.e + i];
-    }
-    __builtin_amdgcn_wave_barrier();
-    rs[t * g.e] = S;
-    rq[t * g.e] = Q;
-  }
-  if (t < ns) {
-    Sums w;
-    w.s = rs[t * g.e];
-    w.sq = rq[t * g.e];
-    const float2 st = finish_stats(w, (double)g.P * g.D, a.eps);
-    sseg[t] = st;
-    if (a.mean) a.mean[S0 + t] = st.x;
-    if (a.rstd) a.rstd[S0 + t] = st.y;
-  }
-  __syncthreads();
-  const long long col0 = (long long)S0 * g.D;
-  for (int i = t; i < ns * g.D; i += T) {
-    const float2 st = sseg[i / g.D];
-    const int c = (int)((col0 + i) % g.C);
-    a.col.mean[col0 + i] = st.x;
-    a.col.a[col0 + i] = st.y * (a.gamma ? a.gamma[c] : 1.0f);
   }
 }
+
+// k1 = rstd * mean_M(gamma g) and k2 = rstd^2 * mean_M(gamma g xh) of a group
+// from the sums of gamma g and gamma g xh
+__device__ __forceinline__ float2 grad_means(double s1, double s2, double M, float rstd) {
+  return make_float2((float)((double)rstd * s1 / M), (float)((double)rstd * rstd * s2 / M));
+}
+
+// Segments S0 .. S0 + ns - 1 by a workgroup: (mean, rstd), or (k1, k2), into
+// sseg.
+template <bool BWD>
+__device__ __forceinline__ void join_segments(const NormArgs& a, int S0, int ns, float2* sseg) {
+  const NormGeo& g = a.g;
+  const int L = g.lanes, j = (int)threadIdx.x & (L - 1), step = (int)blockDim.x / L;
+  const double M = (double)g.P * g.D;
+  for (int s = (int)threadIdx.x / L; s < ns; s += step) {
+    if constexpr (BWD) {
+      const float rstd = a.rstd_in[S0 + s];
+      double s1, s2;
+      segment_sums(a, S0 + s, j, L, s1, s2);
+      s1 = group_sum(s1, L);
+      s2 = group_sum(s2, L);
+      if (j == 0) sseg[s] = grad_means(s1, s2, M, rstd);
+    } else {
+      Sums t = segment_stats(a, S0 + s, j, L);
+      t.s = group_sum(t.s, L);
+      t.sq = group_sum(t.sq, L);
+      if (j == 0) sseg[s] = finish_stats(t, M, a.eps);
+    }
+  }
+  __syncthreads();
+}
+
+// What spreading reads for column i of the segments from S0 on.
+struct ColIn {
+  float ga, mean, rstd;
+};
+template <bool BWD>
+__device__ __forceinline__ ColIn column_in(const NormArgs& a, int S0, int ns, int i) {
+  const NormGeo& g = a.g;
+  i = min(i, ns * g.D - 1);
+  const int S = S0 + (int)fdiv((unsigned)i, g.dD), c = i - (S - S0) * g.D + (S - S / g.G * g.G) * g.D;
+  return ColIn{a.gamma ? a.gamma[c] : 1.0f, BWD ? a.mean_in[S] : 0.0f, BWD ? a.rstd_in[S] : 0.0f};
+}
+// The columns' parameters of segments S0 .. S0 + ns - 1; `in` is what the
+// thread's first column reads, requested before the segments were joined.
+template <bool BWD>
+__device__ __forceinline__ void spread_segments(const NormArgs& a, int S0, int ns, const float2* sseg, ColIn in) {
+  const NormGeo& g = a.g;
+  const long long col0 = (long long)S0 * g.D;
+  for (int i = (int)threadIdx.x; i < ns * g.D; i += (int)blockDim.x) {
+    if (i != (int)threadIdx.x) in = column_in<BWD>(a, S0, ns, i);
+    const float2 st = sseg[fdiv((unsigned)i, g.dD)];
+    a.col.mean[col0 + i] = BWD ? in.mean : st.x;
+    a.col.a[col0 + i] = (BWD ? in.rstd : st.y) * in.ga;
+    if constexpr (BWD) {
+      a.col.k1[col0 + i] = st.x;
+      a.col.k2[col0 + i] = st.y;
+    }
+  }
+}
+__device__ __forceinline__ void keep_stats(const NormArgs& a, int S0, int ns, const float2* sseg) {
+  for (int s = (int)threadIdx.x; s < ns; s += (int)blockDim.x) {
+    if (a.mean) a.mean[S0 + s] = sseg[s].x;
+    if (a.rstd) a.rstd[S0 + s] = sseg[s].y;
+  }
+}
+
+// kJoinT / lanes segments a workgroup.
+template <bool BWD>
+__global__ __launch_bounds__(kJoinT) void norm_join_kernel(const NormArgs a) {
+  __shared__ float2 sseg[kJoinT];
+  const int per = kJoinT / a.g.lanes, S0 = (int)blockIdx.x * per, ns = min(per, a.g.N * a.g.G - S0);
+  const ColIn in = column_in<BWD>(a, S0, ns, (int)threadIdx.x);
+  join_segments<BWD>(a, S0, ns, sseg);
+  if constexpr (!BWD) keep_stats(a, S0, ns, sseg);
+  spread_segments<BWD>(a, S0, ns, sseg, in);
+}
+
+// A workgroup for every segment.
+template <bool BWD>
+__global__ __launch_bounds__(kWideT) void norm_join_wide_kernel(const NormArgs a) {
+  __shared__ double r1[kWideT / 64], r2[kWideT / 64];
+  __shared__ float2 sseg[1];
+  const int S = (int)blockIdx.x, t = (int)threadIdx.x;
+  const ColIn in = column_in<BWD>(a, S, 1, t);
+  double s1, s2;
+  if constexpr (BWD) {
+    segment_sums(a, S, t, kWideT, s1, s2);
+  } else {
+    const Sums s = segment_stats(a, S, t, kWideT);
+    s1 = s.s;
+    s2 = s.sq;
+  }
+  s1 = group_sum(s1, 64);
+  s2 = group_sum(s2, 64);
+  if ((t & 63) == 0) {
+    r1[t >> 6] = s1;
+    r2[t >> 6] = s2;
+  }
+  __syncthreads();
+  if (t == 0) {
+    for (int k = 1; k < kWideT / 64; k++) {
+      s1 += r1[k];
+      s2 += r2[k];
+    }
+    const double M = (double)a.g.P * a.g.D;
+    if constexpr (BWD) {
+      sseg[0] = grad_means(s1, s2, M, a.rstd_in[S]);
+    } else {
+      Sums q;
+      q.s = s1;
+      q.sq = s2;
+      sseg[0] = finish_stats(q, M, a.eps);
+    }
+  }
+  __syncthreads();
+  if constexpr (!BWD) keep_stats(a, S, 1, sseg);
+  spread_segments<BWD>(a, S, 1, sseg, in);
+}
+
+// Segments of the columns of a tile: the first one, and how many.
+__device__ __forceinline__ int tile_segments(const NormGeo& g, int tile, int& ns) {
+  const Oct first = octet(g, tile * g.tx, true), last = octet(g, min(g.TO, (tile + 1) * g.tx) - 1, true);
+  const int S0 = first.n * g.G + (int)fdiv((unsigned)first.c0, g.dD);
+  ns = last.n * g.G + (int)fdiv((unsigned)(last.c0 + last.cnt - 1), g.dD) - S0 + 1;
+  return S0;
+}
+constexpr int kTileOcts = 16;  // widest tile, so at most 8 * kTileOcts segments of it
 
 template <bool FULL, int ACT>
 __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
@@ -461,8 +605,8 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
   const int chunk = (int)blockIdx.x / g.ntile, tile = (int)blockIdx.x - chunk * g.ntile;
   const int ox = (int)threadIdx.x % g.tx, py = (int)threadIdx.x / g.tx;
   const int o = tile * g.tx + ox;
-  if (py >= g.ty || o >= g.TO) return;
-  const Oct t = octet(g, o, true);
+  const bool active = py < g.ty && o < g.TO;
+  const Oct t = octet(g, o, active);
   const long long stride = (long long)g.N * g.C;
   const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;
   // (the first pixels are requested before the parameters)
@@ -475,9 +619,26 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
     }
   };
   load(p0);
-  load_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
-  load_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
-  load_optional<FULL>(a.beta, t.c0, t.cnt, 0.0f, be);
+  if (g.wide) {
+    load_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
+    load_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
+    load_optional<FULL>(a.beta, t.c0, t.cnt, 0.0f, be);
+  } else {
+    __shared__ float2 sseg[8 * kTileOcts];
+    int ns;
+    const int S0 = tile_segments(g, tile, ns);
+    affine<FULL>(a, t, ga, be);
+    join_segments<false>(a, S0, ns, sseg);
+    if (chunk == 0) keep_stats(a, S0, ns, sseg);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const bool ok = i < t.cnt;
+      const float2 st = sseg[ok ? t.n * g.G + (int)fdiv((unsigned)(t.c0 + i), g.dD) - S0 : 0];
+      mean[i] = ok ? st.x : 0.0f;
+      ga[i] = ok ? st.y * ga[i] : 0.0f;
+    }
+  }
+  if (!active) return;
   const DropKey key = drop_key(a.drop);
   for (int p = p0; p < g.P; p += kBatch * dp) {
     float v[kBatch][8];
@@ -528,12 +689,6 @@ __device__ __forceinline__ void grad_terms(const NormArgs& a, const DropKey& key
   norm_values<8>(mean, ga, be, d, u);
   drop_values<8>(a.drop, key, (uint32_t)p * a.g.N + t.n, t.c0, gr);
   act_slopes<ACT, 8>(a.act, u, gr);
-}
-
-// k1 = rstd * mean_M(gamma g) and k2 = rstd^2 * mean_M(gamma g xh) of a group
-// from the sums of gamma g and gamma g xh
-__device__ __forceinline__ float2 grad_means(double s1, double s2, double M, float rstd) {
-  return make_float2((float)((double)rstd * s1 / M), (float)((double)rstd * rstd * s2 / M));
 }
 
 template <int R, bool FULL, int ACT>
@@ -591,7 +746,7 @@ __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a
     }
     const float2 tot = make_float2((float)s1, (float)s2);
     su[i] = tot;
-    a.tot[q.col + (i & 7)] = tot;
+    a.psum[q.col + (i & 7)] = tot;
   }
   __syncthreads();
   const int n0 = (int)fdiv((unsigned)o0, g.dNO);
@@ -639,6 +794,17 @@ __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a
     store_run<8, FULL>(a.col.k1 + t.col, t.cnt, k1);
     store_run<8, FULL>(a.col.k2 + t.col, t.cnt, k2);
   }
+}
+
+// Sums of very many rows of sums (samples and chunks) to kFoldRows.
+constexpr int kFoldC = 32;
+__global__ __launch_bounds__(256) void norm_fold_kernel(const NormArgs a) {
+  const int cb = (int)blockIdx.x / kFoldRows, k = (int)blockIdx.x - cb * kFoldRows;
+  const int per = (a.sum_rows + kFoldRows - 1) / kFoldRows, r0 = min(a.sum_rows, k * per);
+  double s1, s2;
+  sum_rows<kFoldC>(a.sum_src, a.g.C, cb * kFoldC, r0, min(a.sum_rows, r0 + per), s1, s2);
+  const int c = cb * kFoldC + (int)threadIdx.x;
+  if (threadIdx.x < kFoldC && c < a.g.C) a.fold[(long long)k * a.g.C + c] = make_float2((float)s1, (float)s2);
 }
 
 // dgamma and dbeta behind the one-pass kernel
@@ -705,112 +871,19 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
     for (int i = 0; i < 8; i++) su[py * W + ox * 8 + i] = make_float2(s1[i], s2[i]);
   __syncthreads();
   const long long NC = stride;
-  for (int i = (int)threadIdx.x; i < W; i += 256) {
-    const int oo = tile * g.tx + (i >> 3);
-    if (oo >= g.TO) continue;
-    const Oct q = octet(g, oo, true);
-    if ((i & 7) >= q.cnt) continue;
-    double a1 = 0, a2 = 0;
-    for (int r = 0; r < g.ty; r++) {
-      a1 += su[r * W + i].x;
-      a2 += su[r * W + i].y;
-    }
-    a.psum[chunk * NC + q.col + (i & 7)] = make_float2((float)a1, (float)a2);
-  }
-}
-
-// Two means of a group from its columns' sums, spread over its columns.
-__device__ __forceinline__ void spread_grad(const NormArgs& a, const float2* sseg, int S0, int ns, int t, int T) {
-  const NormGeo& g = a.g;
-  const long long col0 = (long long)S0 * g.D;
-  for (int i = t; i < ns * g.D; i += T) {
-    const int s = i / g.D, c = (int)((col0 + i) % g.C);
-    a.col.mean[col0 + i] = a.mean_in[S0 + s];
-    a.col.a[col0 + i] = a.rstd_in[S0 + s] * (a.gamma ? a.gamma[c] : 1.0f);
-    a.col.k1[col0 + i] = sseg[s].x;
-    a.col.k2[col0 + i] = sseg[s].y;
-  }
-}
-
-// Joins the chunks' sums of `cols` neighbouring columns; with whole groups of
-// them (GROUPS), also the groups' means. The columns' sums end in fp32 for
-// every plan, so fp32 and MX results see the same.
-template <bool GROUPS>
-__global__ __launch_bounds__(kJoinT) void norm_join_backward_kernel(const NormArgs a, int cols) {
-  __shared__ double r1[kJoinT], r2[kJoinT];
-  __shared__ float2 sseg[kJoinT];
-  const NormGeo& g = a.g;
-  const long long NC = (long long)g.N * g.C, col0 = (long long)blockIdx.x * cols;
-  const int W = (int)min((long long)cols, NC - col0), rows = kJoinT / W;
-  const float2* part = a.psum + col0;
-  const int t = (int)threadIdx.x, r = t / W, u = t - r * W;
-  double s1 = 0, s2 = 0;
-  if (r < rows) {
-    constexpr int B = 8;
-    for (int k = r; k < g.nchunk; k += B * rows) {
-      float2 w[B];
-#pragma unroll
-      for (int j = 0; j < B; j++)
-        w[j] = k + j * rows < g.nchunk ? part[(k + j * rows) * NC + u] : make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int j = 0; j < B; j++) {
-        s1 += w[j].x;
-        s2 += w[j].y;
-      }
-    }
-  }
-  r1[t] = s1;
-  r2[t] = s2;
-  join_rows(r1, r2, W, rows, r, t);
-  if (t < W) {
-    const float2 w = make_float2((float)r1[t], (float)r2[t]);
-    a.tot[col0 + t] = w;
-    if constexpr (GROUPS) {
-      const double gm = a.gamma ? (double)a.gamma[(col0 + t) % g.C] : 1.0;
-      r1[t] = gm * w.x;
-      r2[t] = gm * w.y;
-    }
-  }
-  if constexpr (GROUPS) {
-    // the columns of every group: column i of a group into its first one
-    const int S0 = (int)(col0 / g.D), ns = W / g.D, i = t % g.D;
-    int have = g.D, h = 1;
-    while (h < have) h <<= 1;
-    for (h >>= 1; h > 0; h >>= 1) {
-      __syncthreads();
-      if (t < W && i < h && i + h < have) {
-        r1[t] += r1[t + h];
-        r2[t] += r2[t + h];
-      }
-      have = min(have, h);
-    }
-    __syncthreads();
-    if (t < ns) sseg[t] = grad_means(r1[t * g.D], r2[t * g.D], (double)g.P * g.D, a.rstd_in[S0 + t]);
-    __syncthreads();
-    spread_grad(a, sseg, S0, ns, t, kJoinT);
-  }
-}
-
-// The two means of a group of many columns, from the columns' sums.
-__global__ __launch_bounds__(kJoinT) void norm_fold_backward_kernel(const NormArgs a) {
-  __shared__ double r1[kJoinT], r2[kJoinT];
-  __shared__ float2 sseg[1];
-  const NormGeo& g = a.g;
-  const int S = (int)blockIdx.x, t = (int)threadIdx.x;
-  const int c0 = S % g.G * g.D;
-  double s1 = 0, s2 = 0;
-  for (int i = t; i < g.D; i += kJoinT) {
-    const float2 w = a.tot[(long long)S * g.D + i];
-    const double gm = a.gamma ? (double)a.gamma[c0 + i] : 1.0;
-    s1 += gm * w.x;
-    s2 += gm * w.y;
-  }
-  r1[t] = s1;
-  r2[t] = s2;
-  join_rows(r1, r2, 1, kJoinT, t, t);
-  if (t == 0) sseg[0] = grad_means(r1[0], r2[0], (double)g.P * g.D, a.rstd_in[S]);
-  __syncthreads();
-  spread_grad(a, sseg, S, 1, t, kJoinT);
+  reduce_rows(
+      W, g.ty,
+      [&](int r, int i, double& s1, double& s2) {
+        s1 += su[r * W + i].x;
+        s2 += su[r * W + i].y;
+      },
+      [&](int i, double s1, double s2) {
+        const int oo = tile * g.tx + (i >> 3);
+        if (oo >= g.TO) return;
+        const Oct q = octet(g, oo, true);
+        if ((i & 7) >= q.cnt) return;
+        a.psum[chunk * NC + q.col + (i & 7)] = make_float2((float)s1, (float)s2);
+      });
 }
 
 template <bool FULL, int ACT>
@@ -824,8 +897,8 @@ __global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs
   const int chunk = id / g.ntile, tile = id - chunk * g.ntile;
   const int ox = (int)threadIdx.x % g.tx, py = (int)threadIdx.x / g.tx;
   const int o = tile * g.tx + ox;
-  if (py >= g.ty || o >= g.TO) return;
-  const Oct t = octet(g, o, true);
+  const bool active = py < g.ty && o < g.TO;
+  const Oct t = octet(g, o, active);
   const long long stride = (long long)g.N * g.C;
   const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;
   constexpr int B = kBatch / 2;
@@ -841,11 +914,28 @@ __global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs
   };
   load(p0);
   float mean[8], ga[8], be[8], k1[8], k2[8];
-  load_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
-  load_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
-  load_run<8, FULL>(a.col.k1 + t.col, t.cnt, k1);
-  load_run<8, FULL>(a.col.k2 + t.col, t.cnt, k2);
-  load_optional<FULL>(a.beta, t.c0, t.cnt, 0.0f, be);
+  if (g.wide) {
+    load_run<8, FULL>(a.col.mean + t.col, t.cnt, mean);
+    load_run<8, FULL>(a.col.a + t.col, t.cnt, ga);
+    load_run<8, FULL>(a.col.k1 + t.col, t.cnt, k1);
+    load_run<8, FULL>(a.col.k2 + t.col, t.cnt, k2);
+    load_optional<FULL>(a.beta, t.c0, t.cnt, 0.0f, be);
+  } else {
+    __shared__ float2 sseg[8 * kTileOcts];
+    int ns;
+    const int S0 = tile_segments(g, tile, ns);
+    float rstd[8];
+    grad_params<FULL>(a, t, mean, rstd, ga, be);
+    join_segments<true>(a, S0, ns, sseg);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const bool ok = i < t.cnt;
+      const float2 k = sseg[ok ? t.n * g.G + (int)fdiv((unsigned)(t.c0 + i), g.dD) - S0 : 0];
+      k1[i] = ok ? k.x : 0.0f;
+      k2[i] = ok ? k.y : 0.0f;
+    }
+  }
+  if (!active) return;
   const DropKey key = drop_key(a.drop);
   for (int p = p0; p < g.P; p += B * dp) {
     float d[B][8], gr[B][8];
@@ -871,19 +961,25 @@ __global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs
 
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// The workspace's parts: the columns' parameters, the backward's sums, and
-// the chunks' partial statistics.
+// The workspace's parts: the columns' parameters, the rows of sums of many
+// samples and chunks, and the chunks' partial statistics or sums.
 struct NormWs {
-  size_t cols, tot, part, bytes;
+  size_t cols, fold, part, bytes;
+  int rows;  // backward: rows of sums
 };
 NormWs norm_ws(const NormGeo& g, bool backward) {
   NormWs w{};
-  const size_t nc = (size_t)g.N * g.C;
+  const size_t nc = (size_t)g.N * g.C, chunks = g.one ? 1 : (size_t)g.nchunk;
   w.cols = align256(nc * sizeof(float));
-  w.tot = w.cols * (backward ? 4 : 2);
-  w.part = w.tot + (backward ? align256(nc * sizeof(float2)) : 0);
-  const size_t each = backward ? sizeof(float2) : sizeof(Part);
-  w.bytes = w.part + (g.one ? 0 : (size_t)g.nchunk * (nc / g.UW) * each);
+  w.fold = w.cols * (backward ? 4 : 2);
+  w.part = w.fold;
+  if (backward) {
+    w.rows = (int)(g.N * chunks);
+    if (w.rows > kFoldFrom) w.part += align256((size_t)kFoldRows * g.C * sizeof(float2));
+    w.bytes = w.part + chunks * nc * sizeof(float2);
+  } else {
+    w.bytes = w.part + (g.one ? 0 : chunks * (nc / g.UW) * sizeof(Part));
+  }
   return w;
 }
 
@@ -895,8 +991,10 @@ void bind_ws(NormArgs& a, void* ws, bool backward) {
   if (backward) {
     a.col.k1 = reinterpret_cast<float*>(b + 2 * w.cols);
     a.col.k2 = reinterpret_cast<float*>(b + 3 * w.cols);
-    a.tot = reinterpret_cast<float2*>(b + w.tot);
+    a.fold = reinterpret_cast<float2*>(b + w.fold);
     a.psum = reinterpret_cast<float2*>(b + w.part);
+    a.sum_src = a.psum;
+    a.sum_rows = w.rows;
   } else {
     a.part = reinterpret_cast<Part*>(b + w.part);
   }
@@ -945,19 +1043,14 @@ void launch_stats(const NormArgs& a, hipStream_t st) {
   }
 }
 
-// Columns of a joining workgroup: as many as leave each thread one round of
-// eight reads.
-int join_width(const NormGeo& g) { return std::max(8, std::min(kJoinT, kJoinT * 8 / g.nchunk)); }
-
-// Joins the streaming statistics.
+// Joins the chunks of every group into the columns' parameters.
+template <bool BWD>
 void launch_join(const NormArgs& a, hipStream_t st) {
   const NormGeo& g = a.g;
   const int NS = g.N * g.G;
-  // groups of few units share a workgroup; one of many takes a larger one
-  const int spw = std::max(1, join_width(g) / 2 / g.e);
-  const dim3 grid((unsigned)ceil_div(NS, spw));
-  if ((long long)g.e * g.nchunk > 8192) hipLaunchKernelGGL(norm_join_kernel<1024>, grid, dim3(1024), 0, st, a, spw);
-  else hipLaunchKernelGGL(norm_join_kernel<kJoinT>, grid, dim3(kJoinT), 0, st, a, spw);
+  if (g.wide) hipLaunchKernelGGL(norm_join_wide_kernel<BWD>, dim3((unsigned)NS), dim3(kWideT), 0, st, a);
+  else
+    hipLaunchKernelGGL(norm_join_kernel<BWD>, dim3((unsigned)ceil_div(NS, kJoinT / g.lanes)), dim3(kJoinT), 0, st, a);
 }
 
 template <bool FULL>
@@ -1016,9 +1109,11 @@ hipError_t launch_group_norm(const NormShape& s, const float* x, const float* ga
   hipError_t e = launch_check();
   if (e != hipSuccess || (g.one && y)) return e;
   if (!g.one) {
-    launch_join(a, st);
-    e = launch_check();
-    if (e != hipSuccess) return e;
+    if (!y || g.wide) {
+      launch_join<false>(a, st);
+      e = launch_check();
+      if (e != hipSuccess) return e;
+    }
     if (y) {
       if (full) launch_apply<true>(a, st);
       else launch_apply<false>(a, st);
@@ -1045,23 +1140,19 @@ hipError_t launch_group_norm_backward(const NormShape& s, const float* dy, const
   else launch_sums<false>(a, st);
   hipError_t e = launch_check();
   if (e != hipSuccess) return e;
+  if (extra && a.sum_rows > kFoldFrom) {
+    hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)(ceil_div(g.C, kFoldC) * kFoldRows)), dim3(256), 0, st, a);
+    e = launch_check();
+    if (e != hipSuccess) return e;
+    a.sum_src = a.fold;
+    a.sum_rows = kFoldRows;
+  }
   if (!g.one) {
-    // groups of up to 64 columns are joined whole, larger ones in two steps
-    const long long NC = (long long)g.N * g.C;
-    if (g.D <= 64) {
-      const int cols = std::max(1, join_width(g) / g.D) * g.D;
-      hipLaunchKernelGGL(norm_join_backward_kernel<true>, dim3((unsigned)ceil_div(NC, cols)), dim3(kJoinT), 0, st, a,
-                         cols);
-      e = launch_check();
-    } else {
-      hipLaunchKernelGGL(norm_join_backward_kernel<false>, dim3((unsigned)ceil_div(NC, 16)), dim3(kJoinT), 0, st, a,
-                         16);
+    if (!dx || g.wide) {
+      launch_join<true>(a, st);
       e = launch_check();
       if (e != hipSuccess) return e;
-      hipLaunchKernelGGL(norm_fold_backward_kernel, dim3((unsigned)(g.N * g.G)), dim3(kJoinT), 0, st, a);
-      e = launch_check();
     }
-    if (e != hipSuccess) return e;
     if (dx) {
       if (full) launch_apply_backward<true>(a, extra, st);
       else launch_apply_backward<false>(a, extra, st);
