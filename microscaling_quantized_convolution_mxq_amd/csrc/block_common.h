@@ -28,34 +28,43 @@ typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 // move an address out of range to one in range and leave its values out): the
 // compiler can then count which loads are under way, and waits for a pixel's
 // values only, not for those it has just requested.
+// Partial runs go by quads, so only a run whose end is no multiple of four
+// takes single loads.
 template <int K, bool FULL = false>
 __device__ __forceinline__ void load_run(const float* p, int cnt, float (&v)[K]) {
-  if (FULL || cnt >= K) {
 #pragma unroll
-    for (int i = 0; i < K; i += 4) {
+  for (int i = 0; i < K; i += 4) {
+    if (FULL || cnt >= i + 4) {
       const f4u t = *reinterpret_cast<const f4u*>(p + i);
 #pragma unroll
       for (int j = 0; j < 4; j++) v[i + j] = t[j];
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int i = 0; i < K; i++) v[i] = i < cnt ? p[i] : 0.0f;
+      for (int j = 0; j < 4; j++) v[i + j] = 0.0f;
+      if (cnt > i) {
+#pragma unroll
+        for (int j = 0; j < 3; j++)
+          if (i + j < cnt) v[i + j] = p[i + j];
+      }
+    }
   }
 }
+// FULL: cnt is 0 or K.
 template <int K, bool FULL = false>
 __device__ __forceinline__ void store_run(float* p, int cnt, const float (&v)[K]) {
-  if (FULL ? cnt > 0 : cnt >= K) {
+  if (FULL && cnt <= 0) return;
 #pragma unroll
-    for (int i = 0; i < K; i += 4) {
+  for (int i = 0; i < K; i += 4) {
+    if (FULL || cnt >= i + 4) {
       f4u t;
 #pragma unroll
       for (int j = 0; j < 4; j++) t[j] = v[i + j];
       *reinterpret_cast<f4u*>(p + i) = t;
-    }
-  } else if constexpr (!FULL) {
+    } else if (cnt > i) {
 #pragma unroll
-    for (int i = 0; i < K; i++)
-      if (i < cnt) p[i] = v[i];
+      for (int j = 0; j < 3; j++)
+        if (i + j < cnt) p[i + j] = v[i + j];
+    }
   }
 }
 

@@ -24,6 +24,7 @@ namespace mq {
 struct MxRows {
   uint8_t *codes, *scales;
   int P, N, C, nCB, bp, nPB;
+  int grp;          // lane pairs of a pixel, where a tile holds several (N < 32)
   int ppt, npt;     // pixels per tile, tiles along the pixels
   int cbw, pw;      // a workgroup's channel blocks and pixel tiles (waves)
   int nslice;       // groups of cbw channel blocks
@@ -39,12 +40,14 @@ inline MxRows mx_rows(const MxOutView& out, int P, int N, int C) {
   g.codes = out.codes; g.scales = out.scales;
   g.P = P; g.N = N; g.C = C; g.bp = out.bp;
   g.nCB = ceil_div(C, 32); g.nPB = ceil_div(N, out.bp);
-  // with fewer than 32 samples a tile holds whole pixels; squares need their
-  // rows in aligned groups of lanes, hence a power of two
-  const bool pack = N < 32 && (out.bp == 1 || 32 % N == 0);
-  g.ppt = pack ? 32 / N : 1;
+  // with fewer than 32 samples a tile holds whole pixels; squares need each
+  // pixel's rows in an aligned group of lanes, a power of two of them
+  g.grp = N < 32 ? N : 32;
+  if (out.bp != 1)
+    for (g.grp = 1; g.grp < 32 && g.grp < N;) g.grp *= 2;
+  g.ppt = 32 / g.grp;
   g.npt = ceil_div(P, g.ppt);
-  g.glanes = out.bp == 1 ? 2 : (pack ? 2 * N : 64);
+  g.glanes = out.bp == 1 ? 2 : 2 * g.grp;
   g.cbw = g.nCB < kRowsWaves ? g.nCB : kRowsWaves;
   g.pw = kRowsWaves / g.cbw;
   if (g.pw > g.npt) g.pw = g.npt;
@@ -79,11 +82,8 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(const Src src,
   const int pi = wave / g.cbw, cbi = wave - pi * g.cbw;
   const int r = lane >> 1, half = lane & 1;
   const int cb = cb0 + cbi, c0 = cb * 32 + half * 16;
-  int psub = 0, n = nt * 32 + r;
-  if (g.N < 32) {
-    psub = r / g.N;
-    n = r - psub * g.N;
-  }
+  const int psub = r / g.grp, n = nt * 32 + r - psub * g.grp;
+  const int srow = psub * g.N + (n - nt * 32);  // the tile's rows in memory order
   const bool row_ok = n < g.N && psub < g.ppt, lane_ok = row_ok && c0 < g.C && cbi < cbe;
   const int cnt = lane_ok ? min(16, g.C - c0) : 0;  // this lane's channels
   const int na = row_ok ? n : 0, ca = c0 < g.C ? c0 : 0;
@@ -120,7 +120,8 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(const Src src,
     float v[16];
     scale_clamp16<F>(x, S, v);
     uint8_t* const tile = &stage[buf][pi * 32 * pitch];
-    if (cbi < cbe) convert_store_half_run<F>(tile + r * pitch + cbi * RB + half * (RB / 2), v, code_keep(S));
+    if (row_ok && cbi < cbe)
+      convert_store_half_run<F>(tile + srow * pitch + cbi * RB + half * (RB / 2), v, code_keep(S));
     if (row_ok && cbi < cbe && t + pi < g.npt && p < g.P && half == 0) {
       if (g.bp == 1) g.scales[((long long)p * g.N + n) * g.nCB + cb] = (uint8_t)S;
       else if ((n & 31) == 0) g.scales[((long long)p * g.nPB + (n >> 5)) * g.nCB + cb] = (uint8_t)S;
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(const Src src,
     asm volatile("" ::: "memory");
     if (t + pi < g.npt) {
       const int p0 = (t + pi) * g.ppt;
-      const int rows = g.N < 32 ? min(g.ppt, g.P - p0) * g.N : min(32, g.N - nt * 32);
+      const int rows = min(g.ppt, g.P - p0) * min(32, g.N - nt * 32);
       const long long row0 = (long long)p0 * g.N + nt * 32;
       constexpr int VW = RB % 16 == 0 ? 16 : 8;
       typedef uint32_t vw_t __attribute__((ext_vector_type(VW / 4)));

@@ -66,7 +66,11 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
     so = std::max(so, unit * (long long)ceil_div(256, (long long)std::min(s.P, 256) * unit));
     so = std::min(so, (long long)tmax / unit * unit);
     so = std::min(so, (long long)ceil_div(g.TO, unit) * unit);
-    for (int t = backward ? 256 : 512; t <= tmax && !g.one; t *= 2) {
+    // few slabs take more threads of fewer pixels, many the smallest
+    // workgroups that hold them (backward, 1,024 slabs of 400 pixels: 256
+    // threads 66, 512 threads 80 us)
+    int t = backward && ceil_div(g.TO, so) >= 256 ? 256 : 512;
+    for (; t <= tmax && !g.one; t *= 2) {
       if (so > t) continue;
       const int ty = std::min(s.P, t / (int)so);
       // (1,024 threads have 128 registers each, room for half as many pixels)
