@@ -12,11 +12,23 @@
 
 namespace mq {
 
-// kActAny (as a template argument): the kernel takes the activation from its
-// arguments. GELU's erf costs registers that the other activations' kernels
-// need for values in flight, so whole-octet tensors take kernels of their own
-// activation.
-enum { kActAny = -1, kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+// Kernels are built for each activation: GELU's erf costs registers that the
+// others need for values in flight.
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+template <int A>
+struct ActTag {
+  static constexpr int value = A;
+};
+// f(an ActTag of the activation)
+template <class F>
+auto with_act(int act, F&& f) {
+  switch (act) {
+    case kActNone: return f(ActTag<kActNone>{});
+    case kActRelu: return f(ActTag<kActRelu>{});
+    case kActSilu: return f(ActTag<kActSilu>{});
+    default: return f(ActTag<kActGelu>{});
+  }
+}
 
 // Four floats at any 4-byte aligned address (one 16-byte access: global
 // memory accesses need no more than dword alignment).
@@ -78,38 +90,36 @@ __device__ __forceinline__ float normal_cdf(float u) {
   return 0.5f * (1.0f + erff(u * 0.70710678f));
 }
 
-// The activation of every value of u, in place (act is uniform).
+// The activation of every value of u, in place.
 template <int ACT, int K>
-__device__ __forceinline__ void act_values(int act, float (&u)[K]) {
+__device__ __forceinline__ void act_values(float (&u)[K]) {
 #pragma clang fp contract(off)
-  if constexpr (ACT != kActAny) act = ACT;
-  if (act == kActSilu) {
+  if constexpr (ACT == kActSilu) {
 #pragma unroll
     for (int i = 0; i < K; i++) u[i] = u[i] * sigmoid(u[i]);
-  } else if (act == kActRelu) {
+  } else if constexpr (ACT == kActRelu) {
 #pragma unroll
     for (int i = 0; i < K; i++) u[i] = u[i] < 0.0f ? 0.0f : u[i];
-  } else if (act == kActGelu) {
+  } else if constexpr (ACT == kActGelu) {
 #pragma unroll
     for (int i = 0; i < K; i++) u[i] = u[i] * normal_cdf(u[i]);
   }
 }
 // g *= act'(u).
 template <int ACT, int K>
-__device__ __forceinline__ void act_slopes(int act, const float (&u)[K], float (&g)[K]) {
+__device__ __forceinline__ void act_slopes(const float (&u)[K], float (&g)[K]) {
 #pragma clang fp contract(off)
-  if constexpr (ACT != kActAny) act = ACT;
-  if (act == kActSilu) {
+  if constexpr (ACT == kActSilu) {
 #pragma unroll
     for (int i = 0; i < K; i++) {
       const float s = sigmoid(u[i]);
       g[i] = g[i] * (s * __builtin_fmaf(u[i], 1.0f - s, 1.0f));
     }
-  } else if (act == kActRelu) {
+  } else if constexpr (ACT == kActRelu) {
     // (a product, not a select: a NaN in u or g stays one)
 #pragma unroll
     for (int i = 0; i < K; i++) g[i] = u[i] != u[i] ? u[i] : g[i] * (u[i] > 0.0f ? 1.0f : 0.0f);
-  } else if (act == kActGelu) {
+  } else if constexpr (ACT == kActGelu) {
 #pragma unroll
     for (int i = 0; i < K; i++)
       g[i] = g[i] * __builtin_fmaf(u[i] * 0.39894228f, exp_neg(0.5f * u[i] * u[i]), normal_cdf(u[i]));

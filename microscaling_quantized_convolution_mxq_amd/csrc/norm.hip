@@ -20,7 +20,6 @@
 // in fp32 around means of the values themselves, so a mean far from zero
 // costs no digits, and joined in fp64.
 #include <algorithm>
-#include <type_traits>
 
 #include "norm.h"
 
@@ -75,10 +74,13 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
       const int ty = std::min(s.P, t / (int)so);
       // (1,024 threads have 128 registers each, room for half as many pixels)
       if (ceil_div(s.P, ty) > (t > 512 ? kOneR / 2 : kOneR)) continue;
+      // a small tensor's few slabs need workgroups more than whole lines
+      // (124 x 4 x 32 x 8, gradient of GELU: 15 us with four octets, 11 with one)
+      if (ceil_div(g.TO, so) < 64) so = unit;
       g.one = true;
       g.so = (int)so;
-      g.ty1 = ty;
-      g.T1 = ceil_div((long long)so * ty, 64) * 64;
+      g.ty1 = std::min(s.P, t / (int)so);
+      g.T1 = ceil_div((long long)so * g.ty1, 64) * 64;
       g.nslab = ceil_div(g.TO, so);
       g.nseg = within ? (int)(so * 8 / g.D) : (int)(so / g.NO) * g.G;
     }
@@ -103,6 +105,8 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
   // thread (gradient of 80 x 80 x 16 x 64: 34 us, 38 with 1,024 workgroups)
   g.ngroup = ceil_div(s.P, g.ty);
   g.nchunk = std::max(1, std::min(kStreamGroups / std::min(kStreamGroups, g.ntile), std::max(ceil_div(g.ngroup, kBatch), std::min(g.ngroup, 256 / std::min(256, g.ntile)))));
+  // and no more chunks than a workgroup of the elementwise pass joins at once
+  g.nchunk = std::min(g.nchunk, 256 / g.tx);
   // eight loads a lane
   const long long entries = (long long)g.e * g.nchunk;
   g.wide = entries > 2048;
@@ -221,13 +225,13 @@ __device__ __forceinline__ double group_sum(double v, int lanes) {  // aligned g
   return v;
 }
 
-// Sums of W columns over rows 0 .. n - 1 by 256 threads: get(row, column, s1,
-// s2) adds a row's values, done(column, s1, s2) takes the sums. Thread t adds
-// rows t / W, t / W + 256 / W, ... of column t % W; then a tree.
+// Sums of columns 0 .. W - 1 over rows 0 .. n - 1 by T threads: get(row,
+// column, s1, s2) adds a row's values, done(column, s1, s2) takes the sums.
+// Thread t adds rows t / W, t / W + T / W, ... of column t % W; then a tree
+// over x1, x2 [T]. W is at most T.
 template <class Get, class Done>
-__device__ __forceinline__ void reduce_rows(int W, int n, Get get, Done done) {
-  __shared__ double x1[256], x2[256];
-  const int t = (int)threadIdx.x, r = t / W, u = t - r * W, R = 256 / W;
+__device__ __forceinline__ void reduce_rows(int T, int W, int n, double* x1, double* x2, Get get, Done done) {
+  const int t = (int)threadIdx.x, r = t / W, u = t - r * W, R = T / W;
   double s1 = 0, s2 = 0;
   if (r < R)
     for (int row = r; row < n; row += R) get(row, u, s1, s2);
@@ -326,7 +330,7 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
         const int p = py + k * g.ty1;
         float u[8];
         norm_values<8>(mean, ga, be, v[k], u);
-        act_values<ACT, 8>(a.act, u);
+        act_values<ACT, 8>(u);
         drop_values<8>(a.drop, key, (uint32_t)p * g.N + t.n, t.c0, u);
         store_run<8, FULL>(a.out + p * stride + t.col, t.cnt, u);
       }
@@ -397,8 +401,9 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
   // pixels of row r of the chunk: a group less where the last group is short
   const int groups = (g.ngroup - chunk + g.nchunk - 1) / g.nchunk, last = g.ngroup - 1;
   const bool owns_last = last % g.nchunk == chunk;
+  __shared__ double x1[256], x2[256];
   reduce_rows(
-      W, g.ty,
+      256, W, g.ty, x1, x2,
       [&](int r, int i, double& s1, double& s2) {
         const int rows = groups - (owns_last && last * g.ty + r >= g.P ? 1 : 0);
         if (rows == 0) return;
@@ -657,7 +662,7 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
       if (q >= g.P) break;
       float u[8];
       norm_values<8>(mean, ga, be, v[k], u);
-      act_values<ACT, 8>(a.act, u);
+      act_values<ACT, 8>(u);
       drop_values<8>(a.drop, key, (uint32_t)q * g.N + t.n, t.c0, u);
       store_run<8, FULL>(a.out + q * stride + t.col, t.cnt, u);
     }
@@ -692,7 +697,7 @@ __device__ __forceinline__ void grad_terms(const NormArgs& a, const DropKey& key
   float u[8];
   norm_values<8>(mean, ga, be, d, u);
   drop_values<8>(a.drop, key, (uint32_t)p * a.g.N + t.n, t.c0, gr);
-  act_slopes<ACT, 8>(a.act, u, gr);
+  act_slopes<ACT, 8>(u, gr);
 }
 
 template <int R, bool FULL, int ACT>
@@ -737,20 +742,28 @@ __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a
     for (int i = 0; i < 8; i++) su[py * W + ox * 8 + i] = make_float2(s1[i], s2[i] * rstd[i]);
   }
   __syncthreads();
-  // the columns' sums over the rows
-  for (int i = (int)threadIdx.x; i < W; i += (int)blockDim.x) {
-    const int oo = o0 + (i >> 3);
-    if (oo >= g.TO) continue;
-    const Oct q = octet(g, oo, true);
-    if ((i & 7) >= q.cnt) continue;
-    double s1 = 0, s2 = 0;
-    for (int r = 0; r < g.ty1; r++) {
-      s1 += su[r * W + i].x;
-      s2 += su[r * W + i].y;
-    }
-    const float2 tot = make_float2((float)s1, (float)s2);
-    su[i] = tot;
-    a.psum[q.col + (i & 7)] = tot;
+  // the columns' sums over the rows, T at a time
+  const int T = (int)blockDim.x;
+  double* const x1 = reinterpret_cast<double*>(sseg);  // [T], x2 behind it: before the segments' values
+  for (int w0 = 0; w0 < W; w0 += T) {
+    const int w = min(T, W - w0);
+    if (w0 > 0) __syncthreads();
+    reduce_rows(
+        T, w, g.ty1, x1, x1 + T,
+        [&](int r, int i, double& s1, double& s2) {
+          s1 += su[r * W + w0 + i].x;
+          s2 += su[r * W + w0 + i].y;
+        },
+        [&](int i, double s1, double s2) {
+          i += w0;
+          const int oo = o0 + (i >> 3);
+          if (oo >= g.TO) return;
+          const Oct q = octet(g, oo, true);
+          if ((i & 7) >= q.cnt) return;
+          const float2 tot = make_float2((float)s1, (float)s2);
+          a.psum[q.col + (i & 7)] = tot;
+          su[i] = tot;  // (row 0 of this column, which only this thread still reads)
+        });
   }
   __syncthreads();
   const int n0 = (int)fdiv((unsigned)o0, g.dNO);
@@ -875,8 +888,9 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
     for (int i = 0; i < 8; i++) su[py * W + ox * 8 + i] = make_float2(s1[i], s2[i]);
   __syncthreads();
   const long long NC = stride;
+  __shared__ double x1[256], x2[256];
   reduce_rows(
-      W, g.ty,
+      256, W, g.ty, x1, x2,
       [&](int r, int i, double& s1, double& s2) {
         s1 += su[r * W + i].x;
         s2 += su[r * W + i].y;
@@ -1004,21 +1018,6 @@ void bind_ws(NormArgs& a, void* ws, bool backward) {
   }
 }
 
-// f(activation as a compile-time constant)
-template <bool FULL, class F>
-void with_act(int act, F&& f) {
-  if constexpr (FULL) {
-    switch (act) {
-      case kActNone: f(std::integral_constant<int, kActNone>{}); break;
-      case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
-      case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
-      default: f(std::integral_constant<int, kActGelu>{}); break;
-    }
-  } else {
-    f(std::integral_constant<int, kActAny>{});
-  }
-}
-
 template <int UW, bool FULL>
 void launch_stats(const NormArgs& a, hipStream_t st) {
   const NormGeo& g = a.g;
@@ -1028,7 +1027,7 @@ void launch_stats(const NormArgs& a, hipStream_t st) {
   }
   const int R = ceil_div(g.P, g.ty1);
   const size_t lds = (size_t)(g.ty1 * g.so * (8 / UW)) * sizeof(Part) + (size_t)g.nseg * sizeof(float2);
-  with_act<FULL>(a.act, [&](auto act) {
+  with_act(a.act, [&](auto act) {
     constexpr int A = decltype(act)::value;
     const auto kern = R <= 1   ? norm_one_kernel<1, UW, FULL, A>
                       : R <= 2 ? norm_one_kernel<2, UW, FULL, A>
@@ -1061,15 +1060,16 @@ template <bool FULL>
 void launch_sums(const NormArgs& a, hipStream_t st) {
   const NormGeo& g = a.g;
   if (!g.one) {
-    with_act<FULL>(a.act, [&](auto act) {
+    with_act(a.act, [&](auto act) {
       hipLaunchKernelGGL((norm_sums_kernel<FULL, decltype(act)::value>), dim3((unsigned)(g.ntile * g.nchunk)),
                          dim3(256), 0, st, a);
     });
     return;
   }
   const int R = ceil_div(g.P, g.ty1);
-  const size_t lds = ((size_t)g.ty1 * g.so * 8 + g.nseg) * sizeof(float2);
-  with_act<FULL>(a.act, [&](auto act) {
+  const size_t lds = (size_t)g.ty1 * g.so * 8 * sizeof(float2) +
+                     std::max((size_t)g.nseg * sizeof(float2), (size_t)g.T1 * 2 * sizeof(double));
+  with_act(a.act, [&](auto act) {
     constexpr int A = decltype(act)::value;
     const auto kern = R <= 1   ? norm_one_backward_kernel<1, FULL, A>
                       : R <= 2 ? norm_one_backward_kernel<2, FULL, A>
@@ -1081,14 +1081,14 @@ void launch_sums(const NormArgs& a, hipStream_t st) {
 
 template <bool FULL>
 void launch_apply(const NormArgs& a, hipStream_t st) {
-  with_act<FULL>(a.act, [&](auto act) {
+  with_act(a.act, [&](auto act) {
     hipLaunchKernelGGL((norm_apply_kernel<FULL, decltype(act)::value>), dim3((unsigned)(a.g.ntile * a.g.nchunk)),
                        dim3(256), 0, st, a);
   });
 }
 template <bool FULL>
 void launch_apply_backward(const NormArgs& a, int extra, hipStream_t st) {
-  with_act<FULL>(a.act, [&](auto act) {
+  with_act(a.act, [&](auto act) {
     hipLaunchKernelGGL((norm_apply_backward_kernel<FULL, decltype(act)::value>),
                        dim3((unsigned)(a.g.ntile * a.g.nchunk + extra)), dim3(256), 0, st, a, extra);
   });

@@ -36,7 +36,7 @@ struct NormSrc {
 #pragma unroll
     for (int i = 0; i < 16; i++) d[i] = r.x[i];
     norm_values<16>(s.mean, s.a, s.be, d, v);
-    act_values<ACT, 16>(a.act, v);
+    act_values<ACT, 16>(v);
     drop_values<16>(a.drop, s.key, (uint32_t)p * a.g.N + n, c0, v);
   }
   __device__ void extra(int) const {}
@@ -80,7 +80,7 @@ struct NormGradSrc {
     }
     norm_values<16>(s.mean, s.a, s.be, d, u);
     drop_values<16>(a.drop, s.key, (uint32_t)p * a.g.N + n, c0, g);
-    act_slopes<ACT, 16>(a.act, u, g);
+    act_slopes<ACT, 16>(u, g);
     norm_grad_values<16>(s.a, s.k1, s.k2, d, g, v);
   }
   __device__ void extra(int b) const { norm_channel_sums(a, b); }
@@ -90,13 +90,11 @@ namespace {
 template <template <bool, int> class Src>
 hipError_t launch(const NormArgs& a, const MxOutView& out, int extra, hipStream_t st) {
   const MxRows g = mx_rows(out, a.g.P, a.g.N, a.g.C);
-  if (a.g.C % 16 != 0) return launch_mx_rows(out.fmt, Src<false, kActAny>{a}, g, extra, st);
-  switch (a.act) {
-    case kActNone: return launch_mx_rows(out.fmt, Src<true, kActNone>{a}, g, extra, st);
-    case kActRelu: return launch_mx_rows(out.fmt, Src<true, kActRelu>{a}, g, extra, st);
-    case kActSilu: return launch_mx_rows(out.fmt, Src<true, kActSilu>{a}, g, extra, st);
-    default: return launch_mx_rows(out.fmt, Src<true, kActGelu>{a}, g, extra, st);
-  }
+  return with_act(a.act, [&](auto act) {
+    constexpr int A = decltype(act)::value;
+    return a.g.C % 16 == 0 ? launch_mx_rows(out.fmt, Src<true, A>{a}, g, extra, st)
+                           : launch_mx_rows(out.fmt, Src<false, A>{a}, g, extra, st);
+  });
 }
 }  // namespace
 
