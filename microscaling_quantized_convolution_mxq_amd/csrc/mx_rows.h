@@ -69,11 +69,11 @@ template <int F, class Src>
 __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(const Src src, const MxRows g) {
   constexpr int RB = run_bytes_of(F);
   __shared__ __attribute__((aligned(16))) uint8_t stage[2][kRowsWaves * 32 * RB];
-  // neighbouring workgroups: neighbouring rows and channels of a pixel
   if ((int)blockIdx.x < g.extra) {  // the source's own work
     src.extra((int)blockIdx.x);
     return;
   }
+  // neighbouring workgroups: neighbouring rows and channels of a pixel
   const int id = (int)blockIdx.x - g.extra;
   const int xb = id / g.ny, yb = id - xb * g.ny;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -425,7 +425,12 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
 // ---------------------------------------------------------------------------
 // joining the chunks
 // ---------------------------------------------------------------------------
-constexpr int kJoinT = 256, kWideT = 1024;
+// Threads of a workgroup that joins segments. The backward's few segments have
+// four parameters a column to write, so they are spread over more workgroups
+// (128 samples of 256 channels in 32 groups, two chunks: 64 threads 4.9, 256
+// 5.8 us); the forward's two are not (16 of 64 channels, 32 chunks: 4.4, 3.9 us).
+constexpr int join_threads(bool bwd) { return bwd ? 64 : 256; }
+constexpr int kWideT = 1024;
 
 // Statistics of segment (sample, group) S from its units of all chunks: lane
 // j of `lanes` takes every lanes-th. Every caller's lanes sum in the same
@@ -546,11 +551,12 @@ __device__ __forceinline__ void keep_stats(const NormArgs& a, int S0, int ns, co
   }
 }
 
-// kJoinT / lanes segments a workgroup.
+// join_threads / lanes segments a workgroup, a latency of three dependent
+// loads: what it costs is mostly its launch.
 template <bool BWD>
-__global__ __launch_bounds__(kJoinT) void norm_join_kernel(const NormArgs a) {
-  __shared__ float2 sseg[kJoinT];
-  const int per = kJoinT / a.g.lanes, S0 = (int)blockIdx.x * per, ns = min(per, a.g.N * a.g.G - S0);
+__global__ __launch_bounds__(join_threads(BWD)) void norm_join_kernel(const NormArgs a) {
+  __shared__ float2 sseg[join_threads(BWD)];
+  const int per = join_threads(BWD) / a.g.lanes, S0 = (int)blockIdx.x * per, ns = min(per, a.g.N * a.g.G - S0);
   const ColIn in = column_in<BWD>(a, S0, ns, (int)threadIdx.x);
   join_segments<BWD>(a, S0, ns, sseg);
   if constexpr (!BWD) keep_stats(a, S0, ns, sseg);
@@ -1052,8 +1058,10 @@ void launch_join(const NormArgs& a, hipStream_t st) {
   const NormGeo& g = a.g;
   const int NS = g.N * g.G;
   if (g.wide) hipLaunchKernelGGL(norm_join_wide_kernel<BWD>, dim3((unsigned)NS), dim3(kWideT), 0, st, a);
-  else
-    hipLaunchKernelGGL(norm_join_kernel<BWD>, dim3((unsigned)ceil_div(NS, kJoinT / g.lanes)), dim3(kJoinT), 0, st, a);
+  else {
+    constexpr int T = join_threads(BWD);
+    hipLaunchKernelGGL(norm_join_kernel<BWD>, dim3((unsigned)ceil_div(NS, T / g.lanes)), dim3(T), 0, st, a);
+  }
 }
 
 template <bool FULL>
