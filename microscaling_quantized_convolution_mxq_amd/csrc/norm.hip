@@ -28,8 +28,14 @@ namespace mq {
 namespace {
 
 constexpr int kOneR = 8;         // most pixels a thread of the one-pass kernels holds
-constexpr int kBatch = 4;        // pixels a thread of the streaming kernels has in flight
+// Values that a thread of the streaming kernels has in flight: two pixels of
+// one tensor or one pixel of two, beside as many being computed. Few registers
+// and many waves read faster than many loads a wave (two, four and eight
+// pixels: 160 x 160 x 32 x 128 236, 239, 244 us; gradient of 80 x 80 x 16 x 64
+// 31.2, 32.5, 40.7 us).
+constexpr int kBatch = 2;
 constexpr int kStreamGroups = 512;  // workgroups of the streaming kernels, about
+constexpr int kMinPixels = 4;       // pixels of a thread, before there are fewer workgroups
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
@@ -102,9 +108,9 @@ NormGeo norm_geo(const NormShape& s, bool backward) {
     }
   }
   // up to 512 workgroups (two per compute unit) of at least four pixels a
-  // thread (gradient of 80 x 80 x 16 x 64: 34 us, 38 with 1,024 workgroups)
+  // thread (MX gradient of 20 x 20 x 128 x 256: 52.4 us, 55.5 with 1,024)
   g.ngroup = ceil_div(s.P, g.ty);
-  g.nchunk = std::max(1, std::min(kStreamGroups / std::min(kStreamGroups, g.ntile), std::max(ceil_div(g.ngroup, kBatch), std::min(g.ngroup, 256 / std::min(256, g.ntile)))));
+  g.nchunk = std::max(1, std::min(kStreamGroups / std::min(kStreamGroups, g.ntile), std::max(ceil_div(g.ngroup, kMinPixels), std::min(g.ngroup, 256 / std::min(256, g.ntile)))));
   // and no more chunks than a workgroup of the elementwise pass joins at once
   g.nchunk = std::min(g.nchunk, 256 / g.tx);
   // eight loads a lane
