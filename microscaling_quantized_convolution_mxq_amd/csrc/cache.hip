@@ -58,6 +58,8 @@ __device__ __forceinline__ void values4(uint32_t w, float sc, float (&v)[4]) {
 // One workgroup: a sample, up to eight of its channel blocks (one wave each)
 // and tiles of 32 consecutive pixels, whose rows are one stretch of the slot.
 // The wave's arrangement is the quantizer's (lane l: row l / 2, 16 channels).
+// Bound by reading pieces of a row as long as a sample's channels: 128 samples
+// of 20 x 20 x 256 as E4M3 14 to 15 us (65.9 MB, 4.5 TB/s).
 struct CacheWrite {
   CacheView c;
   const float* x;
@@ -168,7 +170,8 @@ hipError_t launch_cache_write(const CacheView& c, const float* x, int N, int n0,
 // A thread turns four codes into one 16-byte store, so a wave's stores are
 // 1 KB of consecutive bytes. A workgroup's tile is kReadPix pixels x a few
 // samples: the scale bytes of a slot's neighbouring pixels share cache lines,
-// which one workgroup then uses up.
+// which one workgroup then uses up. Bound by the stores: 128 samples of 20 x 20
+// x 256 from E2M1 15 us (52 MB written, 7 MB read).
 constexpr int kReadPix = 16, kReadUnroll = 4;
 struct CacheRead {
   CacheView c;
@@ -257,7 +260,8 @@ hipError_t launch_cache_read(const CacheView& c, const int32_t* slot, int count,
 // The values of half a stored run are the source of the packed rows; a block
 // whose lines come back with their own format and scale gets its codes back,
 // because the largest code of a line lies in the format's largest binade (or
-// the line's scale byte is 0, and its values' too).
+// the line's scale byte is 0, and its values' too). Bound by decoding and
+// encoding: 128 samples of 20 x 20 x 256 from E3M2 to E4M3 squares 10.7 us (23 MB).
 template <int FI, bool FULL>
 struct CacheSrc {
   CacheView c;

@@ -13,7 +13,11 @@
 // requested before the current one is converted. The up to eight channel
 // blocks of a tile are one workgroup's waves; they pack their codes in LDS
 // and the tile leaves as one contiguous stretch (a row's 32-byte pieces
-// stored one by one reach HBM far less efficiently).
+// stored one by one reach HBM far less efficiently). Eight waves: four were 2
+// to 5% faster for single tensors of 26 MB and as much slower for larger ones
+// (group norm of 160 x 160 x 32 x 128 as E4M3 182 against 187 us).
+// Measured at dropout of 80 x 80 x 16 x 64 as E5M2, a source of few operations:
+// 33 MB in 8.3 us with its launch.
 #pragma once
 #include <type_traits>
 
