@@ -10,7 +10,6 @@ import pytest
 
 import microscaling_quantized_convolution_mxq_amd as mq
 from microscaling_quantized_convolution_mxq_amd import build as b
-from microscaling_quantized_convolution_mxq_amd import build_sanitize as san
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "mqconv_block.h")
@@ -197,12 +196,15 @@ def test_binding_checks_tensors():
     assert "gamma" in reason(FAKE, z(7))
 
 
-@pytest.mark.skipif(not san.runtime(), reason="clang AddressSanitizer runtime not installed")
 def test_refusals_and_plans_under_host_sanitizers():
     if os.environ.get("MQCONV_LIB"):
         pytest.skip("already under the sanitizers")
     if not os.path.exists(b.LIB):
         pytest.skip("libmqconv.so is not built")
+    # (here, so that collecting the tests does not need the sanitizer build's module)
+    from microscaling_quantized_convolution_mxq_amd import build_sanitize as san
+    if not san.runtime():
+        pytest.skip("clang AddressSanitizer runtime not installed")
     env = dict(os.environ, LD_PRELOAD=san.runtime(), MQCONV_LIB=san.build(),
                ASAN_OPTIONS="detect_leaks=0:abort_on_error=1:halt_on_error=1", UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", os.path.abspath(__file__)], cwd=ROOT,
