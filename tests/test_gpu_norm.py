@@ -25,12 +25,13 @@ E, K, EPS = 2.0 ** -24, 64, 1e-5
 # (H, W, N, C, groups): single values, one pixel (tokens), odd extents and
 # channel counts, groups smaller and larger than an octet, one-pass and
 # streaming sizes, a group too large for one workgroup, more samples and
-# chunks than one step sums
+# chunks than one step sums, a workgroup of thousands of groups (82 KB of LDS)
 SHAPES = [
     (1, 1, 1, 1, 1), (1, 1, 1, 8, 2), (1, 1, 300, 64, 1), (1, 1, 7, 1000, 1), (1, 1, 33, 40, 40), (16, 16, 2, 32, 8),
     (5, 3, 33, 45, 9), (19, 23, 5, 90, 9), (20, 20, 8, 64, 8), (31, 33, 2, 24, 24), (40, 40, 3, 96, 4),
     (64, 48, 3, 30, 3), (80, 80, 4, 64, 16), (9, 7, 1, 9008, 1), (33, 31, 2, 2048, 1), (75, 75, 1, 3, 1),
     (57, 61, 17, 33, 11), (1, 1, 2000, 24, 3), (80, 80, 40, 16, 4),
+    (1, 1, 3, 4095, 4095), (2, 2, 3, 4095, 1365),
 ]
 
 
