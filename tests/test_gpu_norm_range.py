@@ -1,0 +1,71 @@
+"""Group norm where its numbers are hard on fp32: repeated calls over
+workspaces that hold anything, very large values, means far from zero and
+long sums, at sizes of the one-pass kernels and of the streaming ones."""
+import numpy as np
+import pytest
+import torch
+
+import microscaling_quantized_convolution_mxq_amd as mq
+from oracle import block
+from gpu_common import dev, host, say
+
+pytestmark = pytest.mark.gpu
+E, EPS = 2.0 ** -24, 1e-5
+
+
+def _forward(shape, x, gamma, beta, act, ws_fill=0, mx=None, drop=None):
+    """(y or (codes, scales), mean, rstd), outputs poisoned before the call."""
+    h, w, n, c, g = shape
+    gn = mq.mq_norm(h, w, n, c, g, act, EPS)
+    mean, rstd = (torch.full((n, g), float("nan"), device="cuda") for _ in range(2))
+    ws = torch.full((mq.mqconv_group_norm_workspace_bytes(gn, mq.NORM_FWD),), ws_fill, dtype=torch.uint8, device="cuda")
+    if mx is None:
+        y = torch.full((h, w, n, c), float("nan"), device="cuda")
+        mq.mqconv_group_norm(gn, x, gamma, beta, y, mean, rstd, ws, drop=drop)
+        return y, mean, rstd
+    t = mq.MxTensor.empty(mq.ROLE_ACT, mx[0], mx[1], (h, w, n, c))
+    t.codes.fill_(ws_fill)
+    t.scales.fill_(ws_fill)
+    mq.mqconv_group_norm_mx(gn, x, gamma, beta, t, mean, rstd, ws, drop=drop)
+    return t.codes, t.scales, mean, rstd
+
+
+def _backward(shape, dy, x, gamma, beta, mean, rstd, act, ws_fill=0, mx=None, drop=None):
+    h, w, n, c, g = shape
+    gn = mq.mq_norm(h, w, n, c, g, act, EPS)
+    dg, db = (torch.full((c,), float("nan"), device="cuda") for _ in range(2))
+    ws = torch.full((mq.mqconv_group_norm_workspace_bytes(gn, mq.NORM_BWD),), ws_fill, dtype=torch.uint8, device="cuda")
+    if mx is None:
+        dx = torch.full((h, w, n, c), float("nan"), device="cuda")
+        mq.mqconv_group_norm_backward(gn, dy, x, gamma, beta, mean, rstd, dx, dg, db, ws, drop=drop)
+        return dx, dg, db
+    t = mq.MxTensor.empty(mq.ROLE_GRAD, mx[0], mx[1], (h, w, n, c))
+    t.codes.fill_(ws_fill)
+    t.scales.fill_(ws_fill)
+    mq.mqconv_group_norm_backward_mx(gn, dy, x, gamma, beta, mean, rstd, t, dg, db, ws, drop=drop)
+    return t.codes, t.scales, dg, db
+
+
+def _random(shape, seed):
+    h, w, n, c, _ = shape
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    return r(h, w, n, c), r(h, w, n, c), 1 + 0.2 * r(c), 0.3 * r(c)
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 2, 32, 8), (19, 23, 5, 90, 9), (20, 20, 128, 256, 32), (80, 80, 16, 64, 16),
+                                   (57, 61, 17, 33, 11), (33, 31, 2, 2048, 1), (1, 1, 2000, 24, 3)], ids=str)
+def test_calls_repeat_bit_for_bit_whatever_the_workspace_holds(shape):
+    say(f"norm repeats {shape}")
+    x, dy, gamma, beta = _random(shape, 17)
+    drop = mq.mq_drop(0.2, 5)
+    ref = None
+    for fill in (0x00, 0xFF, 0x7F, 0x01, 0x80):  # zeros, NaN, large values, small ones of both signs
+        y = _forward(shape, x, gamma, beta, mq.ACT_SILU, fill, drop=drop)
+        got = [*y, *_forward(shape, x, gamma, beta, mq.ACT_SILU, fill, (0, 32), drop),
+               *_backward(shape, dy, x, gamma, beta, y[1], y[2], mq.ACT_SILU, fill, drop=drop),
+               *_backward(shape, dy, x, gamma, beta, y[1], y[2], mq.ACT_SILU, fill, (1, 32), drop)]
+        assert all(bool(torch.isfinite(t).all()) for t in got if t.dtype == torch.float32)
+        ref = ref or got
+        for i, (a, b) in enumerate(zip(got, ref)):
+            assert torch.equal(a, b), f"output {i} differs over a workspace of {fill:#x}"
