@@ -181,14 +181,27 @@ __device__ __forceinline__ Part part_of(double sum, double n, float m, float q) 
   return Part{m, (float)(sum / n - (double)m), q};
 }
 
-// Joins `n` values of mean m and squared deviations q into (mean, m2) of
-// `have` ones.
-__device__ __forceinline__ void join(float& mean, float& m2, float have, float m, float q, float n) {
-  const float f = n / (have + n);
-  const float d = m - mean;
-  mean = __builtin_fmaf(d, f, mean);
-  m2 = m2 + __builtin_fmaf(d * d, have * f, q);
-}
+// Values carried together: the sums of their deviations from a reference p and
+// of the squares of these, in fp64. p is the mean of the first values, so what
+// is summed is small whatever the mean is, and no step multiplies by 0 or
+// divides.
+struct Carry {
+  float p;
+  double s, sq;
+  // n values with their sum, their mean m (rounded) and squared deviations q from m
+  __device__ void add(bool first, double sum, float m, float q, double n) {
+    if (first) p = m;
+    const double e = (double)m - p, t = __builtin_fma(-n, (double)p, sum);
+    s += t;
+    sq += __builtin_fma(e, __builtin_fma(-n, e, 2.0 * t), (double)q);
+  }
+  __device__ Part part(double n) const {
+    const double mean = p + s / n;
+    const float m = (float)mean;
+    const double e = (double)m - p;
+    return Part{m, (float)(mean - m), (float)__builtin_fma(-e, __builtin_fma(-n, e, 2.0 * s), sq)};
+  }
+};
 
 // sum, mean (rounded) and sum of squared deviations of the UW values of every
 // unit of an octet over the first `rows` of R rows
@@ -352,9 +365,9 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
 // ---------------------------------------------------------------------------
 // forward, streaming
 // ---------------------------------------------------------------------------
-// Partial statistics: one read of x. A thread joins batches of pixels of its
-// octet, then a tree in LDS joins the threads of a column, so a chunk leaves
-// one entry a unit. Bound by reading x: 160 x 160 x 32 x 128 92 us (4.6 TB/s);
+// Partial statistics: one read of x. A thread carries batches of pixels of its
+// octet in fp64 sums, then a tree in LDS joins the threads of a column, so a
+// chunk leaves one entry a unit. Bound by reading x: 160 x 160 x 32 x 128 92 us (4.6 TB/s);
 // 80 x 80 x 16 x 64 9.0 us, mostly the first loads' latency.
 template <int UW, bool FULL>
 __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
@@ -368,10 +381,10 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
   const Oct t = octet(g, o, active);
   const long long stride = (long long)g.N * g.C;
   const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;  // pixels p0, p0 + dp, ...
-  double sum[UN];
-  float mean[UN], m2[UN], have = 0.0f;
+  Carry sum[UN];
+  double have = 0;
 #pragma unroll
-  for (int u = 0; u < UN; u++) sum[u] = mean[u] = m2[u] = 0.0f;
+  for (int u = 0; u < UN; u++) sum[u] = Carry{0.0f, 0.0, 0.0};
   if (active) {
     const float* src = a.x + t.col;
     // (the next pixels are requested before the current ones are summed)
@@ -394,19 +407,16 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
         for (int i = 0; i < 8; i++) v[k][i] = next[k][i];
       load(p + kBatch * dp);
       unit_stats<kBatch, UW>(v, rows, bs, bm, bq);
-      const float n = (float)(rows * UW);
+      const double n = (double)(rows * UW);
 #pragma unroll
-      for (int u = 0; u < UN; u++) {
-        sum[u] += bs[u];
-        join(mean[u], m2[u], have, bm[u], bq[u], n);
-      }
+      for (int u = 0; u < UN; u++) sum[u].add(p == p0, bs[u], bm[u], bq[u], n);
       have += n;
     }
   }
   const int W = g.tx * UN;
   if (py < g.ty)
 #pragma unroll
-    for (int u = 0; u < UN; u++) su[py * W + ox * UN + u] = part_of(sum[u], (double)have, mean[u], m2[u]);
+    for (int u = 0; u < UN; u++) su[py * W + ox * UN + u] = sum[u].part(have);
   __syncthreads();
   // units of the tile, joined over the rows of pixels
   const int NU = g.N * g.C / UW;

@@ -69,3 +69,50 @@ def test_calls_repeat_bit_for_bit_whatever_the_workspace_holds(shape):
         ref = ref or got
         for i, (a, b) in enumerate(zip(got, ref)):
             assert torch.equal(a, b), f"output {i} differs over a workspace of {fill:#x}"
+
+
+# one pass; streaming with whole octets, with partial ones, with a group of many workgroups
+RANGE_SHAPES = [(16, 16, 4, 32, 8), (13, 7, 3, 24, 3), (64, 64, 4, 64, 16), (57, 61, 17, 33, 11), (33, 31, 2, 2048, 1)]
+
+
+def _constant_groups(shape, values):
+    """Every sample and group holds one value, and what they hold differs."""
+    h, w, n, c, g = shape
+    v = np.resize(np.asarray(values, np.float32), (n, g))
+    return np.broadcast_to(np.repeat(v, c // g, axis=1), (h, w, n, c)).copy(), v
+
+
+def _equal_to_beta(y, beta):
+    np.testing.assert_array_equal(host(y), np.broadcast_to(host(beta), tuple(y.shape)))
+
+
+@pytest.mark.parametrize("shape", RANGE_SHAPES, ids=str)
+def test_large_constant_groups_have_their_value_as_mean(shape):
+    """x - mean is 0, so y = beta, however large the value is (its square passes fp32's range from 1.85e19 on)."""
+    say(f"norm large constants {shape}")
+    _, _, gamma, beta = _random(shape, 3)
+    x, v = _constant_groups(shape, [2e19, -1e20, 1.8e19, 3e30])
+    y, mean, _ = _forward(shape, dev(x), gamma, beta, mq.ACT_NONE)
+    np.testing.assert_array_equal(host(mean), v)
+    _equal_to_beta(y, beta)
+    _, _, mean, rstd = _forward(shape, dev(x), gamma, beta, mq.ACT_NONE, mx=(0, 32))
+    np.testing.assert_array_equal(host(mean), v)
+    assert np.isfinite(host(rstd)).all()
+
+
+@pytest.mark.parametrize("shape", RANGE_SHAPES, ids=str)
+def test_deviations_beyond_the_squares_range_give_rstd_0(shape):
+    """Deviations from 1e20 to 2e20: their squares are infinite in fp32, rstd is 0 and y = beta; the gradient is 0."""
+    say(f"norm large deviations {shape}")
+    h, w, n, c, g = shape
+    _, dy, gamma, beta = _random(shape, 4)
+    rng = np.random.default_rng(4)
+    x = (rng.uniform(1e20, 2e20, (h, w, n, c)) * rng.choice([-1, 1], (h, w, n, c))).astype(np.float32)
+    ref = x.astype(np.float64).reshape(h * w, n, g, c // g).mean(axis=(0, 3))
+    y, mean, rstd = _forward(shape, dev(x), gamma, beta, mq.ACT_NONE)
+    # a mean of fp64 sums, rounded once
+    assert (np.abs(host(mean) - ref) <= E * np.abs(ref) + 2.0 ** -40 * 2e20).all()
+    assert (host(rstd) == 0).all()
+    _equal_to_beta(y, beta)
+    dx, dgamma, dbeta = _backward(shape, dy, dev(x), gamma, beta, mean, rstd, mq.ACT_NONE)
+    assert not host(dx).any() and not host(dgamma).any() and np.isfinite(host(dbeta)).all()
