@@ -208,7 +208,11 @@ struct Carry {
 template <int R, int UW>
 __device__ __forceinline__ void unit_stats(const float (&v)[R][8], int rows, double (&sum)[8 / UW],
                                            float (&mean)[8 / UW], float (&m2)[8 / UW]) {
-  const float inv = 1.0f / (float)(rows * UW);
+  // fp64: the sum of finite values may pass fp32's range, their mean does not
+  // (1 / n by one Newton step from fp32's, so that the mean of equal values is
+  // that value)
+  const double n = (double)(rows * UW), r = (double)(1.0f / (float)(rows * UW));
+  const double inv = r * __builtin_fma(-n, r, 2.0);
 #pragma unroll
   for (int u = 0; u < 8 / UW; u++) {
     double s = 0.0;
@@ -217,7 +221,7 @@ __device__ __forceinline__ void unit_stats(const float (&v)[R][8], int rows, dou
 #pragma unroll
       for (int i = 0; i < UW; i++) s += k < rows ? (double)v[k][u * UW + i] : 0.0;
     sum[u] = s;
-    const float m = (float)s * inv;
+    const float m = (float)(s * inv);
     float q = 0.0f;
 #pragma unroll
     for (int k = 0; k < R; k++)

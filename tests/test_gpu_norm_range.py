@@ -116,3 +116,15 @@ def test_deviations_beyond_the_squares_range_give_rstd_0(shape):
     _equal_to_beta(y, beta)
     dx, dgamma, dbeta = _backward(shape, dy, dev(x), gamma, beta, mean, rstd, mq.ACT_NONE)
     assert not host(dx).any() and not host(dgamma).any() and np.isfinite(host(dbeta)).all()
+
+
+@pytest.mark.parametrize("shape", [*RANGE_SHAPES, (6, 5, 3, 24, 3)], ids=str)
+def test_sums_beyond_fp32_of_values_within_it(shape):
+    """Groups of 3e38, whose sums of two values already pass fp32's range, and of 1e37, for sums of 64."""
+    say(f"norm largest constants {shape}")
+    _, _, gamma, beta = _random(shape, 5)
+    x, v = _constant_groups(shape, [3e38, 1e37, -3e38, 6e36])
+    y, mean, rstd = _forward(shape, dev(x), gamma, beta, mq.ACT_NONE)
+    np.testing.assert_array_equal(host(mean), v)
+    assert np.isfinite(host(rstd)).all()
+    _equal_to_beta(y, beta)
