@@ -166,34 +166,26 @@ __device__ __forceinline__ void affine(const NormArgs& a, const Oct& t, float (&
   load_optional<FULL>(a.gamma, t.c0, t.cnt, 1.0f, ga);
 }
 
-// Statistics of some values: a mean m + lo (m is its fp32 rounding) and the
-// sum q of squared deviations from m. With c values their sum is c (m + lo)
-// and the sum of their squares q + c m (m + 2 lo).
+// Statistics of some values: their mean m + lo (m is its fp32 rounding) and the
+// sum q of squared deviations from m.
 using Part = NormPart;
+// Sums of c values' deviations from a reference p, and of the squares of
+// these, in fp64. p is a mean of some of the values, so what is summed is as
+// small as their spread whatever their mean is, and nothing cancels in
+// sq - s^2 / c; no step multiplies by 0 or divides.
 struct Sums {
+  float p = 0;
   double s = 0, sq = 0;
-  __device__ void add(const Part& p, double c) {
-    s += c * ((double)p.m + p.lo);
-    sq += (double)p.q + c * p.m * ((double)p.m + 2.0 * p.lo);
-  }
-};
-__device__ __forceinline__ Part part_of(double sum, double n, float m, float q) {
-  return Part{m, (float)(sum / n - (double)m), q};
-}
-
-// Values carried together: the sums of their deviations from a reference p and
-// of the squares of these, in fp64. p is the mean of the first values, so what
-// is summed is small whatever the mean is, and no step multiplies by 0 or
-// divides.
-struct Carry {
-  float p;
-  double s, sq;
-  // n values with their sum, their mean m (rounded) and squared deviations q from m
-  __device__ void add(bool first, double sum, float m, float q, double n) {
-    if (first) p = m;
+  // n values of sum `sum`, rounded mean m and squared deviations q from m
+  __device__ void add(double sum, float m, float q, double n) {
     const double e = (double)m - p, t = __builtin_fma(-n, (double)p, sum);
     s += t;
     sq += __builtin_fma(e, __builtin_fma(-n, e, 2.0 * t), (double)q);
+  }
+  __device__ void add(const Part& a, double n) {
+    const double d = (double)a.m - p;
+    s += n * (d + a.lo);
+    sq += (double)a.q + n * d * (d + 2.0 * a.lo);
   }
   __device__ Part part(double n) const {
     const double mean = p + s / n;
@@ -237,10 +229,10 @@ __device__ __forceinline__ void unit_stats(const float (&v)[R][8], int rows, dou
 
 // mean and rstd of M values
 __device__ __forceinline__ float2 finish_stats(const Sums& t, double M, float eps) {
-  const double mean = t.s / M;
-  double var = t.sq / M - mean * mean;
+  const double d = t.s / M;
+  double var = t.sq / M - d * d;
   if (var < 0.0) var = 0.0;
-  return make_float2((float)mean, (float)(1.0 / sqrt(var + (double)eps)));
+  return make_float2((float)(t.p + d), (float)(1.0 / sqrt(var + (double)eps)));
 }
 
 __device__ __forceinline__ double group_sum(double v, int lanes) {  // aligned groups of lanes (a power of two)
@@ -309,7 +301,12 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
     float mean[UN], m2[UN];
     unit_stats<R, UW>(v, rows, sum, mean, m2);
 #pragma unroll
-    for (int u = 0; u < UN; u++) su[py * W + ox * UN + u] = part_of(sum[u], (double)(rows * UW), mean[u], m2[u]);
+    for (int u = 0; u < UN; u++) {
+      Sums one;
+      one.p = mean[u];
+      one.add(sum[u], mean[u], m2[u], (double)(rows * UW));
+      su[py * W + ox * UN + u] = one.part((double)(rows * UW));
+    }
   }
   __syncthreads();
   // segments (sample, group) of the slab: e units each, over ty1 rows
@@ -323,6 +320,7 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
       const int S = S0 + s, n = S / g.G, gr = S - n * g.G;
       const int pos = (n * g.NO - o0) * UN + gr * g.e;
       Sums sum;
+      sum.p = su[pos].m;
       for (int i = j; i < g.ty1 * g.e; i += lanes) {
         const int row = i / g.e;
         sum.add(su[row * W + pos + (i - row * g.e)], (double)(((g.P - row + g.ty1 - 1) / g.ty1) * UW));
@@ -385,10 +383,8 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
   const Oct t = octet(g, o, active);
   const long long stride = (long long)g.N * g.C;
   const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;  // pixels p0, p0 + dp, ...
-  Carry sum[UN];
+  Sums sum[UN];
   double have = 0;
-#pragma unroll
-  for (int u = 0; u < UN; u++) sum[u] = Carry{0.0f, 0.0, 0.0};
   if (active) {
     const float* src = a.x + t.col;
     // (the next pixels are requested before the current ones are summed)
@@ -413,7 +409,10 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
       unit_stats<kBatch, UW>(v, rows, bs, bm, bq);
       const double n = (double)(rows * UW);
 #pragma unroll
-      for (int u = 0; u < UN; u++) sum[u].add(p == p0, bs[u], bm[u], bq[u], n);
+      for (int u = 0; u < UN; u++) {
+        if (p == p0) sum[u].p = bm[u];
+        sum[u].add(bs[u], bm[u], bq[u], n);
+      }
       have += n;
     }
   }
@@ -435,6 +434,7 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
         const int rows = groups - (owns_last && last * g.ty + r >= g.P ? 1 : 0);
         if (rows == 0) return;
         Sums q;
+        q.p = su[i].m;  // (row 0 has pixels in every chunk)
         q.add(su[r * W + i], (double)rows * UW);
         s1 += q.s;
         s2 += q.sq;
@@ -444,8 +444,11 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
         if (oo >= g.TO) return;
         const Oct q = octet(g, oo, true);
         if (u * UW >= q.cnt) return;
-        const double m = s1 / c;
-        a.part[(long long)chunk * NU + (q.col / UW + u)] = part_of(s1, c, (float)m, (float)(s2 - m * s1));
+        Sums all;
+        all.p = su[i].m;
+        all.s = s1;
+        all.sq = s2;
+        a.part[(long long)chunk * NU + (q.col / UW + u)] = all.part(c);
       });
 }
 
@@ -469,6 +472,7 @@ __device__ __forceinline__ Sums segment_stats(const NormArgs& a, int S, int j, i
   const Part* part = a.part + (long long)S * g.e;
   constexpr int B = 8;
   Sums s;
+  s.p = part->m;  // of the segment's first unit and chunk, for every lane
   for (int i = j; i < n; i += B * lanes) {
     Part q[B];
     int k[B];
@@ -598,12 +602,13 @@ __global__ __launch_bounds__(kWideT) void norm_join_wide_kernel(const NormArgs a
   const int S = (int)blockIdx.x, t = (int)threadIdx.x;
   const ColIn in = column_in<BWD>(a, S, 1, t);
   double s1, s2;
+  Sums stats;
   if constexpr (BWD) {
     segment_sums(a, S, t, kWideT, s1, s2);
   } else {
-    const Sums s = segment_stats(a, S, t, kWideT);
-    s1 = s.s;
-    s2 = s.sq;
+    stats = segment_stats(a, S, t, kWideT);
+    s1 = stats.s;
+    s2 = stats.sq;
   }
   s1 = group_sum(s1, 64);
   s2 = group_sum(s2, 64);
@@ -621,10 +626,9 @@ __global__ __launch_bounds__(kWideT) void norm_join_wide_kernel(const NormArgs a
     if constexpr (BWD) {
       sseg[0] = grad_means(s1, s2, M, a.rstd_in[S]);
     } else {
-      Sums q;
-      q.s = s1;
-      q.sq = s2;
-      sseg[0] = finish_stats(q, M, a.eps);
+      stats.s = s1;
+      stats.sq = s2;
+      sseg[0] = finish_stats(stats, M, a.eps);
     }
   }
   __syncthreads();

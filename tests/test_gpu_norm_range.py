@@ -128,3 +128,33 @@ def test_sums_beyond_fp32_of_values_within_it(shape):
     np.testing.assert_array_equal(host(mean), v)
     assert np.isfinite(host(rstd)).all()
     _equal_to_beta(y, beta)
+
+
+@pytest.mark.parametrize("shape", [*RANGE_SHAPES, (6, 5, 3, 24, 3)], ids=str)
+def test_constant_groups_have_variance_0(shape):
+    """rstd is 1 / sqrt(eps), one rounding and one of a square root from it, whatever the value."""
+    say(f"norm rstd of constants {shape}")
+    _, _, gamma, beta = _random(shape, 6)
+    x, _ = _constant_groups(shape, [1e6, -3e37, 0.1, 1e20, 7e4])
+    _, _, rstd = _forward(shape, dev(x), gamma, beta, mq.ACT_NONE)
+    assert (np.abs(host(rstd) * np.sqrt(np.float64(np.float32(EPS))) - 1) <= 2 * E).all()
+
+
+@pytest.mark.parametrize("ratio", [1e4, 1e6, 5e6])
+@pytest.mark.parametrize("shape", RANGE_SHAPES, ids=str)
+def test_rstd_keeps_its_digits_at_any_mean(shape, ratio):
+    """Squared deviations are fp32 around a mean of at most b values (64 in one pass, 16 streaming): three roundings of each
+    and b additions; two roundings as partial results are kept, the rest in fp64. So the variance is within (b + 4) 2^-24, and
+    rstd within half of that and a rounding. The values are taken as they are in fp32, with the mean's rounding."""
+    say(f"norm far means {shape} {ratio}")
+    h, w, n, c, g = shape
+    _, _, gamma, beta = _random(shape, 7)
+    rng = np.random.default_rng(7)
+    far = np.repeat(ratio * rng.uniform(1, 3, (n, g)) * rng.choice([-1, 1], (n, g)), c // g, axis=1)
+    x = (rng.standard_normal((h, w, n, c)) + far).astype(np.float32)
+    mean, rstd = block.stats(x, g, np.float64(np.float32(EPS)))
+    got = _forward(shape, dev(x), gamma, beta, mq.ACT_NONE)
+    assert (np.abs(host(got[1]) - mean) <= E * np.abs(mean)).all()
+    b = 64 if shape in RANGE_SHAPES[:2] else 16
+    err = np.abs(host(got[2]) / rstd - 1)
+    assert (err <= ((b + 4) / 2 + 1) * E).all(), f"{err.max():.2e}"
