@@ -69,8 +69,10 @@ int mqconv_dropout_mx(const float* x, const mq_drop* drop, mq_mx dst, void* stre
  * gamma, beta: fp32 [C], NULL for 1 and 0. mean, rstd: fp32 [N][groups],
  * written by the forward pass (NULL: not kept) and read by the backward.
  * drop: NULL for none. Values are summed in fp64, squared deviations in fp32
- * around local means and joined in fp64, so deviations of 1.8e19 and more
- * overflow (rstd is 0 then), and those below 1e-19 count as none.
+ * around the mean of at most 64 values and joined in fp64 around a mean, so
+ * rstd has fp32's accuracy whatever the mean is. Deviations of 1.8e19 and more
+ * overflow (rstd is 0 then), from 2.3e18 on they may, and the squares of those
+ * below 1e-19 lose digits.
  *   Backward, from dy (gradient of y) and the forward's x, mean, rstd:
  *   g = drop(dy) * act'(u);  xh = (x - mean) * rstd
  *   dbeta[c] = sum g;  dgamma[c] = sum g * xh          (over H, W, N)

@@ -167,7 +167,8 @@ __device__ __forceinline__ void affine(const NormArgs& a, const Oct& t, float (&
 }
 
 // Statistics of some values: their mean m + lo (m is its fp32 rounding) and the
-// sum q of squared deviations from m.
+// mean q of squared deviations from m (a mean, which stays in fp32's range
+// however many values there are).
 using Part = NormPart;
 // Sums of c values' deviations from a reference p, and of the squares of
 // these, in fp64. p is a mean of some of the values, so what is summed is as
@@ -185,13 +186,13 @@ struct Sums {
   __device__ void add(const Part& a, double n) {
     const double d = (double)a.m - p;
     s += n * (d + a.lo);
-    sq += (double)a.q + n * d * (d + 2.0 * a.lo);
+    sq += n * ((double)a.q + d * (d + 2.0 * a.lo));
   }
   __device__ Part part(double n) const {
-    const double mean = p + s / n;
+    const double inv = 1.0 / n, d = s * inv, mean = p + d;
     const float m = (float)mean;
     const double e = (double)m - p;
-    return Part{m, (float)(mean - m), (float)__builtin_fma(-e, __builtin_fma(-n, e, 2.0 * s), sq)};
+    return Part{m, (float)(mean - m), (float)(sq * inv - e * (2.0 * d - e))};
   }
 };
 

@@ -158,3 +158,25 @@ def test_rstd_keeps_its_digits_at_any_mean(shape, ratio):
     b = 64 if shape in RANGE_SHAPES[:2] else 16
     err = np.abs(host(got[2]) / rstd - 1)
     assert (err <= ((b + 4) / 2 + 1) * E).all(), f"{err.max():.2e}"
+
+
+@pytest.mark.parametrize("scale", [1e18, 1e-17])
+@pytest.mark.parametrize("shape", [*RANGE_SHAPES, (160, 160, 1, 32, 2)], ids=str)
+def test_rstd_of_large_and_small_deviations_whatever_their_number(shape, scale):
+    """Squares of 1e36 and 1e-34, whose sums over a group pass fp32's range where they are large: rstd within the bound above
+    (eps is 0 for the small ones)."""
+    say(f"norm scaled deviations {shape} {scale}")
+    h, w, n, c, g = shape
+    rng = np.random.default_rng(8)
+    x = (scale * rng.uniform(0.5, 1, (h, w, n, c)) * rng.choice([-1, 1], (h, w, n, c))).astype(np.float32)
+    eps = 0.0 if scale < 1 else EPS
+    gn = mq.mq_norm(h, w, n, c, g, mq.ACT_NONE, eps)
+    y, m, r = torch.empty((h, w, n, c), device="cuda"), torch.empty((n, g), device="cuda"), torch.empty((n, g), device="cuda")
+    ws = torch.empty(mq.mqconv_group_norm_workspace_bytes(gn, mq.NORM_FWD), dtype=torch.uint8, device="cuda")
+    mq.mqconv_group_norm(gn, dev(x), None, None, y, m, r, ws)
+    mean, rstd = block.stats(x, g, eps)
+    err = np.abs(host(r) / rstd - 1)
+    assert (err <= ((64 + 4) / 2 + 1) * E).all(), f"{err.max():.2e}"
+    ref = (x - np.repeat(mean, c // g, axis=1)) * np.repeat(rstd, c // g, axis=1)
+    # rstd as above, x - mean from a mean rounded to fp32, one rounding of each operation
+    assert (np.abs(host(y) - ref) <= 64 * E * np.abs(ref) + 4 * E).all()
