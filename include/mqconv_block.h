@@ -77,7 +77,8 @@ int mqconv_dropout_mx(const float* x, const mq_drop* drop, mq_mx dst, void* stre
  *   g = drop(dy) * act'(u);  xh = (x - mean) * rstd
  *   dbeta[c] = sum g;  dgamma[c] = sum g * xh          (over H, W, N)
  *   dx = rstd * (gamma g - mean_M(gamma g) - xh * mean_M(gamma g xh))
- * act'(0) is 0 for MQ_ACT_RELU. dgamma, dbeta may be NULL. */
+ * act'(0) is 0 for MQ_ACT_RELU. dgamma, dbeta may be NULL. Sums over pixels
+ * and samples are fp64, their partial results kept in fp32. */
 typedef struct {
   int32_t h, w, n, c; /* all >= 1 */
   int32_t groups;     /* divides c, else MQ_ERR_SHAPE */

@@ -887,9 +887,9 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
   const Oct t = octet(g, o, active);
   const long long stride = (long long)g.N * g.C;
   const int p0 = chunk * g.ty + py, dp = g.nchunk * g.ty;
-  float s1[8], s2[8];
+  double s1[8], s2[8];  // (a thread's pixels are thousands where there are many columns)
 #pragma unroll
-  for (int i = 0; i < 8; i++) s1[i] = s2[i] = 0.0f;
+  for (int i = 0; i < 8; i++) s1[i] = s2[i] = 0;
   if (active) {
     constexpr int B = kBatch / 2;  // two tensors
     float nd[B][8], ng[B][8];
@@ -924,7 +924,7 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
           s1[i] += gr[k][i];
-          s2[i] = __builtin_fmaf(gr[k][i], d[k][i], s2[i]);
+          s2[i] = __builtin_fma((double)gr[k][i], (double)d[k][i], s2[i]);
         }
       }
     }
@@ -934,7 +934,7 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
   const int W = g.tx * 8;
   if (py < g.ty)
 #pragma unroll
-    for (int i = 0; i < 8; i++) su[py * W + ox * 8 + i] = make_float2(s1[i], s2[i]);
+    for (int i = 0; i < 8; i++) su[py * W + ox * 8 + i] = make_float2((float)s1[i], (float)s2[i]);
   __syncthreads();
   const long long NC = stride;
   __shared__ double x1[256], x2[256];

@@ -180,3 +180,29 @@ def test_rstd_of_large_and_small_deviations_whatever_their_number(shape, scale):
     ref = (x - np.repeat(mean, c // g, axis=1)) * np.repeat(rstd, c // g, axis=1)
     # rstd as above, x - mean from a mean rounded to fp32, one rounding of each operation
     assert (np.abs(host(y) - ref) <= 64 * E * np.abs(ref) + 4 * E).all()
+
+
+@pytest.mark.parametrize("shape", [(160, 160, 8, 256, 32), (64, 64, 128, 512, 64)], ids=str)
+def test_long_sums_of_the_gradient(shape):
+    """Equal terms in every pixel and sample, whose roundings do not cancel: 100 and 256 of them in a thread. dbeta's terms are
+    exact, and a thread's, a chunk's and the whole sum are rounded once each; dgamma's have the rounding of x - mean too."""
+    say(f"norm gradient's long sums {shape}")
+    h, w, n, c, g = shape
+    rng = np.random.default_rng(9)
+    xc, gc = rng.standard_normal(c).astype(np.float32), rng.uniform(0.1, 1, c).astype(np.float32)
+    x, dy = (dev(v).expand(h, w, n, c).contiguous() for v in (xc, gc))
+    _, mean, rstd = _forward(shape, x, None, None, mq.ACT_NONE)
+    dx, dgamma, dbeta = _backward(shape, dy, x, None, None, mean, rstd, mq.ACT_NONE)
+    m, r = (np.repeat(host(v)[0].astype(np.float64), c // g) for v in (mean, rstd))
+    ref_b = gc.astype(np.float64) * (h * w * n)
+    ref_g = ref_b * (xc - m) * r
+    eb, eg = (np.abs(host(a) / b - 1).max() for a, b in ((dbeta, ref_b), (dgamma, ref_g)))
+    say(f"  dbeta {eb / E:.2f}, dgamma {eg / E:.2f} units of 2^-24")
+    assert eb <= 3 * E and eg <= 5 * E
+    # dx = r (g - mean g - xh mean(g xh)) with the group's means: six roundings of terms of these sizes
+    xh = (xc - m) * r
+    fold = lambda v: np.repeat(v.reshape(g, -1).mean(axis=1), c // g)  # noqa: E731
+    a, b = fold(gc), fold(gc * xh)
+    ref = r * (gc - a - xh * b)
+    got = host(dx.view(h * w, n, c)[[0, h * w // 2, h * w - 1]])
+    assert (np.abs(got - ref) <= 16 * E * r * (gc + a + np.abs(xh) * fold(gc * np.abs(xh)))).all()
