@@ -12,8 +12,8 @@
 
 namespace mq {
 
-// Kernels are built for each activation: GELU's erf costs registers that the
-// others need for values in flight.
+// Kernels are built for each activation: GELU's integral costs registers that
+// the others need for values in flight.
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 template <int A>
 struct ActTag {
@@ -85,9 +85,31 @@ __device__ __forceinline__ void store_run(float* p, int cnt, const float (&v)[K]
 // as long as the rest. Overflow to infinity makes a sigmoid 0, as it should.
 __device__ __forceinline__ float exp_neg(float u) { return __builtin_amdgcn_exp2f(u * -1.4426950408889634f); }
 __device__ __forceinline__ float sigmoid(float u) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(u)); }
-__device__ __forceinline__ float normal_cdf(float u) {
+// The normal distribution: e = exp(-u^2 / 2) and the integral cdf up to u. The
+// tail is e t P(t) with t = 1 / (1 + 0.38 |u|) and P of degree 9, fitted to the
+// smallest largest relative error over |u| <= 14 (9e-9; 4.5 2^-24 as evaluated
+// here), so below 0 cdf keeps its digits, which 1 + erf loses, but for the
+// rounding of e's argument: u^2 2^-24 times 1.3 of the result. One exponential
+// for both. Group norm of 160 x 160 x 32 x 128 245 us, 299 by a call of erfc.
+struct Normal {
+  float e, cdf;
+};
+__device__ __forceinline__ Normal normal(float u) {
 #pragma clang fp contract(off)
-  return 0.5f * (1.0f + erff(u * 0.70710678f));
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.38f, fabsf(u), 1.0f));
+  float p = 0.0242854198f;
+  p = __builtin_fmaf(p, t, -0.149213825f);
+  p = __builtin_fmaf(p, t, 0.368569631f);
+  p = __builtin_fmaf(p, t, -0.434484348f);
+  p = __builtin_fmaf(p, t, 0.210207231f);
+  p = __builtin_fmaf(p, t, -0.0559188846f);
+  p = __builtin_fmaf(p, t, 0.106472857f);
+  p = __builtin_fmaf(p, t, 0.126635639f);
+  p = __builtin_fmaf(p, t, 0.151857647f);
+  p = __builtin_fmaf(p, t, 0.151588629f);
+  const float e = __builtin_amdgcn_exp2f(u * u * -0.72134752f);
+  const float tail = e * (t * p);
+  return Normal{e, u > 0.0f ? 1.0f - tail : tail};
 }
 
 // The activation of every value of u, in place.
@@ -102,7 +124,7 @@ __device__ __forceinline__ void act_values(float (&u)[K]) {
     for (int i = 0; i < K; i++) u[i] = u[i] < 0.0f ? 0.0f : u[i];
   } else if constexpr (ACT == kActGelu) {
 #pragma unroll
-    for (int i = 0; i < K; i++) u[i] = u[i] * normal_cdf(u[i]);
+    for (int i = 0; i < K; i++) u[i] = u[i] * normal(u[i]).cdf;
   }
 }
 // g *= act'(u).
@@ -121,8 +143,10 @@ __device__ __forceinline__ void act_slopes(const float (&u)[K], float (&g)[K]) {
     for (int i = 0; i < K; i++) g[i] = u[i] != u[i] ? u[i] : g[i] * (u[i] > 0.0f ? 1.0f : 0.0f);
   } else if constexpr (ACT == kActGelu) {
 #pragma unroll
-    for (int i = 0; i < K; i++)
-      g[i] = g[i] * __builtin_fmaf(u[i] * 0.39894228f, exp_neg(0.5f * u[i] * u[i]), normal_cdf(u[i]));
+    for (int i = 0; i < K; i++) {
+      const Normal d = normal(u[i]);
+      g[i] = g[i] * __builtin_fmaf(u[i] * 0.39894228f, d.e, d.cdf);
+    }
   }
 }
 

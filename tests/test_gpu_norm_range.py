@@ -1,6 +1,8 @@
 """Group norm where its numbers are hard on fp32: repeated calls over
 workspaces that hold anything, very large values, means far from zero and
 long sums, at sizes of the one-pass kernels and of the streaming ones."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -206,3 +208,36 @@ def test_long_sums_of_the_gradient(shape):
     ref = r * (gc - a - xh * b)
     got = host(dx.view(h * w, n, c)[[0, h * w // 2, h * w - 1]])
     assert (np.abs(got - ref) <= 16 * E * r * (gc + a + np.abs(xh) * fold(gc * np.abs(xh)))).all()
+
+
+@pytest.mark.parametrize("hwn", [(1, 1, 1), (64, 64, 2)], ids=str)
+def test_gelu_keeps_its_digits_in_the_tail(hwn):
+    """With gamma 0 u is beta exactly: y = u cdf(u), and with dy = 1 dbeta = h w n (cdf(u) + u phi(u)). The argument's rounding
+    and its constant's are 1.3 2^-24 of it, (u^2 + 1) times that of cdf; erfc's own error is a few units; phi's argument has three
+    roundings of u^2 / 2. Below -12.5 the results are subnormal."""
+    h, w, n = hwn
+    c = 2048
+    u = np.linspace(-12.5, 8, c).astype(np.float32)
+    say(f"gelu tail {hwn}")
+    shape = (h, w, n, c, 16)
+    x, _, _, _ = _random(shape, 10)
+    gamma, beta = torch.zeros(c, device="cuda"), dev(u)
+    y, mean, rstd = _forward(shape, x, gamma, beta, mq.ACT_GELU)
+    v = u.astype(np.float64)
+    cdf = np.array([0.5 * math.erfc(-t * math.sqrt(0.5)) for t in v])
+    phi = np.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    bound = (1.5 * (v * v + 1) + 16) * E
+    got = host(y).reshape(-1, c)
+    assert (got == got[0]).all()
+    err = np.abs(got[0] - v * cdf) / np.maximum(np.abs(v * cdf), 1e-300)
+    assert (err <= bound).all(), f"u = {v[np.argmax(err / bound)]}: {err[np.argmax(err / bound)]:.2e}"
+    # 32 values of the tail as a block of their own: its scale is that of the true values
+    q = _forward(shape, x, gamma, beta, mq.ACT_GELU, mx=(1, 1))
+    scales = host(q[1]).reshape(-1, c // 32)
+    top = np.abs((v * cdf).reshape(-1, 32)).max(axis=1)
+    clear = np.abs(np.log2(top) - np.round(np.log2(top))) > 1e-3
+    assert (scales[:, clear] == (np.floor(np.log2(top)) + 127 - 15).clip(0)[clear]).all()
+    dbeta = host(_backward(shape, torch.ones_like(x), x, gamma, beta, mean, rstd, mq.ACT_GELU)[2]) / (h * w * n)
+    tol = bound * cdf + (2 * v * v + 16) * E * np.abs(v) * phi
+    bad = np.abs(dbeta - (cdf + v * phi)) > tol
+    assert not bad.any(), f"u = {v[bad][0]}: {dbeta[bad][0]} for {(cdf + v * phi)[bad][0]}"
