@@ -241,3 +241,25 @@ def test_gelu_keeps_its_digits_in_the_tail(hwn):
     tol = bound * cdf + (2 * v * v + 16) * E * np.abs(v) * phi
     bad = np.abs(dbeta - (cdf + v * phi)) > tol
     assert not bad.any(), f"u = {v[bad][0]}: {dbeta[bad][0]} for {(cdf + v * phi)[bad][0]}"
+
+
+def test_silu_keeps_its_digits_in_the_tail():
+    """u = beta as above: y = u s(u), dbeta = s (1 + u (1 - s)). exp's argument has a relative rounding of 2^-24 and its
+    constant's, the rest a few units; from -88 on the results are tiny or 0."""
+    c = 2048
+    u = np.linspace(-86, 20, c).astype(np.float32)
+    u[:4] = -89, -104, -1e5, -3e38
+    say("silu tail")
+    shape = (1, 1, 1, c, 16)
+    x, _, _, _ = _random(shape, 11)
+    gamma, beta = torch.zeros(c, device="cuda"), dev(u)
+    y, mean, rstd = _forward(shape, x, gamma, beta, mq.ACT_SILU)
+    dbeta = host(_backward(shape, torch.ones_like(x), x, gamma, beta, mean, rstd, mq.ACT_SILU)[2])
+    y = host(y).reshape(-1)
+    assert (np.abs(y[:4]) <= 1e-36).all() and (np.abs(dbeta[:4]) <= 1e-36).all()
+    v, y, dbeta = u[4:].astype(np.float64), y[4:], dbeta[4:]
+    s = 1 / (1 + np.exp(-v))
+    bound = (1.5 * np.abs(v) + 8) * E
+    assert (np.abs(y - v * s) <= bound * np.abs(v * s)).all()
+    # 1 - s and 1 + u (1 - s) have roundings of 1 and of u
+    assert (np.abs(dbeta - (s + v * s * (1 - s))) <= bound * (s + np.abs(v) * s * (1 - s)) + 4 * E * np.abs(v) * s).all()
