@@ -320,7 +320,7 @@ struct CacheSrc {
       for (int j = 0; j < 4; j++) v[4 * i + j] = FULL || 4 * i + j < cnt ? q[j] : 0.0f;
     }
   }
-  __device__ void extra(int) const {}
+  __device__ void extra(int, int) const {}
 };
 
 namespace {

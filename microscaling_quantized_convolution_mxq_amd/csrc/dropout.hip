@@ -94,7 +94,7 @@ struct DropSrc {
     for (int i = 0; i < 16; i++) v[i] = r.x[i];
     drop_values<16>(d, s.key, (uint32_t)p * N + n, c0, v);
   }
-  __device__ void extra(int) const {}
+  __device__ void extra(int, int) const {}
 };
 
 hipError_t launch_dropout_mx(const float* x, int P, int N, int C, const DropSpec& drop, const MxOutView& out,

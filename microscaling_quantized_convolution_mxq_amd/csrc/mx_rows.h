@@ -65,8 +65,8 @@ inline MxRows mx_rows(const MxOutView& out, int P, int N, int C) {
 // and its parameters, by params(state, n, c0, cnt), where cnt (0 to 16) of
 // the channels c0 .. exist and the first tile is on its way; Raw (what a lane
 // reads of a pixel) by load(state, raw, p, n, c0, cnt); the 16 values, zeros
-// past cnt, by values(state, raw, p, n, c0, x); extra(b) runs in workgroups
-// of its own.
+// past cnt, by values(state, raw, p, n, c0, x); extra(b, n) runs in n
+// workgroups of its own.
 // p, n and c0 are in range on every lane (a lane without a row or channels
 // gets those of another, with cnt 0, and its values are left out).
 template <int F, class Src>
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(const Src src,
   constexpr int RB = run_bytes_of(F);
   __shared__ __attribute__((aligned(16))) uint8_t stage[2][kRowsWaves * 32 * RB];
   if ((int)blockIdx.x < g.extra) {  // the source's own work
-    src.extra((int)blockIdx.x);
+    src.extra((int)blockIdx.x, g.extra);
     return;
   }
   // neighbouring workgroups: neighbouring rows and channels of a pixel

@@ -100,18 +100,22 @@ __device__ __forceinline__ void sum_rows(const float2* rows, int C, int c0, int 
     }
 }
 
-// dgamma and dbeta of channels kSumC b ..: eight channels a workgroup, so that
-// its threads share the samples' and chunks' rows between them (a thread a
-// channel had been the tail of the whole gradient).
-constexpr int kSumC = 8;
+// dgamma and dbeta by workgroup b of n: eight channels at a time, so that its
+// threads share the samples' and chunks' rows between them (a thread a channel
+// had been the tail of the whole gradient). At most kSumGroups workgroups: one
+// for every eight of 2^27 channels would be more threads than a launch takes.
+constexpr int kSumC = 8, kSumGroups = 1 << 16;
 constexpr int kFoldRows = 64, kFoldFrom = 1024;  // more rows than kFoldFrom are first summed to kFoldRows
-__device__ __forceinline__ void norm_channel_sums(const NormArgs& a, int b) {
-  double s1, s2;
-  sum_rows<kSumC>(a.sum_src, a.g.C, b * kSumC, 0, a.sum_rows, s1, s2);
-  const int c = b * kSumC + (int)threadIdx.x;
-  if (threadIdx.x < kSumC && c < a.g.C) {
-    if (a.dbeta) a.dbeta[c] = (float)s1;
-    if (a.dgamma) a.dgamma[c] = (float)s2;
+__device__ __forceinline__ void norm_channel_sums(const NormArgs& a, int b, int n) {
+  for (int c0 = b * kSumC; c0 < a.g.C; c0 += n * kSumC) {
+    if (c0 != b * kSumC) __syncthreads();  // (the sums before are read)
+    double s1, s2;
+    sum_rows<kSumC>(a.sum_src, a.g.C, c0, 0, a.sum_rows, s1, s2);
+    const int c = c0 + (int)threadIdx.x;
+    if (threadIdx.x < kSumC && c < a.g.C) {
+      if (a.dbeta) a.dbeta[c] = (float)s1;
+      if (a.dgamma) a.dgamma[c] = (float)s2;
+    }
   }
 }
 

@@ -871,7 +871,9 @@ __global__ __launch_bounds__(256) void norm_fold_kernel(const NormArgs a) {
 }
 
 // dgamma and dbeta behind the one-pass kernel
-__global__ __launch_bounds__(256) void norm_channel_kernel(const NormArgs a) { norm_channel_sums(a, blockIdx.x); }
+__global__ __launch_bounds__(256) void norm_channel_kernel(const NormArgs a) {
+  norm_channel_sums(a, (int)blockIdx.x, (int)gridDim.x);
+}
 
 // Every column's sums of g and g xh over a chunk of pixels: one read of x and
 // dy. Columns, not groups, because dgamma and dbeta need them. Bound by
@@ -961,7 +963,7 @@ template <bool FULL, int ACT>
 __global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs a, int extra) {
   const NormGeo& g = a.g;
   if ((int)blockIdx.x < extra) {
-    norm_channel_sums(a, (int)blockIdx.x);
+    norm_channel_sums(a, (int)blockIdx.x, extra);
     return;
   }
   const int id = (int)blockIdx.x - extra;
@@ -1194,7 +1196,7 @@ hipError_t launch_group_norm_backward(const NormShape& s, const float* dy, const
   bind_ws(a, ws, true);
   const NormGeo& g = a.g;
   const bool full = g.C % 8 == 0;
-  const int extra = dgamma || dbeta ? ceil_div(g.C, kSumC) : 0;
+  const int extra = dgamma || dbeta ? std::min(ceil_div(g.C, kSumC), kSumGroups) : 0;
   if (full) launch_sums<true>(a, st);
   else launch_sums<false>(a, st);
   hipError_t e = launch_check();

@@ -44,7 +44,7 @@ struct NormSrc {
     act_values<ACT, 16>(v);
     drop_values<16>(a.drop, s.key, (uint32_t)p * a.g.N + n, c0, v);
   }
-  __device__ void extra(int) const {}
+  __device__ void extra(int, int) const {}
 };
 
 template <bool FULL, int ACT>
@@ -88,7 +88,7 @@ struct NormGradSrc {
     act_slopes<ACT, 16>(u, g);
     norm_grad_values<16>(s.a, s.k1, s.k2, d, g, v);
   }
-  __device__ void extra(int b) const { norm_channel_sums(a, b); }
+  __device__ void extra(int b, int n) const { norm_channel_sums(a, b, n); }
 };
 
 namespace {

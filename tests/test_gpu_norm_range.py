@@ -263,3 +263,30 @@ def test_silu_keeps_its_digits_in_the_tail():
     assert (np.abs(y - v * s) <= bound * np.abs(v * s)).all()
     # 1 - s and 1 + u (1 - s) have roundings of 1 and of u
     assert (np.abs(dbeta - (s + v * s * (1 - s))) <= bound * (s + np.abs(v) * s * (1 - s)) + 4 * E * np.abs(v) * s).all()
+
+
+def test_gradient_of_more_than_2_to_the_27_channels():
+    """One pixel of one sample: dbeta is dy, dgamma dy xh with a rounding of x - mean, of a partial sum and of the result. Eight
+    channels a workgroup would be more threads than a launch takes."""
+    c, d = 2**27 + 96, 32
+    shape = (1, 1, 1, c, c // d)
+    say(f"norm gradient of {c} channels")
+    x, dy, gamma, beta = _random((1, 1, 1, c, 1), 12)
+    _, mean, rstd = _forward(shape, x, gamma, beta, mq.ACT_NONE)
+    dx, dgamma, dbeta = _backward(shape, dy, x, gamma, beta, mean, rstd, mq.ACT_NONE)
+    codes, scales, dgamma2, dbeta2 = _backward(shape, dy, x, gamma, beta, mean, rstd, mq.ACT_NONE, mx=(1, 32))
+    assert torch.equal(dgamma, dgamma2) and torch.equal(dbeta, dbeta2) and torch.equal(dbeta, dy.view(-1))
+    ref = mq.MxTensor.empty(mq.ROLE_GRAD, 1, 32, shape[:4])
+    mq.mqconv_quantize(dx, ref)
+    assert torch.equal(codes, ref.codes) and torch.equal(scales, ref.scales)
+    for part in (slice(0, 2**20), slice(c - 2**20, c)):
+        m, r = (v.view(-1).repeat_interleave(d)[part].double() for v in (mean, rstd))
+        want = dy.view(-1)[part].double() * (x.view(-1)[part].double() - m) * r
+        assert bool(((dgamma[part] - want).abs() <= 4 * E * want.abs()).all())
+    seg = slice(c - 2**20, c)
+    xg, gg = x.view(-1)[seg].double().view(-1, d), (dy.view(-1) * gamma)[seg].double().view(-1, d)
+    m, r = mean.view(-1, 1)[-(2**20) // d:].double(), rstd.view(-1, 1)[-(2**20) // d:].double()
+    xh = (xg - m) * r
+    want = r * (gg - gg.mean(1, keepdim=True) - xh * (gg * xh).mean(1, keepdim=True))
+    size = r * (gg.abs() + gg.abs().mean(1, keepdim=True) + xh.abs() * (gg * xh).abs().mean(1, keepdim=True))
+    assert bool(((dx.view(-1)[seg].view(-1, d) - want).abs() <= 16 * E * size).all())
