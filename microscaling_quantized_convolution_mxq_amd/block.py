@@ -210,6 +210,12 @@ def _slots(slot, count: int) -> Optional[int]:
     return _mq._buf(slot, 4 * count, "int32", "slot")
 
 
+def _count(slot) -> int:
+    if not hasattr(slot, "numel"):
+        raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, "slot", "a tensor gives the number of samples")
+    return slot.numel()
+
+
 def _batch(x, c: MxCache, what: str):
     """Samples of an [H][W][N][C] tensor that goes into or comes from the cache."""
     h, w, n, ch = _dims(x, what)
@@ -221,7 +227,7 @@ def _batch(x, c: MxCache, what: str):
 def mqconv_cache_write(cache: MxCache, x, slot, n0: int = 0, stream=None) -> None:
     """Stores samples n0 .. of x [H][W][N][C], one for each entry of `slot` (int32), in these slots."""
     n, p = _batch(x, cache, "x")
-    count = slot.numel()
+    count = _count(slot)
     _mq._check(_lib().mqconv_cache_write(cache.c_struct(), p, n, n0, count, _slots(slot, count), _mq._stream(stream)),
                "mqconv_cache_write")
 
@@ -229,7 +235,7 @@ def mqconv_cache_write(cache: MxCache, x, slot, n0: int = 0, stream=None) -> Non
 def mqconv_cache_read(cache: MxCache, slot, x, n0: int = 0, stream=None) -> None:
     """Writes the values of the slots to samples n0 .. of x [H][W][N][C]."""
     n, p = _batch(x, cache, "x")
-    count = slot.numel()
+    count = _count(slot)
     _mq._check(_lib().mqconv_cache_read(cache.c_struct(), _slots(slot, count), count, p, n, n0, _mq._stream(stream)),
                "mqconv_cache_read")
 

@@ -196,6 +196,28 @@ def test_binding_checks_tensors():
     assert "gamma" in reason(FAKE, z(7))
 
 
+def test_cache_calls_refuse_slots_that_are_no_tensor():
+    """An address does not say how many samples there are."""
+    cache = mq.MxCache(FAKE, FAKE, 0, 4, 2, 3, 40)
+    import torch
+    for slot in (FAKE, None, [0, 1]):
+        assert _status(mq.mqconv_cache_write, cache, FakeBatch((2, 3, 5, 40)), slot) == SHAPE
+        assert _status(mq.mqconv_cache_read, cache, slot, FakeBatch((2, 3, 5, 40))) == SHAPE
+    none = torch.zeros(0, dtype=torch.int32)  # no samples
+    assert _status(mq.mqconv_cache_write, cache, FakeBatch((2, 3, 5, 40)), none) == SHAPE
+
+
+class FakeBatch(FakeWorkspace):
+    """An fp32 tensor as the binding sees one, at an address that is never used."""
+
+    def __init__(self, shape):
+        super().__init__(4)
+        import torch
+        self.shape, self.dtype = shape, torch.float32
+        for d in shape:
+            self.nbytes *= d
+
+
 def test_refusals_and_plans_under_host_sanitizers():
     if os.environ.get("MQCONV_LIB"):
         pytest.skip("already under the sanitizers")
