@@ -16,6 +16,14 @@ NORM_FWD, NORM_BWD = 0, 1
 CACHE_COUNT_MAX = 4096
 
 
+def _int32(what: str, *values: int):
+    """Values of the library's 32-bit arguments: ctypes would pass the low bits of larger ones on."""
+    for v in values:
+        if not -2**31 <= v < 2**31:
+            raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, what, f"{v} does not fit 32 bits")
+    return values
+
+
 class mq_drop(ctypes.Structure):
     """Dropout with probability p. `step`: None, or a one-element int64 GPU
     tensor added to the seed when the kernel runs (a captured graph then draws
@@ -33,7 +41,7 @@ class mq_norm(ctypes.Structure):
                 ("groups", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
 
     def __init__(self, h: int, w: int, n: int, c: int, groups: int, act: int = ACT_NONE, eps: float = 1e-5):
-        super().__init__(h, w, n, c, groups, act, eps)
+        super().__init__(*_int32("mq_norm", h, w, n, c, groups, act), eps)
 
 
 class mq_cache(ctypes.Structure):
@@ -89,7 +97,7 @@ def _drop(drop: Optional[mq_drop]):
 def _dims(t, what: str):
     if not hasattr(t, "shape") or len(t.shape) != 4:
         raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, what, "a tensor of four dimensions [H][W][N][C] gives the sizes")
-    return tuple(t.shape)
+    return _int32(what, *t.shape)
 
 
 def mqconv_dropout(x, drop: mq_drop, y, residual=None, stream=None) -> None:
@@ -103,7 +111,7 @@ def mqconv_dropout(x, drop: mq_drop, y, residual=None, stream=None) -> None:
 
 def mqconv_dropout_mx(x, drop: mq_drop, dst, stream=None) -> None:
     """drop(x) quantized into dst (an ACT or GRAD MxTensor)."""
-    _mq._check(_lib().mqconv_dropout_mx(_floats(x, _mq._prod(dst.dims), "x"), _drop(drop), dst.c_struct("dst"),
+    _mq._check(_lib().mqconv_dropout_mx(_floats(x, _mq._prod(_int32("dst", *dst.dims)), "x"), _drop(drop), dst.c_struct("dst"),
                                         _mq._stream(stream)), "mqconv_dropout_mx")
 
 
@@ -193,6 +201,7 @@ class MxCache:
     @staticmethod
     def empty(fmt: int, slots: int, h: int, w: int, c: int, device="cuda") -> "MxCache":
         import torch
+        _int32("MxCache.empty", slots, h, w, c)
         nc, ns = mqconv_cache_codes_bytes(fmt, slots, h, w, c), mqconv_cache_scales_bytes(slots, h, w, c)
         if nc == 0 or ns == 0:
             raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, "MxCache.empty")
@@ -201,7 +210,7 @@ class MxCache:
 
     def c_struct(self) -> mq_cache:
         """The C view; tensor buffers are checked against the sizes the layout needs."""
-        t = (self.slots, self.h, self.w, self.c)
+        t = _int32("cache", self.slots, self.h, self.w, self.c)
         return mq_cache(_mq._buf(self.codes, mqconv_cache_codes_bytes(self.fmt, *t), "uint8", "cache.codes"),
                         _mq._buf(self.scales, mqconv_cache_scales_bytes(*t), "uint8", "cache.scales"), self.fmt, *t)
 
@@ -213,7 +222,7 @@ def _slots(slot, count: int) -> Optional[int]:
 def _count(slot) -> int:
     if not hasattr(slot, "numel"):
         raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, "slot", "a tensor gives the number of samples")
-    return slot.numel()
+    return _int32("slot", slot.numel())[0]
 
 
 def _batch(x, c: MxCache, what: str):
@@ -228,16 +237,16 @@ def mqconv_cache_write(cache: MxCache, x, slot, n0: int = 0, stream=None) -> Non
     """Stores samples n0 .. of x [H][W][N][C], one for each entry of `slot` (int32), in these slots."""
     n, p = _batch(x, cache, "x")
     count = _count(slot)
-    _mq._check(_lib().mqconv_cache_write(cache.c_struct(), p, n, n0, count, _slots(slot, count), _mq._stream(stream)),
-               "mqconv_cache_write")
+    _mq._check(_lib().mqconv_cache_write(cache.c_struct(), p, n, *_int32("n0", n0), count, _slots(slot, count),
+                                         _mq._stream(stream)), "mqconv_cache_write")
 
 
 def mqconv_cache_read(cache: MxCache, slot, x, n0: int = 0, stream=None) -> None:
     """Writes the values of the slots to samples n0 .. of x [H][W][N][C]."""
     n, p = _batch(x, cache, "x")
     count = _count(slot)
-    _mq._check(_lib().mqconv_cache_read(cache.c_struct(), _slots(slot, count), count, p, n, n0, _mq._stream(stream)),
-               "mqconv_cache_read")
+    _mq._check(_lib().mqconv_cache_read(cache.c_struct(), _slots(slot, count), count, p, n, *_int32("n0", n0),
+                                        _mq._stream(stream)), "mqconv_cache_read")
 
 
 def mqconv_cache_read_mx(cache: MxCache, slot, xq, stream=None) -> None:

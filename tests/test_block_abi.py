@@ -207,6 +207,39 @@ def test_cache_calls_refuse_slots_that_are_no_tensor():
     assert _status(mq.mqconv_cache_write, cache, FakeBatch((2, 3, 5, 40)), none) == SHAPE
 
 
+def test_sizes_beyond_32_bits_are_refused():
+    """Their low 32 bits are valid sizes, which the library must not be given."""
+    import torch
+    big = 2**32
+    for i in range(5):
+        sizes = [2, 3, 4, 8, 2]
+        sizes[i] += big
+        with pytest.raises(mq.MqConvError) as e:
+            mq.mq_norm(*sizes)
+        assert e.value.status == SHAPE
+    d = mq.mq_drop(0.5, 3)
+    for i in range(4):
+        dims = [2, 3, 4, 8]
+        dims[i] += big
+        x = FakeBatch(tuple(dims))
+        assert _status(mq.mqconv_dropout, x, d, x) == SHAPE
+        assert _status(mq.mqconv_dropout_mx, x, d, _mx(mq.ROLE_ACT, dims)) == SHAPE
+        with pytest.raises(mq.MqConvError):
+            mq.MxCache.empty(0, *dims, device="cpu")
+    slot = FakeBatch((2,))
+    slot.dtype = torch.int32
+    slot.numel = lambda: 2
+    batch = FakeBatch((2, 3, 5, 40))
+    for slots, n0 in ((4 + big, 0), (4, big), (4, -big)):
+        cache = mq.MxCache(FAKE, FAKE, 0, slots, 2, 3, 40)
+        assert _status(mq.mqconv_cache_write, cache, batch, slot, n0=n0) == SHAPE
+        assert _status(mq.mqconv_cache_read, cache, slot, batch, n0=n0) == SHAPE
+    slot.nbytes, slot.numel = 4 * (big + 2), lambda: big + 2
+    cache = mq.MxCache(FAKE, FAKE, 0, 4, 2, 3, 40)
+    assert _status(mq.mqconv_cache_write, cache, batch, slot) == SHAPE
+    assert _status(mq.mqconv_cache_read, cache, slot, batch) == SHAPE
+
+
 class FakeBatch(FakeWorkspace):
     """An fp32 tensor as the binding sees one, at an address that is never used."""
 
