@@ -23,7 +23,7 @@ extern "C" {
 /* Activations. MQ_ACT_SILU: u / (1 + exp(-u)); MQ_ACT_GELU: u times the
  * normal distribution's integral (the erf form). Both keep their digits in the
  * negative tail, but for about |u| and 1.5 u^2 roundings (2^-24 of the result),
- * and are 0 where the exponential leaves fp32's normal range (SiLU from -87,
+ * and may be 0 where the exponential leaves fp32's normal range (SiLU from -87,
  * GELU from -13 on). A plain 32-bit integer, as mq_elem; an unknown value is
  * rejected with MQ_ERR_FORMAT. */
 enum { MQ_ACT_NONE = 0, MQ_ACT_RELU = 1, MQ_ACT_SILU = 2, MQ_ACT_GELU = 3 };

@@ -170,8 +170,10 @@ hipError_t launch_cache_write(const CacheView& c, const float* x, int N, int n0,
 // A thread turns four codes into one 16-byte store, so a wave's stores are
 // 1 KB of consecutive bytes. A workgroup's tile is kReadPix pixels x a few
 // samples: the scale bytes of a slot's neighbouring pixels share cache lines,
-// which one workgroup then uses up. Bound by the stores: 128 samples of 20 x 20
-// x 256 from E2M1 15 us (52 MB written, 7 MB read).
+// which one workgroup then uses up. Bound by instructions (addresses and
+// decoding issue in 72% of the busy cycles) and by loads of which only one round
+// is in flight: 128 samples of 20 x 20 x 256 from E2M1 15 us (52 MB written, 7 MB
+// read, 3.9 TB/s).
 constexpr int kReadPix = 16, kReadUnroll = 4;
 struct CacheRead {
   CacheView c;
@@ -261,7 +263,8 @@ hipError_t launch_cache_read(const CacheView& c, const int32_t* slot, int count,
 // whose lines come back with their own format and scale gets its codes back,
 // because the largest code of a line lies in the format's largest binade (or
 // the line's scale byte is 0, and its values' too). Bound by decoding and
-// encoding: 128 samples of 20 x 20 x 256 from E3M2 to E4M3 squares 10.7 us (23 MB).
+// encoding, whose instructions issue in 84% of the busy cycles: 128 samples of
+// 20 x 20 x 256 from E3M2 to E4M3 squares 11 us (23 MB).
 template <int FI, bool FULL>
 struct CacheSrc {
   CacheView c;

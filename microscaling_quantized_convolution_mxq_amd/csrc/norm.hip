@@ -9,16 +9,18 @@
 //   One pass: where a slab of whole groups over all pixels fits the registers
 //     of a workgroup, that workgroup reads it once, joins the statistics in
 //     LDS and writes the result from its registers: one launch, no workspace.
-//   Streaming: partial statistics (a mean and a sum of squares around it) or
+//   Streaming: partial statistics (a mean and the mean square around it) or
 //     sums of chunks of pixels, and an elementwise pass that reads x (and dy)
 //     again. The fp32 pass joins the chunks of its own columns' groups first,
 //     in a fixed order (narrow tiles have few chunks, so that is one round of
 //     loads); for MX results, whose tiles span 32 samples, and for groups of
 //     very many columns a kernel in between joins them once.
-// Sums of values are fp64 (two operations a value, hidden behind the loads),
-// so a mean is its fp32 rounding, whatever cancels in it; squares are summed
-// in fp32 around means of the values themselves, so a mean far from zero
-// costs no digits, and joined in fp64.
+// Sums of values, and of the gradient's terms, are fp64 (two operations a
+// value, hidden behind the loads), so a mean is its fp32 rounding, whatever
+// cancels in it, and no sum loses digits with its length. Squares are summed in
+// fp32 around the mean of the few values that a thread has at one time, and
+// joined in fp64 around one of those means, so a mean far from zero costs no
+// digits. Partial results are kept in fp32.
 #include <algorithm>
 
 #include "norm.h"
@@ -278,7 +280,7 @@ __device__ __forceinline__ int seg_lanes(int threads, int nseg) {
 // ---------------------------------------------------------------------------
 // A slab of whole groups over all pixels, R pixels of an octet a thread in
 // registers. Bound by latency (one round of loads, two barriers, one of
-// stores): 16 x 16 x 2 x 32 in 8 groups takes 6 us.
+// stores): 16 x 16 x 2 x 32 in 8 groups takes 6.1 us.
 template <int R, int UW, bool FULL, int ACT>
 __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_kernel(const NormArgs a) {
   constexpr int UN = 8 / UW;
@@ -370,8 +372,9 @@ __global__ __launch_bounds__(UW == 1 || R == kOneR ? 512 : 1024) void norm_one_k
 // ---------------------------------------------------------------------------
 // Partial statistics: one read of x. A thread carries batches of pixels of its
 // octet in fp64 sums, then a tree in LDS joins the threads of a column, so a
-// chunk leaves one entry a unit. Bound by reading x: 160 x 160 x 32 x 128 92 us (4.6 TB/s);
-// 80 x 80 x 16 x 64 9.0 us, mostly the first loads' latency.
+// chunk leaves one entry a unit. Bound by reading x: 160 x 160 x 32 x 128 92 us
+// (4.6 TB/s; vector instructions issue in 43% of the busy cycles);
+// 80 x 80 x 16 x 64 8.3 us, mostly the first loads' latency.
 template <int UW, bool FULL>
 __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
   constexpr int UN = 8 / UW;
@@ -458,8 +461,9 @@ __global__ __launch_bounds__(256) void norm_stats_kernel(const NormArgs a) {
 // ---------------------------------------------------------------------------
 // Threads of a workgroup that joins segments. The backward's few segments have
 // four parameters a column to write, so they are spread over more workgroups
-// (128 samples of 256 channels in 32 groups, two chunks: 64 threads 4.9, 256
-// 5.8 us); the forward's two are not (16 of 64 channels, 32 chunks: 4.4, 3.9 us).
+// (128 samples of 256 channels in 32 groups, two chunks: 64 threads 4.8, 256
+// 5.8 us); the forward's two are not (16 of 64 channels, 32 chunks: 64 threads
+// half a microsecond more than 256, 4.4 us).
 constexpr int join_threads(bool bwd) { return bwd ? 64 : 256; }
 constexpr int kWideT = 1024;
 
@@ -648,7 +652,7 @@ constexpr int kTileOcts = 16;  // widest tile, so at most 8 * kTileOcts segments
 
 // y, on the tiles and chunks of the statistics. Every workgroup joins the few
 // chunks of its own columns while its first pixels are on their way, which
-// saves a launch. Bound by memory: 160 x 160 x 32 x 128 144 us, 839 MB at
+// saves a launch. Bound by memory: 160 x 160 x 32 x 128 146 us, 839 MB at
 // 5.8 TB/s.
 template <bool FULL, int ACT>
 __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
@@ -714,7 +718,7 @@ __global__ __launch_bounds__(256) void norm_apply_kernel(const NormArgs a) {
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// mean and gamma * rstd of an octet from the forward's statistics
+// mean, rstd, gamma * rstd and beta of an octet from the forward's statistics
 template <bool FULL>
 __device__ __forceinline__ void grad_params(const NormArgs& a, const Oct& t, float (&mean)[8], float (&rstd)[8],
                                             float (&ga)[8], float (&be)[8]) {
@@ -730,8 +734,8 @@ __device__ __forceinline__ void grad_params(const NormArgs& a, const Oct& t, flo
   }
 }
 
-// adds g and g * (x - mean) of one pixel to the octet's sums; d and gr are
-// left holding x - mean and g
+// turns x (in d) into x - mean, and dy (in gr) into g = drop(dy) act'(u), for one
+// pixel of the octet
 template <int ACT>
 __device__ __forceinline__ void grad_terms(const NormArgs& a, const DropKey& key, const Oct& t, int p,
                                            const float (&mean)[8], const float (&ga)[8], const float (&be)[8],
@@ -744,8 +748,8 @@ __device__ __forceinline__ void grad_terms(const NormArgs& a, const DropKey& key
 
 // The gradient of a slab of whole groups whose x and dy stay in registers: the
 // columns' sums of g and g (x - mean) through LDS, the groups' means of them,
-// then dx. Bound by latency (124 x 4 x 32
-// x 8, GELU: 11 us with the channels' sums behind it).
+// then dx. Bound by latency (124 x 4 x 32 x 8, GELU: 10.1 us, and 3.8 of the
+// channels' sums behind it).
 template <int R, bool FULL, int ACT>
 __global__ __launch_bounds__(512) void norm_one_backward_kernel(const NormArgs a) {
   extern __shared__ float2 sh[];
@@ -877,7 +881,8 @@ __global__ __launch_bounds__(256) void norm_channel_kernel(const NormArgs a) {
 
 // Every column's sums of g and g xh over a chunk of pixels: one read of x and
 // dy. Columns, not groups, because dgamma and dbeta need them. Bound by
-// reading: 20 x 20 x 128 x 256 20.2 us (5.2 TB/s), 80 x 80 x 16 x 64 11.6 us.
+// reading: 20 x 20 x 128 x 256 20.8 us (5.0 TB/s; vector instructions in 56% of
+// the busy cycles), 80 x 80 x 16 x 64 12.0 us.
 template <bool FULL, int ACT>
 __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
   __shared__ float2 su[256 * 8];
@@ -958,7 +963,7 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormArgs a) {
 // dx, on the tiles and chunks of the sums, whose chunks it joins for its own
 // columns; the first `extra` workgroups sum dgamma and dbeta. Bound by memory
 // and, at small sizes, by the chain of loads before the first result: 80 x 80 x
-// 16 x 64 18.8 us (79 MB), 80 x 80 x 64 x 64 55 us (315 MB, 5.7 TB/s).
+// 16 x 64 18.7 us (79 MB), 80 x 80 x 64 x 64 56 us (315 MB, 5.6 TB/s).
 template <bool FULL, int ACT>
 __global__ __launch_bounds__(256) void norm_apply_backward_kernel(const NormArgs a, int extra) {
   const NormGeo& g = a.g;

@@ -2,10 +2,11 @@
 // MX output: every value is made again from x (and dy) and the columns'
 // parameters, and quantized in place (mx_rows.h). A read of x (and dy) and a
 // quarter of that or less written: 80 x 80 x 16 x 64 with SiLU and dropout
-// takes 12.0 us (26 MB; sigmoid, Philox and packing beside the loads), the
-// gradient of 20 x 20 x 128 x 256 26.2 us (118 MB, 4.5 TB/s; its five
-// parameters a channel leave registers for eight waves a compute unit, and
-// four for sixteen made it spill and take 35 us).
+// takes 12.2 us (33 MB; sigmoid, Philox and packing beside the loads: vector
+// instructions issue in 58% of the busy cycles), the gradient of 20 x 20 x 128 x
+// 256 26.3 us (118 MB, 4.5 TB/s, 55%; its five parameters a channel leave
+// registers for eight waves a compute unit, and four for sixteen made it spill
+// and take 35 us).
 #include "mx_rows.h"
 #include "norm.h"
 
