@@ -75,7 +75,7 @@ int mqconv_dropout_mx(const float* x, const mq_drop* drop, mq_mx dst, void* stre
  * around the mean of at most 64 values and joined in fp64 around a mean, so
  * rstd has fp32's accuracy whatever the mean is. Deviations of 1.8e19 and more
  * overflow (rstd is 0 then), from 2.3e18 on they may, and the squares of those
- * below 1e-19 lose digits.
+ * below 1e-19 lose digits. x - mean itself has to stay in fp32's range.
  *   Backward, from dy (gradient of y) and the forward's x, mean, rstd:
  *   g = drop(dy) * act'(u);  xh = (x - mean) * rstd
  *   dbeta[c] = sum g;  dgamma[c] = sum g * xh          (over H, W, N)
