@@ -465,3 +465,7 @@ from .block import (ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, CACHE_COUNT_MAX, EXP
                     mqconv_cache_read_mx, mqconv_cache_scales_bytes, mqconv_cache_write, mqconv_dropout,
                     mqconv_dropout_mx, mqconv_group_norm, mqconv_group_norm_backward, mqconv_group_norm_backward_mx,
                     mqconv_group_norm_mx, mqconv_group_norm_workspace_bytes)
+
+# ---- a layer's norm, products and update (include/mqconv_train.h) --------------------
+from .train import (EXPORTED_TRAIN, mq_layer_norm, mqconv_layer_norm, mqconv_layer_norm_backward,  # noqa: E402,F401
+                    mqconv_layer_norm_backward_mx, mqconv_layer_norm_mx, mqconv_layer_norm_workspace_bytes)

@@ -11,6 +11,7 @@ namespace mq {
 const long long kMaxElems = 1LL << 30;
 
 inline bool fmt_ok(int f) { return f >= MQ_E4M3 && f <= MQ_E2M1; }
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 inline bool dims_ok(int32_t d0, int32_t d1, int32_t d2, int32_t d3) {
@@ -32,6 +33,10 @@ inline int check_mx(const mq_mx& t, mq_role role, int32_t d0, int32_t d1, int32_
   if (t.d0 != d0 || t.d1 != d1 || t.d2 != d2 || t.d3 != d3) return MQ_ERR_SHAPE;
   if (!aligned16(t.codes) || !aligned16(t.scales)) return MQ_ERR_ALIGN;
   return MQ_OK;
+}
+
+inline MxOutView out_view(const mq_mx& t) {
+  return MxOutView{static_cast<uint8_t*>(t.codes), t.scales, t.fmt, t.block_partner};
 }
 
 inline int hip_status(hipError_t e) { return e == hipSuccess ? MQ_OK : MQ_ERR_HIP; }

@@ -11,8 +11,6 @@ using namespace mq;
 
 namespace {
 
-bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
-
 int check_drop(const mq_drop* d, DropSpec* out) {
   *out = DropSpec{0.0f, 0, nullptr};
   if (!d) return MQ_OK;
@@ -35,10 +33,6 @@ int check_norm(const mq_norm* gn, NormShape* s) {
 int check_ws(const NormShape& s, int op, const void* ws, size_t ws_bytes) {
   if (!ws || ws_bytes < norm_workspace_bytes(s, op)) return MQ_ERR_WORKSPACE;
   return aligned16(ws) ? MQ_OK : MQ_ERR_ALIGN;
-}
-
-MxOutView out_view(const mq_mx& t) {
-  return MxOutView{static_cast<uint8_t*>(t.codes), t.scales, t.fmt, t.block_partner};
 }
 
 const MxOutView kNoMx{nullptr, nullptr, 0, 0};

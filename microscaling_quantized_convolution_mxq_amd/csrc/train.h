@@ -1,0 +1,23 @@
+// train.h -- launchers of the layer norm kernels, of the products of two-level
+// codes and of the orthogonalised weight update, shared with their C ABI layer.
+// Host-side; arguments are already validated.
+#pragma once
+#include "mqconv_internal.h"
+
+namespace mq {
+
+// One layer norm: the rows of P pixels and N samples, C channels each.
+struct LnShape {
+  int P, N, C;
+  float eps;
+};
+size_t layer_norm_workspace_bytes(const LnShape& s, int op);
+// exactly one of y and yq (yq.codes) is given; residual, sum, mean, rstd may be null (sum is given where yq and residual are)
+hipError_t launch_layer_norm(const LnShape& s, const float* x, const float* residual, const float* gamma,
+                             const float* beta, float* sum, float* y, const MxOutView& yq, float* mean, float* rstd,
+                             void* ws, hipStream_t st);
+hipError_t launch_layer_norm_backward(const LnShape& s, const float* dy, const float* x, const float* gamma,
+                                      const float* mean, const float* rstd, const float* dskip, float* dx,
+                                      const MxOutView& dxq, float* dgamma, float* dbeta, void* ws, hipStream_t st);
+
+}  // namespace mq

@@ -1,0 +1,29 @@
+"""CPU oracle of what include/mqconv_train.h computes, in plain fp64 numpy from
+the definitions. Tensors are [H][W][N][C], weights [Cout][Kh][Kw][Cin].
+
+TEST INFRASTRUCTURE: shares no code with the GPU library.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def layer_norm(s, gamma, beta, eps):
+    """(y, mean, rstd) of rows s [..., C]."""
+    s = np.asarray(s, np.float64)
+    mean = s.mean(axis=-1)
+    d = s - mean[..., None]
+    rstd = 1 / np.sqrt((d * d).mean(axis=-1) + eps)
+    return gamma * d * rstd[..., None] + beta, mean, rstd
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, dskip=0.0):
+    """(dx, dgamma, dbeta, parts) from the forward's mean and rstd; parts are what a bound on dx's error is made of."""
+    dy, x = np.asarray(dy, np.float64), np.asarray(x, np.float64)
+    m, r = np.asarray(mean, np.float64)[..., None], np.asarray(rstd, np.float64)[..., None]
+    xh = (x - m) * r
+    g = gamma * dy
+    k1, k2 = g.mean(axis=-1, keepdims=True), (g * xh).mean(axis=-1, keepdims=True)
+    dx = r * (g - k1 - xh * k2) + dskip
+    rows = tuple(range(dy.ndim - 1))
+    return dx, (dy * xh).sum(axis=rows), dy.sum(axis=rows), {"xh": xh, "g": g, "k1": k1, "k2": k2, "r": r}

@@ -1,0 +1,90 @@
+"""include/mqconv_train.h on a machine without a GPU: exported symbols, buffer
+sizes, and the refusal of every invalid argument before any HIP call; the same
+tests under the host sanitizers."""
+import os
+import re
+import subprocess
+import sys
+
+import pytest
+
+import microscaling_quantized_convolution_mxq_amd as mq
+from test_block_abi import ALIGN, FAKE, FORMAT, NULL, SHAPE, UNSUPPORTED, WORKSPACE, FakeWorkspace, _mx, _status
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "mqconv_train.h")
+pytestmark = pytest.mark.skipif(not os.path.exists(mq.LIB_PATH), reason="libmqconv.so not built")
+
+
+def test_exports_every_declared_symbol():
+    src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"\b(mqconv_\w+)\s*\(", src))
+    out = subprocess.run(["nm", "-D", "--defined-only", mq.LIB_PATH], capture_output=True, text=True).stdout
+    assert names == set(mq.EXPORTED_TRAIN)
+    assert names <= set(re.findall(r"\bT\s+(mqconv_\w+)", out))
+
+
+# ---- layer norm ---------------------------------------------------------------------------------
+def test_layer_norm_workspace_sizes():
+    for h, w, n, c in ((1, 1, 1, 1), (7, 9, 3, 45), (80, 80, 16, 64), (1, 512, 16, 4096), (1, 1, 2, 2**20), (1, 1, 2**25, 1)):
+        rows = h * w * n
+        ln = mq.mq_layer_norm(h, w, n, c)
+        fwd, bwd = (mq.mqconv_layer_norm_workspace_bytes(ln, op) for op in (mq.NORM_FWD, mq.NORM_BWD))
+        assert fwd >= 8 * rows and fwd <= 8 * rows + 16
+        assert bwd >= fwd + 8 * c and bwd <= fwd + 8 * c * min(rows, 1024)
+    for ln, op in ((mq.mq_layer_norm(4, 5, 3, 24), 2), (mq.mq_layer_norm(4, 5, 3, 24), -1), (mq.mq_layer_norm(0, 5, 3, 24), 0),
+                   (mq.mq_layer_norm(4, 5, 3, -1), 1), (mq.mq_layer_norm(2**15, 2**15, 2, 1), 0),
+                   (mq.mq_layer_norm(4, 5, 3, 24, float("nan")), 0)):
+        assert mq.mqconv_layer_norm_workspace_bytes(ln, op) == 0
+    with pytest.raises(mq.MqConvError):
+        mq.mq_layer_norm(1, 1, 1, 2**32 + 4)
+
+
+def test_layer_norm_refusals():
+    ln = mq.mq_layer_norm(4, 5, 3, 24)
+    ws, dims = FakeWorkspace(1 << 20), (4, 5, 3, 24)
+    fwd = lambda s=ln, x=FAKE, ga=FAKE, be=FAKE, y=FAKE, m=FAKE, r=FAKE, res=None, sm=None: _status(  # noqa: E731
+        mq.mqconv_layer_norm, s, x, ga, be, y, m, r, residual=res, sum=sm)
+    assert fwd(x=0) == NULL and fwd(y=0) == NULL and fwd(res=FAKE) == NULL and fwd(sm=FAKE) == UNSUPPORTED
+    for k in ("x", "ga", "be", "y", "m", "r"):
+        assert fwd(**{k: FAKE + 2}) == ALIGN, k
+    assert fwd(res=FAKE + 1, sm=FAKE) == ALIGN and fwd(res=FAKE, sm=FAKE + 2) == ALIGN
+    for eps in (-1e-5, float("nan"), float("inf")):
+        assert fwd(s=mq.mq_layer_norm(4, 5, 3, 24, eps)) == UNSUPPORTED
+    assert fwd(s=mq.mq_layer_norm(4, 5, 0, 24)) == SHAPE and fwd(s=mq.mq_layer_norm(2**15, 2**15, 2, 1)) == SHAPE
+    mx = lambda t, w=ws: _status(mq.mqconv_layer_norm_mx, ln, FAKE, FAKE, FAKE, t, ws=w)  # noqa: E731
+    assert mx(_mx(mq.ROLE_GRAD, dims)) == FORMAT and mx(_mx(mq.ROLE_ACT, dims, fmt=5)) == FORMAT
+    assert mx(_mx(mq.ROLE_ACT, dims, bp=16)) == UNSUPPORTED and mx(_mx(mq.ROLE_ACT, (4, 5, 3, 25))) == SHAPE
+    assert mx(_mx(mq.ROLE_ACT, dims, codes=0)) == NULL and mx(_mx(mq.ROLE_ACT, dims, scales=FAKE + 8)) == ALIGN
+    ok = _mx(mq.ROLE_ACT, dims)
+    assert mx(ok, None) == WORKSPACE and mx(ok, FakeWorkspace(8)) == WORKSPACE and mx(ok, FakeWorkspace(1 << 20, FAKE + 8)) == ALIGN
+
+    bwd = lambda dy=FAKE, x=FAKE, ga=FAKE, m=FAKE, r=FAKE, dx=FAKE, dg=FAKE, db=FAKE, w=ws, sk=None: _status(  # noqa: E731
+        mq.mqconv_layer_norm_backward, ln, dy, x, ga, m, r, dx, dg, db, w, dskip=sk)
+    for k in ("dy", "x", "m", "r", "dx"):
+        assert bwd(**{k: 0}) == NULL, k
+    for k in ("dy", "x", "ga", "m", "r", "dx", "dg", "db", "sk"):
+        assert bwd(**{k: FAKE + 2}) == ALIGN, k
+    assert bwd(w=None) == WORKSPACE and bwd(w=FakeWorkspace(64)) == WORKSPACE and bwd(w=FakeWorkspace(1 << 20, FAKE + 4)) == ALIGN
+    bmx = lambda t: _status(mq.mqconv_layer_norm_backward_mx, ln, FAKE, FAKE, FAKE, FAKE, FAKE, t, ws=ws)  # noqa: E731
+    assert bmx(_mx(mq.ROLE_ACT, dims)) == FORMAT and bmx(_mx(mq.ROLE_GRAD, (4, 5, 4, 24))) == SHAPE
+    L = mq.train._lib()
+    assert L.mqconv_layer_norm(None, FAKE, None, None, None, None, FAKE, None, None, None) == NULL
+    assert L.mqconv_layer_norm_backward(None, FAKE, FAKE, None, FAKE, FAKE, None, FAKE, None, None, FAKE, 1 << 20, None) == NULL
+
+
+# ---- the same under the host sanitizers ---------------------------------------------------------
+def test_refusals_under_host_sanitizers():
+    if os.environ.get("MQCONV_LIB"):
+        pytest.skip("already under the sanitizers")
+    # (here, so that collecting the tests does not need the sanitizer build's module)
+    from microscaling_quantized_convolution_mxq_amd import build_sanitize as san
+    if not san.runtime():
+        pytest.skip("clang AddressSanitizer runtime not installed")
+    env = dict(os.environ, LD_PRELOAD=san.runtime(), MQCONV_LIB=san.build(),
+               ASAN_OPTIONS="detect_leaks=0:abort_on_error=1:halt_on_error=1", UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", os.path.abspath(__file__)], cwd=ROOT,
+                       env=env, capture_output=True, text=True, timeout=600)
+    out = r.stdout + r.stderr
+    assert "AddressSanitizer" not in out and "runtime error:" not in out, out[-4000:]
+    assert r.returncode == 0 and " passed" in out, out[-4000:]
