@@ -1,7 +1,8 @@
 /*
  * mqconv_train.h -- C ABI of what a layer needs, beside the calls of mqconv.h
  * and mqconv_block.h, to be trained in the two-level 4-bit format: layer
- * normalization over the channels (forward and backward).
+ * normalization over the channels (forward and backward), and the
+ * orthogonalised update of the weights.
  *
  * The conventions of mqconv.h hold: device pointers owned by the caller, work
  * enqueued on `stream`, every argument checked before any HIP call, an
@@ -70,6 +71,65 @@ int mqconv_layer_norm_backward(const mq_layer_norm* ln, const float* dy, const f
 int mqconv_layer_norm_backward_mx(const mq_layer_norm* ln, const float* dy, const float* x, const float* gamma,
                                   const float* mean, const float* rstd, const float* dskip, mq_mx dxq, float* dgamma,
                                   float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Orthogonalised weight update (Newton-Schulz steps, as the Muon optimizer's)
+ * ---------------------------------------------------------------------------
+ * A weight [Cout][Kh][Kw][Cin] is the matrix of `rows` = Cout and `cols` = Kh
+ * Kw Cin. With U its gradient or momentum:
+ *   X = U / (|U|_F + eps);   steps times:  X <- a X + (b S + c S^2) X,  S = X X^T
+ * so a singular value x becomes p(x) = a x + b x^3 + c x^5, step after step,
+ * and the singular vectors stay: a few steps bring every singular value near
+ * 1 that is not far below the largest. |U|_F and the products' sums are held
+ * in 32 bits or more; every factor of a product in two f16 parts, 22 bits or
+ * more, so results have the accuracy of fp32 products.
+ * Parts of U whose share of |U|_F is below 2^-40 may be lost; a NaN or an
+ * infinity in U makes its whole result NaN; U = 0 gives 0 (NaN with eps = 0,
+ * as the formula does). */
+typedef struct {
+  int32_t steps; /* 1 .. MQ_NEWTON_STEPS_MAX, else MQ_ERR_UNSUPPORTED */
+  float a, b, c; /* finite, and such that |x| < 1.41 and |a + b x^2 + c x^4| < 3.99 wherever the steps lead from
+                    x in [0, 1], else MQ_ERR_UNSUPPORTED; (3.4445, -4.7750, 2.0315) is the usual choice */
+  float eps;     /* finite, >= 0, else MQ_ERR_UNSUPPORTED */
+} mq_newton;
+#define MQ_NEWTON_STEPS_MAX 32
+
+/* The optimizer step around it, for gradient g, momentum m and weight w:
+ *   m <- momentum * m + g
+ *   U  = nesterov ? g + momentum * m : m
+ *   w <- (1 - r * decay) * w - r * s * X(U),   r = lr * *rate (lr where rate is NULL)
+ * s: 1 (MQ_SCALE_NONE), sqrt(max(1, rows / cols)) (MQ_SCALE_ASPECT) or
+ * 0.2 sqrt(max(rows, cols)) (MQ_SCALE_RMS). */
+enum { MQ_SCALE_NONE = 0, MQ_SCALE_ASPECT = 1, MQ_SCALE_RMS = 2 };
+typedef struct {
+  mq_newton newton;
+  float lr, momentum, decay; /* finite, else MQ_ERR_UNSUPPORTED */
+  int32_t nesterov;          /* 0 or 1 */
+  int32_t scale;             /* MQ_SCALE_*, else MQ_ERR_FORMAT */
+  const float* rate;         /* device, 4-byte aligned, or NULL: read when the kernel runs, so a captured graph
+                                follows a schedule */
+} mq_muon;
+
+/* The weights of one call: 1 .. MQ_UPDATE_GROUP_MAX matrices, which share
+ * every launch. Arrays are HOST arrays, read during the call only. */
+#define MQ_UPDATE_GROUP_MAX 32
+
+/* Workspace (device bytes, 16-byte aligned) of the calls below for these
+ * matrices; 0 for invalid arguments. A matrix is refused with MQ_ERR_SHAPE
+ * where its extents, rounded up to 32, have a product or a smaller one's
+ * square of 2^29 - 64 or more. */
+size_t mqconv_orthogonalize_workspace_bytes(int32_t count, const int32_t* rows, const int32_t* cols);
+
+/* x[i] (fp32 [rows][cols], fully overwritten) = X(u[i]); x[i] may be u[i],
+ * otherwise outputs must not overlap anything. */
+int mqconv_orthogonalize(const mq_newton* newton, int32_t count, const int32_t* rows, const int32_t* cols,
+                         const float* const* u, float* const* x, void* ws, size_t ws_bytes, void* stream);
+
+/* One optimizer step: m[i] and w[i] are updated from g[i]. Nothing may
+ * overlap. */
+int mqconv_muon_update(const mq_muon* opt, int32_t count, const int32_t* rows, const int32_t* cols,
+                       const float* const* g, float* const* m, float* const* w, void* ws, size_t ws_bytes,
+                       void* stream);
 
 #ifdef __cplusplus
 }

@@ -467,5 +467,7 @@ from .block import (ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, CACHE_COUNT_MAX, EXP
                     mqconv_group_norm_mx, mqconv_group_norm_workspace_bytes)
 
 # ---- a layer's norm, products and update (include/mqconv_train.h) --------------------
-from .train import (EXPORTED_TRAIN, mq_layer_norm, mqconv_layer_norm, mqconv_layer_norm_backward,  # noqa: E402,F401
-                    mqconv_layer_norm_backward_mx, mqconv_layer_norm_mx, mqconv_layer_norm_workspace_bytes)
+from .train import (EXPORTED_TRAIN, MUON_SCALE_ASPECT, MUON_SCALE_NONE, MUON_SCALE_RMS, UPDATE_GROUP_MAX,  # noqa: E402,F401
+                    mq_layer_norm, mq_muon, mq_newton, mqconv_layer_norm, mqconv_layer_norm_backward,
+                    mqconv_layer_norm_backward_mx, mqconv_layer_norm_mx, mqconv_layer_norm_workspace_bytes,
+                    mqconv_muon_update, mqconv_orthogonalize, mqconv_orthogonalize_workspace_bytes)

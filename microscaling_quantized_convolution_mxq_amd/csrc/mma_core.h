@@ -1,0 +1,205 @@
+// mma_core.h -- the K loop shared by the 16-bit matrix products: the two-level
+// products (bf16 operands) and the Newton-Schulz products (fp32 values as two
+// f16 planes).
+//
+// C[i][j] = sum_k A[i][k] B[j][k]. Both operands are rows with k contiguous,
+// read in steps of 128 bytes of every row:
+//   Bf16:   64 values;
+//   Split:  32 values as 32 f16 high parts, then their 32 low parts:
+//           a = ah + al with ah = f16(a), al = f16(a - ah), 22 bits or more,
+//           a b = ah bh + ah bl + al bh (al bl, below 2^-22 of it, is left out).
+// A step of a tile is [row][8] chunks of 16 bytes in LDS, written by loads that
+// go to LDS directly. Chunk c of row r is in slot c ^ ((r >> 1) & 7): a row is
+// half of the 64 banks, so the sixteen rows that an operand read touches at one
+// time lie in sixteen different groups of four banks.
+// ST stages form a ring: one barrier a step, after which the stage that was
+// read in the step before is filled again.
+#pragma once
+#include <type_traits>
+
+#include "mx_common.h"
+
+namespace mq {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
+
+constexpr int kPiece = 128;         // bytes of a row in a step
+constexpr int kBeyond = 0x7fffff00; // an offset past the end of every buffer: such loads write zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mma_rsrc(const void* p, long long bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(bytes < kBeyond ? bytes : kBeyond),
+                                           0x00020000);
+}
+
+typedef __attribute__((address_space(3))) void* mma_lds_t;
+// 16 bytes a lane from voff + soff to lds + 16 * lane
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mma_lds_t)lds, 16, voff, soff, 0, 0);
+}
+
+// Waits until at most N of this wave's loads are under way and its LDS reads
+// are done, then for the other waves. (No memory fence: the wait is explicit,
+// and the empty asm statements keep LDS accesses on their side.)
+template <int N>
+__device__ __forceinline__ void stage_ready() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A workgroup's tile: BM x BN outputs by WM x WN waves, a ring of ST stages.
+template <int BM_, int BN_, int WM_, int WN_, int ST_>
+struct MmaShape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
+  static constexpr int NW = WM * WN, THREADS = 64 * NW;
+  static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;  // a wave's 32 x 32 products
+  static constexpr int STAGE = (BM + BN) * kPiece, LDS = ST * STAGE;
+  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;     // loads of a wave and step
+  static_assert(LA >= 1 && LB >= 1 && TM >= 1 && TN >= 1 && NW % 2 == 0, "tile");
+};
+
+// What a lane loads: load j of wave w covers rows 8 (w + NW j) ..+8, the lane
+// row + lane / 8; with an even number of waves its chunk is the same in all.
+__device__ __forceinline__ int lane_chunk(int wave, int lane) { return (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7); }
+template <int NW>
+__device__ __forceinline__ int lane_row(int wave, int lane, int j) {
+  return 8 * (wave + NW * j) + (lane >> 3);
+}
+
+// Rows of a matrix with k contiguous.
+template <int L, int NW>
+struct RowLoader {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int off[L];
+  __device__ void init(const void* p, long long bytes, int row0, int rows, int pitch, int wave, int lane) {
+    rsrc = mma_rsrc(p, bytes);
+#pragma unroll
+    for (int j = 0; j < L; j++) {
+      const int r = row0 + lane_row<NW>(wave, lane, j);
+      off[j] = r < rows ? r * pitch + lane_chunk(wave, lane) * 16 : kBeyond;
+    }
+  }
+  __device__ void issue(int step, uint8_t* lds, int wave) const {
+#pragma unroll
+    for (int j = 0; j < L; j++) load_lds16(rsrc, lds + (wave + NW * j) * 1024, off[j], step * kPiece);
+  }
+};
+
+struct Bf16 {};
+struct Split {};
+
+template <class T, int TM, int TN>
+__device__ __forceinline__ void mma_step(const uint8_t* a, const uint8_t* b, int lane, v16f (&acc)[TM][TN]) {
+  const int r = lane & 31, q = lane >> 5, sw = (r >> 1) & 7;
+  const uint8_t* const ar = a + r * kPiece;
+  const uint8_t* const br = b + r * kPiece;
+  if constexpr (std::is_same<T, Bf16>::value) {
+#pragma unroll
+    for (int kk = 0; kk < 4; kk++) {
+      const int at = ((2 * kk + q) ^ sw) << 4;
+      bhalf8 x[TM], y[TN];
+#pragma unroll
+      for (int i = 0; i < TM; i++) x[i] = *reinterpret_cast<const bhalf8*>(ar + 32 * i * kPiece + at);
+#pragma unroll
+      for (int j = 0; j < TN; j++) y[j] = *reinterpret_cast<const bhalf8*>(br + 32 * j * kPiece + at);
+#pragma unroll
+      for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < 2; kk++) {
+      const int hi = ((2 * kk + q) ^ sw) << 4, lo = ((4 + 2 * kk + q) ^ sw) << 4;
+      half8 xh[TM], xl[TM], yh[TN], yl[TN];
+#pragma unroll
+      for (int i = 0; i < TM; i++) {
+        xh[i] = *reinterpret_cast<const half8*>(ar + 32 * i * kPiece + hi);
+        xl[i] = *reinterpret_cast<const half8*>(ar + 32 * i * kPiece + lo);
+      }
+#pragma unroll
+      for (int j = 0; j < TN; j++) {
+        yh[j] = *reinterpret_cast<const half8*>(br + 32 * j * kPiece + hi);
+        yl[j] = *reinterpret_cast<const half8*>(br + 32 * j * kPiece + lo);
+      }
+      // the small products first, each kind over all tiles before the next
+#pragma unroll
+      for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl[i], yh[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[i], yl[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[i], yh[j], acc[i][j], 0, 0, 0);
+    }
+  }
+}
+
+// The steps step0 .. step0 + n - 1 of a tile. Loaders: issue(step, lds, wave)
+// makes L loads of every wave, whatever the step is.
+template <class T, class S, class LA, class LB>
+__device__ __forceinline__ void mma_loop(uint8_t* lds, LA& la, LB& lb, int step0, int n, int wave, int lane,
+                                         v16f (&acc)[S::TM][S::TN]) {
+  constexpr int ST = S::ST, LPS = S::LA + S::LB;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  auto issue = [&](int s, int slot) {
+    uint8_t* const to = lds + slot * S::STAGE;
+    la.issue(step0 + s, to, wave);
+    lb.issue(step0 + s, to + S::BM * kPiece, wave);
+  };
+#pragma unroll
+  for (int s = 0; s < ST - 1; s++)
+    if (s < n) issue(s, s);
+  int slot = 0, fill = ST - 1;
+  for (int s = 0; s < n; s++) {
+    // step s has arrived once only the ST - 2 steps behind it are under way
+    if (s + ST - 2 < n) stage_ready<(ST - 2) * LPS>();
+    else stage_ready<0>();
+    if (s + ST - 1 < n) issue(s + ST - 1, fill);
+    const uint8_t* const at = lds + slot * S::STAGE;
+    mma_step<T, S::TM, S::TN>(at + wm * S::TM * 32 * kPiece, at + (S::BM + wn * S::TN * 32) * kPiece, lane, acc);
+    slot = slot + 1 == ST ? 0 : slot + 1;
+    fill = fill + 1 == ST ? 0 : fill + 1;
+  }
+}
+
+// f(row, column, quad): the four values of rows row .. row + 3 in one column, of a wave's results.
+template <class S, class F>
+__device__ __forceinline__ void mma_results(const v16f (&acc)[S::TM][S::TN], int wave, int lane, F&& f) {
+  const int wm = wave / S::WN, wn = wave % S::WN;
+#pragma unroll
+  for (int i = 0; i < S::TM; i++)
+#pragma unroll
+    for (int j = 0; j < S::TN; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const float v[4] = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+        f((wm * S::TM + i) * 32 + 8 * e + 4 * (lane >> 5), (wn * S::TN + j) * 32 + (lane & 31), v);
+      }
+}
+
+template <class S>
+__device__ __forceinline__ void mma_zero(v16f (&acc)[S::TM][S::TN]) {
+#pragma unroll
+  for (int i = 0; i < S::TM; i++)
+#pragma unroll
+    for (int j = 0; j < S::TN; j++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+}
+
+// Workgroups go to the eight XCDs in turn; this gives each XCD a contiguous
+// range of the n tiles, which share operand rows in its L2.
+__device__ __forceinline__ int xcd_tile(int b, int n) {
+  const int x = b & 7, i = b >> 3, q = n >> 3, r = n & 7;
+  return x * q + min(x, r) + i;
+}
+
+}  // namespace mq

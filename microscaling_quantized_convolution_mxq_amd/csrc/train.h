@@ -20,4 +20,21 @@ hipError_t launch_layer_norm_backward(const LnShape& s, const float* dy, const f
                                       const float* mean, const float* rstd, const float* dskip, float* dx,
                                       const MxOutView& dxq, float* dgamma, float* dbeta, void* ws, hipStream_t st);
 
+// The weight update: Newton-Schulz steps, and the optimizer around them.
+constexpr int kUpdateGroup = 32;  // MQ_UPDATE_GROUP_MAX
+struct UpdateSpec {
+  int steps;
+  float a, b, c, eps;
+  float momentum, decay, lr;
+  bool nesterov;
+  int scale;          // MQ_SCALE_*
+  const float* rate;  // device, or null
+};
+// whether the planes of a matrix stay within 32-bit offsets
+bool newton_shape_ok(int rows, int cols);
+size_t newton_workspace_bytes(int count, const int* rows, const int* cols);
+// mom null: out = the orthogonalised gradient; else mom and out (the weight) are updated
+hipError_t launch_newton(const UpdateSpec& u, int count, const int* rows, const int* cols, const float* const* grad,
+                         float* const* mom, float* const* out, void* ws, hipStream_t st);
+
 }  // namespace mq

@@ -11,6 +11,8 @@ using namespace mq;
 
 namespace {
 
+static_assert(kUpdateGroup == MQ_UPDATE_GROUP_MAX, "matrices of a call");
+
 const MxOutView kNoMx{nullptr, nullptr, 0, 0};
 
 int check_layer_norm(const mq_layer_norm* ln, LnShape* s) {
@@ -59,6 +61,67 @@ int layer_norm_backward(const mq_layer_norm* ln, const float* dy, const float* x
                                                dgamma, dbeta, ws, (hipStream_t)stream));
 }
 
+// Whether the steps stay where the stored values are in range (newton.hip):
+// |x| and |x|^2 below 2, the factor of a step below 4, with room for rounding.
+bool newton_in_range(const mq_newton& p) {
+  const double a = p.a, b = p.b, c = p.c;
+  double top = 1.0;  // of the singular values before the step
+  for (int s = 0; s < p.steps; s++) {
+    const double y1 = top * top * 1.002;
+    if (!(y1 < 1.99)) return false;
+    // extremes over y = x^2 in [0, y1]: the ends and the stationary points
+    double most_f = fmax(fabs(a), fabs(a + y1 * (b + c * y1))), most_p = 0;
+    if (c != 0) {
+      const double y = -b / (2 * c);
+      if (y > 0 && y < y1) most_f = fmax(most_f, fabs(a + y * (b + c * y)));
+    }
+    if (!(most_f < 3.99)) return false;
+    auto take = [&](double y) {
+      if (y >= 0 && y <= y1) most_p = fmax(most_p, fabs(sqrt(y) * (a + y * (b + c * y))));
+    };
+    take(y1);
+    if (c != 0) {
+      const double d = 9 * b * b - 20 * a * c;
+      if (d >= 0) {
+        take((-3 * b + sqrt(d)) / (10 * c));
+        take((-3 * b - sqrt(d)) / (10 * c));
+      }
+    } else if (b != 0) {
+      take(-a / (3 * b));
+    }
+    top = most_p;
+  }
+  return true;
+}
+
+bool finite(float v) { return v - v == 0.0f; }
+
+int check_newton(const mq_newton& p) {
+  if (p.steps < 1 || p.steps > MQ_NEWTON_STEPS_MAX) return MQ_ERR_UNSUPPORTED;
+  if (!finite(p.a) || !finite(p.b) || !finite(p.c) || !finite(p.eps) || !(p.eps >= 0.0f)) return MQ_ERR_UNSUPPORTED;
+  return newton_in_range(p) ? MQ_OK : MQ_ERR_UNSUPPORTED;
+}
+
+bool matrices_ok(int32_t count, const int32_t* rows, const int32_t* cols) {
+  if (count < 1 || count > MQ_UPDATE_GROUP_MAX) return false;
+  for (int i = 0; i < count; i++)
+    if (rows[i] < 1 || cols[i] < 1 || rows[i] >= 1 << 30 || cols[i] >= 1 << 30 || !newton_shape_ok(rows[i], cols[i]))
+      return false;
+  return true;
+}
+
+int check_matrices(int32_t count, const int32_t* rows, const int32_t* cols, const float* const* in, float* const* mom,
+                   bool update, float* const* out, const void* ws, size_t ws_bytes) {
+  if (!rows || !cols || !in || !out || (update && !mom)) return MQ_ERR_NULL;
+  if (!matrices_ok(count, rows, cols)) return MQ_ERR_SHAPE;
+  for (int i = 0; i < count; i++) {
+    if (!in[i] || !out[i] || (update && !mom[i])) return MQ_ERR_NULL;
+    if (!aligned4(in[i]) || !aligned4(out[i]) || (update && !aligned4(mom[i]))) return MQ_ERR_ALIGN;
+  }
+  if (!ws || ws_bytes < newton_workspace_bytes(count, rows, cols)) return MQ_ERR_WORKSPACE;
+  return aligned16(ws) ? MQ_OK : MQ_ERR_ALIGN;
+}
+
 }  // namespace
 
 extern "C" {
@@ -90,6 +153,38 @@ int mqconv_layer_norm_backward_mx(const mq_layer_norm* ln, const float* dy, cons
                                   const float* mean, const float* rstd, const float* dskip, mq_mx dxq, float* dgamma,
                                   float* dbeta, void* ws, size_t ws_bytes, void* stream) {
   return layer_norm_backward(ln, dy, x, gamma, mean, rstd, dskip, nullptr, &dxq, dgamma, dbeta, ws, ws_bytes, stream);
+}
+
+size_t mqconv_orthogonalize_workspace_bytes(int32_t count, const int32_t* rows, const int32_t* cols) {
+  if (!rows || !cols || !matrices_ok(count, rows, cols)) return 0;
+  return newton_workspace_bytes(count, rows, cols);
+}
+
+int mqconv_orthogonalize(const mq_newton* newton, int32_t count, const int32_t* rows, const int32_t* cols,
+                         const float* const* u, float* const* x, void* ws, size_t ws_bytes, void* stream) {
+  if (!newton) return MQ_ERR_NULL;
+  int e = check_newton(*newton);
+  if (e != MQ_OK) return e;
+  if ((e = check_matrices(count, rows, cols, u, nullptr, false, x, ws, ws_bytes)) != MQ_OK) return e;
+  UpdateSpec s{};
+  s.steps = newton->steps; s.a = newton->a; s.b = newton->b; s.c = newton->c; s.eps = newton->eps;
+  return hip_status(launch_newton(s, count, rows, cols, u, nullptr, x, ws, (hipStream_t)stream));
+}
+
+int mqconv_muon_update(const mq_muon* opt, int32_t count, const int32_t* rows, const int32_t* cols,
+                       const float* const* g, float* const* m, float* const* w, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (!opt) return MQ_ERR_NULL;
+  int e = check_newton(opt->newton);
+  if (e != MQ_OK) return e;
+  if (!finite(opt->lr) || !finite(opt->momentum) || !finite(opt->decay) || (opt->nesterov & ~1)) return MQ_ERR_UNSUPPORTED;
+  if (opt->scale < MQ_SCALE_NONE || opt->scale > MQ_SCALE_RMS) return MQ_ERR_FORMAT;
+  if (!aligned4(opt->rate)) return MQ_ERR_ALIGN;
+  if ((e = check_matrices(count, rows, cols, g, m, true, w, ws, ws_bytes)) != MQ_OK) return e;
+  const mq_newton& n = opt->newton;
+  const UpdateSpec s{n.steps, n.a, n.b, n.c, n.eps, opt->momentum, opt->decay, opt->lr, opt->nesterov != 0, opt->scale,
+                     opt->rate};
+  return hip_status(launch_newton(s, count, rows, cols, g, m, w, ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

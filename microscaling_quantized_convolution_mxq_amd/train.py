@@ -1,6 +1,6 @@
-"""Binding of include/mqconv_train.h: layer norm. Same names as the C entry
-points; only arguments are marshalled here. Descriptors may be kept and used
-again by the program that made them."""
+"""Binding of include/mqconv_train.h: layer norm and the orthogonalised weight
+update. Same names as the C entry points; only arguments are marshalled here.
+Descriptors may be kept and used again by the program that made them."""
 from __future__ import annotations
 
 import ctypes
@@ -20,9 +20,36 @@ class mq_layer_norm(ctypes.Structure):
         super().__init__(*_int32("mq_layer_norm", h, w, n, c), eps)
 
 
+MUON_SCALE_NONE, MUON_SCALE_ASPECT, MUON_SCALE_RMS = 0, 1, 2
+UPDATE_GROUP_MAX = 32
+
+
+class mq_newton(ctypes.Structure):
+    """Newton-Schulz steps of p(x) = a x + b x^3 + c x^5."""
+    _fields_ = [("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+    def __init__(self, steps: int = 5, a: float = 3.4445, b: float = -4.7750, c: float = 2.0315, eps: float = 1e-7):
+        super().__init__(*_int32("mq_newton", steps), a, b, c, eps)
+
+
+class mq_muon(ctypes.Structure):
+    """The optimizer step around them. `rate`: None, or a one-element float32
+    GPU tensor that multiplies lr when the kernel runs (a captured graph then
+    follows a schedule)."""
+    _fields_ = [("newton", mq_newton), ("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("decay", ctypes.c_float),
+                ("nesterov", ctypes.c_int32), ("scale", ctypes.c_int32), ("rate", ctypes.c_void_p)]
+
+    def __init__(self, lr: float, momentum: float = 0.95, decay: float = 0.0, nesterov: bool = True,
+                 scale: int = MUON_SCALE_ASPECT, newton: Optional[mq_newton] = None, rate=None):
+        super().__init__(newton or mq_newton(), lr, momentum, decay, *_int32("mq_muon", int(nesterov), scale),
+                         _mq._buf(rate, 4, "float32", "rate"))
+        self._rate = rate  # its memory is read by every call
+
+
 EXPORTED_TRAIN = (
     "mqconv_layer_norm_workspace_bytes", "mqconv_layer_norm", "mqconv_layer_norm_mx", "mqconv_layer_norm_backward",
-    "mqconv_layer_norm_backward_mx")
+    "mqconv_layer_norm_backward_mx", "mqconv_orthogonalize_workspace_bytes", "mqconv_orthogonalize", "mqconv_muon_update")
 
 _fns = None
 
@@ -40,6 +67,12 @@ def _lib():
             "mqconv_layer_norm_mx": (I, [LN, P, P, P, P, P, MX, P, P, P, S, P]),
             "mqconv_layer_norm_backward": (I, [LN, P, P, P, P, P, P, P, P, P, P, S, P]),
             "mqconv_layer_norm_backward_mx": (I, [LN, P, P, P, P, P, P, MX, P, P, P, S, P]),
+        }
+        NE, MU = ctypes.POINTER(mq_newton), ctypes.POINTER(mq_muon)
+        sig |= {
+            "mqconv_orthogonalize_workspace_bytes": (S, [I, P, P]),
+            "mqconv_orthogonalize": (I, [NE, I, P, P, P, P, P, S, P]),
+            "mqconv_muon_update": (I, [MU, I, P, P, P, P, P, P, S, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -111,3 +144,58 @@ def mqconv_layer_norm_backward_mx(norm: mq_layer_norm, dy, x, gamma, mean, rstd,
         ctypes.byref(s), *_layer_grad_inputs(s, dy, x, gamma, mean, rstd, dskip), dxq.c_struct("dxq"),
         _maybe(dgamma, s.c, "dgamma"), _maybe(dbeta, s.c, "dbeta"), p, nb, _mq._stream(stream)),
         "mqconv_layer_norm_backward_mx")
+
+
+# ---- orthogonalised weight update ---------------------------------------------------------------
+def _matrix(shape):
+    """(rows, cols) of a weight: its first extent and the product of the others."""
+    if len(shape) < 1:
+        raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, "shape", "a weight has at least one extent")
+    return _int32("shape", int(shape[0]), _mq._prod(shape[1:]))
+
+
+def _matrices(shapes):
+    """(count, rows, cols) as the C calls take them."""
+    pairs = [_matrix(s) for s in shapes]
+    n = len(pairs)
+    of = lambda k: (ctypes.c_int32 * max(1, n))(*(p[k] for p in pairs))  # noqa: E731
+    return n, of(0), of(1)
+
+
+def _addresses(tensors, shapes, what: str):
+    if len(tensors) != len(shapes):
+        raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, what, f"{len(tensors)} tensors for {len(shapes)} matrices")
+    return (ctypes.c_void_p * max(1, len(tensors)))(
+        *(_floats(t, _mq._prod(s), f"{what}[{i}]") for i, (t, s) in enumerate(zip(tensors, shapes))))
+
+
+def _shapes_of(tensors, what: str):
+    tensors = list(tensors)
+    for t in tensors:
+        if not hasattr(t, "shape"):
+            raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, what, "tensors give the sizes")
+    return tensors, [tuple(t.shape) for t in tensors]
+
+
+def mqconv_orthogonalize_workspace_bytes(shapes) -> int:
+    """Workspace for weights of these shapes ([rows, ...] each)."""
+    return _lib().mqconv_orthogonalize_workspace_bytes(*_matrices(shapes))
+
+
+def mqconv_orthogonalize(newton: mq_newton, u, x, ws=None, stream=None) -> None:
+    """x[i] = the orthogonalised u[i], for lists of up to UPDATE_GROUP_MAX tensors [rows, ...]."""
+    u, shapes = _shapes_of(u, "u")
+    p, nb = _mq._ws(ws)
+    _mq._check(_lib().mqconv_orthogonalize(
+        ctypes.byref(newton), *_matrices(shapes), _addresses(u, shapes, "u"), _addresses(list(x), shapes, "x"), p, nb,
+        _mq._stream(stream)), "mqconv_orthogonalize")
+
+
+def mqconv_muon_update(opt: mq_muon, grads, momenta, weights, ws=None, stream=None) -> None:
+    """One step of up to UPDATE_GROUP_MAX weights [rows, ...] and their momenta, in place."""
+    grads, shapes = _shapes_of(grads, "grads")
+    p, nb = _mq._ws(ws)
+    _mq._check(_lib().mqconv_muon_update(
+        ctypes.byref(opt), *_matrices(shapes), _addresses(grads, shapes, "grads"),
+        _addresses(list(momenta), shapes, "momenta"), _addresses(list(weights), shapes, "weights"), p, nb,
+        _mq._stream(stream)), "mqconv_muon_update")

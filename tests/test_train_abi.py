@@ -73,6 +73,72 @@ def test_layer_norm_refusals():
     assert L.mqconv_layer_norm_backward(None, FAKE, FAKE, None, FAKE, FAKE, None, FAKE, None, None, FAKE, 1 << 20, None) == NULL
 
 
+# ---- orthogonalised update ----------------------------------------------------------------------
+class FakeMatrix(FakeWorkspace):
+    """An fp32 weight as the binding sees one, at an address that is never used."""
+
+    def __init__(self, shape, at=FAKE):
+        import torch
+        super().__init__(4 * max(1, abs(mq._prod(shape))), at)
+        self.shape, self.dtype = shape, torch.float32
+
+
+def test_orthogonalize_workspace_sizes():
+    ws = mq.mqconv_orthogonalize_workspace_bytes
+    for shapes in ([(1, 1)], [(64, 3, 3, 64)], [(16, 27), (32, 144), (2048, 4096)], [(7, 5, 5, 3)] * 32, [(1, 10**6)], [(10**6,)]):
+        up = lambda v: (v + 31) // 32 * 32  # noqa: E731
+        planes = 0
+        for s in shapes:
+            m, n = sorted((s[0], mq._prod(s[1:])))
+            planes += 4 * (3 * up(m) * up(n) + 2 * up(m) ** 2)
+        assert planes < ws(shapes) <= 1.5 * planes + len(shapes) * 16384
+    assert ws([]) == 0 and ws([(4, 4)] * 33) == 0 and ws([(0, 4)]) == 0 and ws([(4, -1)]) == 0
+    assert ws([(23169, 23169)]) == 0 and ws([(23168, 23168)]) > 0 and ws([(32, 2**24)]) == 0 and ws([(2**30 + 1, 1)]) == 0
+    with pytest.raises(mq.MqConvError):
+        ws([(2**32 + 4, 4)])
+    assert mq.train._lib().mqconv_orthogonalize_workspace_bytes(1, None, None) == 0
+
+
+def test_update_refusals():
+    ws = FakeWorkspace(1 << 20)
+    M = FakeMatrix
+    orth = lambda n=mq.mq_newton(), u=None, x=None, w=ws: _status(  # noqa: E731
+        mq.mqconv_orthogonalize, n, [M((8, 8))] if u is None else u, [M((8, 8))] if x is None else x, w)
+    assert orth(u=[], x=[]) == SHAPE and orth(u=[M((8, 8))] * 33, x=[M((8, 8))] * 33) == SHAPE
+    assert orth(u=[M((8, 0))], x=[M((8, 0))]) == SHAPE and orth(x=[]) == SHAPE and orth(x=[M((4, 8))]) == SHAPE
+    assert orth(u=[M((23169, 23169))], x=[M((23169, 23169))]) == SHAPE
+    assert orth(u=[M((8, 8), 0)]) == NULL and orth(x=[M((8, 8), 0)]) == NULL
+    assert orth(u=[M((8, 8), FAKE + 2)]) == ALIGN and orth(x=[M((8, 8), FAKE + 1)]) == ALIGN
+    assert orth(w=None) == WORKSPACE and orth(w=FakeWorkspace(4096)) == WORKSPACE and orth(w=FakeWorkspace(1 << 20, FAKE + 8)) == ALIGN
+    N = mq.mq_newton
+    nan, inf = float("nan"), float("inf")
+    for bad in (N(0), N(33), N(-1), N(5, eps=-1e-7), N(5, eps=nan), N(5, eps=inf), N(5, a=nan), N(5, b=inf), N(5, c=nan),
+                # values that leave the stored range: a step's factor of 4, a polynomial that grows, one that does in its third step
+                N(1, 4.0, 0.0, 0.0), N(5, 2.0, 0.0, 0.0), N(3, 1.2, 0.0, 0.0), N(1, 1.0, 3.5, 0.0), N(9, 3.9, -6.0, 3.2)):
+        assert orth(n=bad) == UNSUPPORTED, (bad.steps, bad.a, bad.b, bad.c, bad.eps)
+    for good in (N(), N(32), N(1, 1.5, -0.5, 0.0), N(32, 1.5, -0.5, 0.0), N(10, 15 / 8, -10 / 8, 3 / 8), N(2, 1.2, 0.0, 0.0),
+                 N(12, 2.0, -1.5, 0.5), N(5, 0.0, 0.0, 0.0)):
+        assert orth(n=good, w=None) == WORKSPACE, (good.steps, good.a, good.b, good.c)
+
+    upd = lambda o=mq.mq_muon(0.1), g=None, m=None, p=None, w=ws: _status(  # noqa: E731
+        mq.mqconv_muon_update, o, *([M((8, 8))] if t is None else t for t in (g, m, p)), w)
+    U = mq.mq_muon
+    for bad in (U(nan), U(0.1, inf), U(0.1, 0.9, nan), U(0.1, nesterov=2), U(0.1, newton=N(0))):
+        assert upd(o=bad) == UNSUPPORTED
+    assert upd(o=U(0.1, scale=3)) == FORMAT and upd(o=U(0.1, scale=-1)) == FORMAT and upd(o=U(0.1, rate=FAKE + 2)) == ALIGN
+    for k in ("g", "m", "p"):
+        assert upd(**{k: [M((8, 8), 0)]}) == NULL and upd(**{k: [M((8, 8), FAKE + 2)]}) == ALIGN
+    assert upd(m=[M((8, 4))]) == SHAPE and upd(p=[]) == SHAPE and upd(w=FakeWorkspace(64)) == WORKSPACE
+    L = mq.train._lib()
+    assert L.mqconv_orthogonalize(None, 1, None, None, None, None, FAKE, 1 << 20, None) == NULL
+    assert L.mqconv_muon_update(None, 1, None, None, None, None, None, FAKE, 1 << 20, None) == NULL
+    import ctypes
+    one = (ctypes.c_int32 * 1)(8)
+    p = (ctypes.c_void_p * 1)(FAKE)
+    assert L.mqconv_orthogonalize(ctypes.byref(N()), 1, one, one, None, p, FAKE, 1 << 20, None) == NULL
+    assert L.mqconv_muon_update(ctypes.byref(U(0.1)), 1, one, one, p, None, p, FAKE, 1 << 20, None) == NULL
+
+
 # ---- the same under the host sanitizers ---------------------------------------------------------
 def test_refusals_under_host_sanitizers():
     if os.environ.get("MQCONV_LIB"):
