@@ -91,8 +91,10 @@ struct RowLoader {
 struct Bf16 {};
 struct Split {};
 
-template <class T, int TM, int TN>
-__device__ __forceinline__ void mma_step(const uint8_t* a, const uint8_t* b, int lane, v16f (&acc)[TM][TN]) {
+// acc, and for Split `low`: sums of the products of a high and a low part.
+template <class T, int TM, int TN, int LM, int LN>
+__device__ __forceinline__ void mma_step(const uint8_t* a, const uint8_t* b, int lane, v16f (&acc)[TM][TN],
+                                         v16f (&low)[LM][LN]) {
   const int r = lane & 31, q = lane >> 5, sw = (r >> 1) & 7;
   const uint8_t* const ar = a + r * kPiece;
   const uint8_t* const br = b + r * kPiece;
@@ -125,15 +127,15 @@ __device__ __forceinline__ void mma_step(const uint8_t* a, const uint8_t* b, int
         yh[j] = *reinterpret_cast<const half8*>(br + 32 * j * kPiece + hi);
         yl[j] = *reinterpret_cast<const half8*>(br + 32 * j * kPiece + lo);
       }
-      // the small products first, each kind over all tiles before the next
+      // (each kind over all tiles before the next, so that no instruction waits for the one before it)
 #pragma unroll
       for (int i = 0; i < TM; i++)
 #pragma unroll
-        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl[i], yh[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < TN; j++) low[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xl[i], yh[j], low[i][j], 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < TM; i++)
 #pragma unroll
-        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[i], yl[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < TN; j++) low[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xh[i], yl[j], low[i][j], 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < TM; i++)
 #pragma unroll
@@ -142,8 +144,31 @@ __device__ __forceinline__ void mma_step(const uint8_t* a, const uint8_t* b, int
   }
 }
 
+template <class S>
+__device__ __forceinline__ void mma_zero(v16f (&acc)[S::TM][S::TN]) {
+#pragma unroll
+  for (int i = 0; i < S::TM; i++)
+#pragma unroll
+    for (int j = 0; j < S::TN; j++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+}
+template <class S>
+__device__ __forceinline__ void mma_add(v16f (&a)[S::TM][S::TN], const v16f (&b)[S::TM][S::TN]) {
+#pragma unroll
+  for (int i = 0; i < S::TM; i++)
+#pragma unroll
+    for (int j = 0; j < S::TN; j++) a[i][j] += b[i][j];
+}
+
 // The steps step0 .. step0 + n - 1 of a tile. Loaders: issue(step, lds, wave)
 // makes L loads of every wave, whatever the step is.
+//
+// The matrix units align the 16 products of an instruction to the largest of
+// them and the accumulator, and drop what lies below 2^-26 of that (measured: 1
+// + 16 x 2^-27 stays 1, 1 + 4 x 2^-25 does not). The products with a low part
+// are 2^-11 of the others, so they have accumulators of their own, and the two
+// are added at the end.
 template <class T, class S, class LA, class LB>
 __device__ __forceinline__ void mma_loop(uint8_t* lds, LA& la, LB& lb, int step0, int n, int wave, int lane,
                                          v16f (&acc)[S::TM][S::TN]) {
@@ -158,16 +183,20 @@ __device__ __forceinline__ void mma_loop(uint8_t* lds, LA& la, LB& lb, int step0
   for (int s = 0; s < ST - 1; s++)
     if (s < n) issue(s, s);
   int slot = 0, fill = ST - 1;
+  constexpr bool LOW = std::is_same<T, Split>::value;
+  v16f low[LOW ? S::TM : 1][LOW ? S::TN : 1];
+  if constexpr (LOW) mma_zero<S>(low);
   for (int s = 0; s < n; s++) {
     // step s has arrived once only the ST - 2 steps behind it are under way
     if (s + ST - 2 < n) stage_ready<(ST - 2) * LPS>();
     else stage_ready<0>();
     if (s + ST - 1 < n) issue(s + ST - 1, fill);
     const uint8_t* const at = lds + slot * S::STAGE;
-    mma_step<T, S::TM, S::TN>(at + wm * S::TM * 32 * kPiece, at + (S::BM + wn * S::TN * 32) * kPiece, lane, acc);
+    mma_step<T, S::TM, S::TN>(at + wm * S::TM * 32 * kPiece, at + (S::BM + wn * S::TN * 32) * kPiece, lane, acc, low);
     slot = slot + 1 == ST ? 0 : slot + 1;
     fill = fill + 1 == ST ? 0 : fill + 1;
   }
+  if constexpr (LOW) mma_add<S>(acc, low);
 }
 
 // f(row, column, quad): the four values of rows row .. row + 3 in one column, of a wave's results.
@@ -183,16 +212,6 @@ __device__ __forceinline__ void mma_results(const v16f (&acc)[S::TM][S::TN], int
         const float v[4] = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
         f((wm * S::TM + i) * 32 + 8 * e + 4 * (lane >> 5), (wn * S::TN + j) * 32 + (lane & 31), v);
       }
-}
-
-template <class S>
-__device__ __forceinline__ void mma_zero(v16f (&acc)[S::TM][S::TN]) {
-#pragma unroll
-  for (int i = 0; i < S::TM; i++)
-#pragma unroll
-    for (int j = 0; j < S::TN; j++)
-#pragma unroll
-      for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
 }
 
 // Workgroups go to the eight XCDs in turn; this gives each XCD a contiguous

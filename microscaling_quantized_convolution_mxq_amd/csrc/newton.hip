@@ -202,7 +202,7 @@ __device__ __forceinline__ void triangle(int k, int t, int& i, int& j) {
 }
 
 template <int KIND, class S>
-__global__ __launch_bounds__(S::THREADS) void newton_kernel(const Group g) {
+__global__ __launch_bounds__(S::THREADS, 2) void newton_kernel(const Group g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int local;
