@@ -1,8 +1,9 @@
 /*
  * mqconv_train.h -- C ABI of what a layer needs, beside the calls of mqconv.h
  * and mqconv_block.h, to be trained in the two-level 4-bit format: layer
- * normalization over the channels (forward and backward), and the
- * orthogonalised update of the weights.
+ * normalization over the channels (forward and backward), the three products
+ * of a convolution on two-level codes, and the orthogonalised update of the
+ * weights.
  *
  * The conventions of mqconv.h hold: device pointers owned by the caller, work
  * enqueued on `stream`, every argument checked before any HIP call, an
@@ -71,6 +72,43 @@ int mqconv_layer_norm_backward(const mq_layer_norm* ln, const float* dy, const f
 int mqconv_layer_norm_backward_mx(const mq_layer_norm* ln, const float* dy, const float* x, const float* gamma,
                                   const float* mean, const float* rstd, const float* dskip, mq_mx dxq, float* dgamma,
                                   float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Products of two-level codes
+ * ---------------------------------------------------------------------------
+ * The three products of a convolution (mqconv.h; a linear layer is a 1 x 1
+ * convolution of a 1 x 1 image whose samples are its rows) on operands that
+ * mqconv_nvfp_quantize wrote, each quantized once: its blocks of 8 x 8 serve the
+ * sums along either of their sides. An element's value is value(q) * B * T;
+ * value(q) * B is exact in 16 bits, products are exact, sums fp32 (products
+ * below 2^-26 of a sum may be lost in it), and T T' is applied to them. A block
+ * with the scale byte 0x7F (NaN) makes every output that it is part of NaN. */
+typedef struct {
+  const void* codes;           /* device, 16-byte aligned: the packed layout of the role */
+  const uint8_t* block_scales; /* device: E4M3 bytes (mqconv_nvfp_scales_bytes) */
+  const float* tensor_scale;   /* device, 4-byte aligned: one value */
+  mq_elem fmt;
+  mq_role role;
+  int32_t d0, d1, d2, d3;      /* ACT/GRAD: (H, W, N, C); WEIGHT: (Cout, Kh, Kw, Cin) */
+} mq_nvfp;
+
+/* Workspace (device bytes, 16-byte aligned); op 0 forward, 1 backward data, 2
+ * backward weight, fa/fb the operands' formats in the order of the call. 0 for
+ * invalid arguments, and where an operand's rounded-up size (channels to 64;
+ * backward weight: samples to 8 instead) is 2^30 - 128 elements or more, which
+ * the calls refuse with MQ_ERR_SHAPE. */
+size_t mqconv_nvfp_gemm_workspace_bytes(const mq_conv* cv, int op, mq_elem fa, mq_elem fb);
+
+/* Y: fp32 [Ho][Wo][N][Cout], fully overwritten. xq ACT, wq WEIGHT, any formats. */
+int mqconv_nvfp_forward(const mq_conv* cv, mq_nvfp xq, mq_nvfp wq, float* y, void* ws, size_t ws_bytes, void* stream);
+
+/* dX: fp32 [H][W][N][Cin], fully overwritten. dyq GRAD, wq WEIGHT. */
+int mqconv_nvfp_backward_data(const mq_conv* cv, mq_nvfp dyq, mq_nvfp wq, float* dx, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* dW: fp32 [Cout][Kh][Kw][Cin], fully overwritten. dyq GRAD, xq ACT. */
+int mqconv_nvfp_backward_weight(const mq_conv* cv, mq_nvfp dyq, mq_nvfp xq, float* dw, void* ws, size_t ws_bytes,
+                                void* stream);
 
 /* ---------------------------------------------------------------------------
  * Orthogonalised weight update (Newton-Schulz steps, as the Muon optimizer's)

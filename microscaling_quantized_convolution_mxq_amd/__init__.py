@@ -468,6 +468,7 @@ from .block import (ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, CACHE_COUNT_MAX, EXP
 
 # ---- a layer's norm, products and update (include/mqconv_train.h) --------------------
 from .train import (EXPORTED_TRAIN, MUON_SCALE_ASPECT, MUON_SCALE_NONE, MUON_SCALE_RMS, UPDATE_GROUP_MAX,  # noqa: E402,F401
-                    mq_layer_norm, mq_muon, mq_newton, mqconv_layer_norm, mqconv_layer_norm_backward,
+                    NvfpTensor, mq_layer_norm, mq_muon, mq_newton, mq_nvfp, mqconv_layer_norm, mqconv_layer_norm_backward,
                     mqconv_layer_norm_backward_mx, mqconv_layer_norm_mx, mqconv_layer_norm_workspace_bytes,
-                    mqconv_muon_update, mqconv_orthogonalize, mqconv_orthogonalize_workspace_bytes)
+                    mqconv_muon_update, mqconv_nvfp_backward_data, mqconv_nvfp_backward_weight, mqconv_nvfp_forward,
+                    mqconv_nvfp_gemm_workspace_bytes, mqconv_orthogonalize, mqconv_orthogonalize_workspace_bytes)

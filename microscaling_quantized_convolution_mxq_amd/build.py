@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libmqconv.so")
 SOURCES = ["quantize.hip", "layout.hip", "gemm_fwd.hip", "gemm_fwd_mx.hip", "gemm_dgrad.hip", "gemm_dgrad_mx.hip", "gemm_dgrad_mx_relaid.hip", "gemm_wgrad.hip", "gemm_wgrad_sub.hip", "gemm_plain.hip",
            "naive.hip", "cuyckens.hip", "nvfp.hip", "mqconv_api.hip",
            "dropout.hip", "norm.hip", "norm_mx.hip", "cache.hip", "block_api.hip",
-           "layer_norm.hip", "layer_norm_mx.hip", "newton.hip", "train_api.hip"]
+           "layer_norm.hip", "layer_norm_mx.hip", "newton.hip", "nvfp_gemm.hip", "train_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

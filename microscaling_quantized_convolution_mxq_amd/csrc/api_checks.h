@@ -35,6 +35,33 @@ inline int check_mx(const mq_mx& t, mq_role role, int32_t d0, int32_t d1, int32_
   return MQ_OK;
 }
 
+// Element counts of the conv's tensors (0 if the geometry is invalid).
+inline bool conv_ok(const mq_conv* c) {
+  if (!c) return false;
+  if (c->n < 1 || c->cin < 1 || c->h < 1 || c->w < 1 || c->cout < 1) return false;
+  if (c->kh < 1 || c->kw < 1 || c->kh > 15 || c->kw > 15) return false;
+  if (c->stride_h < 1 || c->stride_w < 1 || c->stride_h > 8 || c->stride_w > 8) return false;
+  if (c->pad_h < 0 || c->pad_w < 0 || c->pad_h >= c->kh || c->pad_w >= c->kw) return false;
+  long long ho = ((long long)c->h + 2LL * c->pad_h - c->kh) / c->stride_h + 1;
+  long long wo = ((long long)c->w + 2LL * c->pad_w - c->kw) / c->stride_w + 1;
+  if (c->h + 2LL * c->pad_h < c->kh || c->w + 2LL * c->pad_w < c->kw) return false;
+  if (ho < 1 || wo < 1) return false;
+  long long cpi = ((long long)c->cin + 31) / 32 * 32, cpo = ((long long)c->cout + 31) / 32 * 32;
+  long long npad = ((long long)c->n + 31) / 32 * 32;
+  if ((long long)c->h * c->w * npad * cpi > kMaxElems) return false;
+  if (ho * wo * npad * cpo > kMaxElems) return false;
+  if (ho * wo * c->n * (long long)c->kh * c->kw * cpi > kMaxElems) return false;
+  if ((long long)c->cout * c->kh * c->kw * cpi > kMaxElems) return false;
+  return true;
+}
+
+inline Conv to_conv(const mq_conv* c) {
+  Conv v;
+  v.n = c->n; v.cin = c->cin; v.h = c->h; v.w = c->w; v.cout = c->cout; v.kh = c->kh; v.kw = c->kw;
+  v.sh = c->stride_h; v.sw = c->stride_w; v.ph = c->pad_h; v.pw = c->pad_w;
+  return v;
+}
+
 inline MxOutView out_view(const mq_mx& t) {
   return MxOutView{static_cast<uint8_t*>(t.codes), t.scales, t.fmt, t.block_partner};
 }

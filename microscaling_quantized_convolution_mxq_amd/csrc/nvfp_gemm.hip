@@ -1,0 +1,620 @@
+// nvfp_gemm.hip -- the three products of a convolution on two-level codes.
+//
+// An operand's value is q B T: element code, E4M3 scale of its 8 x 8 block,
+// fp32 scale of the tensor. q B has at most 8 significant bits in every format
+// (E4M3 and E2M3 elements 4, times 4 of the scale), so it is a bf16 exactly,
+// and the products q B q' B' are exact in the bf16 matrix units; T T' multiplies
+// the sums. A block of 8 x 8 has one scale for 8 values along either product's
+// k, where the block-scaled matrix instructions take a power of two for 32, so
+// values are made first:
+//   1. both operands are written as bf16 with k contiguous, channels (weight
+//      gradient: samples) padded with zeros;
+//   2. a product gathers rows of 128 bytes (64 values of k) from them: of the
+//      pixel that a tap reaches, or past the end of the buffer, which reads as
+//      zeros, outside the image.
+//   forward:   Y[(ho wo n)][co] = sum over (kh kw ci) of X[..] W[co][..]
+//   data:      dX[(h w n)][ci] = sum over (kh kw co) of dY[..] W'[ci][..], the
+//              rows in classes of equal (h mod stride, w mod stride), which
+//              have the same taps
+//   weight:    dW[co][(kh kw ci)] = sum over (ho wo n) of dY'[co][..] X'[ci][..]
+//              with the operands transposed in step 1
+// Few tiles with long sums are split along k into slices, whose sums a last
+// kernel adds in a fixed order.
+#include <math.h>
+
+#include <algorithm>
+
+#include "mma_core.h"
+#include "train.h"
+
+namespace mq {
+
+namespace {
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+// ---- values of codes ----------------------------------------------------------------------------
+// Eight neighbouring codes (4, 6 or 8 bytes at p) as floats.
+template <int F>
+__device__ __forceinline__ void decode8(const uint8_t* p, float (&v)[8]) {
+  if constexpr (Fmt<F>::bits == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      v2f a, b;
+      if constexpr (F == 0) {
+        a = __builtin_amdgcn_cvt_pk_f32_fp8(u[i], false);
+        b = __builtin_amdgcn_cvt_pk_f32_fp8(u[i], true);
+      } else {
+        a = __builtin_amdgcn_cvt_pk_f32_bf8(u[i], false);
+        b = __builtin_amdgcn_cvt_pk_f32_bf8(u[i], true);
+      }
+      v[4 * i] = a[0]; v[4 * i + 1] = a[1]; v[4 * i + 2] = b[0]; v[4 * i + 3] = b[1];
+    }
+  } else if constexpr (Fmt<F>::bits == 6) {
+    const uint16_t* const h = reinterpret_cast<const uint16_t*>(p);
+    const uint64_t w = (uint64_t)h[0] | (uint64_t)h[1] << 16 | (uint64_t)h[2] << 32;
+    // magnitude bits as the top of an fp32's: its exponent is off by 127 - bias, subnormals included
+    constexpr float up = __builtin_bit_cast(float, (uint32_t)(254 - Fmt<F>::bias) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint32_t c = (uint32_t)(w >> (6 * i));
+      v[i] = __uint_as_float((c & 31u) << (23 - Fmt<F>::M) | (c & 32u) << 26) * up;
+    }
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1),
+              c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+    v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1]; v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
+  }
+}
+
+// An operand as the quantizer wrote it: an [A][P][B] x C view, P the partner index.
+struct Codes {
+  const uint8_t *codes, *scales;
+  int fmt, A, P, B, C;
+  int rbytes, nPB, nCB;  // bytes of a row's codes; blocks along P and C
+};
+
+Codes codes_of(const NvfpView& t, int A, int P, int B, int C) {
+  return Codes{t.codes, t.scales, t.fmt, A, P, B, C, (int)row_bytes(t.fmt, C), ceil_div(P, 8), ceil_div(C, 8)};
+}
+
+// Channels 8 ch .. 8 ch + 7 of row (ab, p) as bf16; zeros past C.
+template <int F>
+__device__ __forceinline__ bhalf8 values8(const Codes& t, long long row, int ab, int p, int ch) {
+  bhalf8 o;
+  float v[8];
+  const int c0 = 8 * ch;
+  if (c0 < t.C) {
+    decode8<F>(t.codes + row * t.rbytes + (c0 >> 5) * run_bytes_of(F) + (c0 & 31) * Fmt<F>::bits / 8, v);
+    const float s = __builtin_amdgcn_cvt_f32_fp8(t.scales[((long long)ab * t.nPB + (p >> 3)) * t.nCB + ch], 0);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = c0 + i < t.C ? v[i] * s : 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) o[i] = (__bf16)v[i];
+  return o;
+}
+
+// out[row][Cp], Cp a multiple of 64: 8 channels a thread.
+struct RowsArgs {
+  Codes t;
+  __bf16* out;
+  int n;  // pieces of 8 channels
+  FastDiv pieces, dP, dB;
+};
+template <int F>
+__global__ __launch_bounds__(256) void nvfp_rows_kernel(const RowsArgs a) {
+  const unsigned i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= (unsigned)a.n) return;
+  const unsigned row = fdiv(i, a.pieces), ch = i - row * a.pieces.d;
+  const unsigned q = fdiv(row, a.dB), b = row - q * a.dB.d, aa = fdiv(q, a.dP), p = q - aa * a.dP.d;
+  *reinterpret_cast<bhalf8*>(a.out + (long long)i * 8) = values8<F>(a.t, row, (int)(aa * a.dB.d + b), (int)p, (int)ch);
+}
+
+// out[c][ab][Pp], Pp a multiple of 8: tiles of 64 channels x 64 of the (ab, p).
+struct AcrossArgs {
+  Codes t;
+  __bf16* out;
+  int Pp, S, tiles;  // S = A B Pp; tiles along S
+  FastDiv dPp, dB;
+};
+template <int F>
+__global__ __launch_bounds__(256) void nvfp_across_kernel(const AcrossArgs a) {
+  constexpr int PITCH = 66;  // (eight threads of one slot write 8 channels each: 264 dwords apart, eight banks)
+  __shared__ __attribute__((aligned(16))) __bf16 tile[64 * PITCH];
+  const int ct = blockIdx.x / a.tiles, s0 = (blockIdx.x - ct * a.tiles) * 64, c0 = ct * 64;
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int ch = i & 7, slot = i >> 3, s = s0 + slot;
+    bhalf8 v;
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = (__bf16)0.0f;
+    if (s < a.S) {
+      const unsigned ab = fdiv((unsigned)s, a.dPp), p = (unsigned)s - ab * a.dPp.d;
+      if ((int)p < a.t.P) {
+        const unsigned aa = fdiv(ab, a.dB), b = ab - aa * a.dB.d;
+        v = values8<F>(a.t, ((long long)aa * a.t.P + p) * a.dB.d + b, (int)ab, (int)p, (c0 >> 3) + ch);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) tile[(8 * ch + e) * PITCH + slot] = v[e];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int k = i & 7, c = i >> 3, s = s0 + 8 * k;
+    if (c0 + c >= a.t.C || s >= a.S) continue;
+    uint4 w;
+    const uint32_t* const from = reinterpret_cast<const uint32_t*>(tile + c * PITCH + 8 * k);
+    w.x = from[0]; w.y = from[1]; w.z = from[2]; w.w = from[3];
+    *reinterpret_cast<uint4*>(a.out + (long long)(c0 + c) * a.S + s) = w;
+  }
+}
+
+template <class L>
+hipError_t with_format(int fmt, L&& launch) {
+  switch (fmt) {
+    case 0: launch(std::integral_constant<int, 0>{}); break;
+    case 1: launch(std::integral_constant<int, 1>{}); break;
+    case 2: launch(std::integral_constant<int, 2>{}); break;
+    case 3: launch(std::integral_constant<int, 3>{}); break;
+    default: launch(std::integral_constant<int, 4>{}); break;
+  }
+  return launch_check();
+}
+
+long long up(long long v, int m) { return (v + m - 1) / m * m; }
+
+hipError_t launch_rows(const Codes& t, __bf16* out, hipStream_t st) {
+  const int cp = (int)up(t.C, 64);
+  RowsArgs a{t, out, (int)((long long)t.A * t.P * t.B * (cp / 8)), make_fastdiv(cp / 8), make_fastdiv(t.P), make_fastdiv(t.B)};
+  return with_format(t.fmt, [&](auto f) {
+    hipLaunchKernelGGL(nvfp_rows_kernel<decltype(f)::value>, dim3((unsigned)((a.n + 255LL) / 256)), dim3(256), 0, st, a);
+  });
+}
+hipError_t launch_across(const Codes& t, __bf16* out, int pad, hipStream_t st) {
+  AcrossArgs a{t, out, (int)up(t.P, pad), 0, 0, make_fastdiv((unsigned)up(t.P, pad)), make_fastdiv(t.B)};
+  a.S = t.A * t.B * a.Pp;
+  a.tiles = ceil_div(a.S, 64);
+  return with_format(t.fmt, [&](auto f) {
+    hipLaunchKernelGGL(nvfp_across_kernel<decltype(f)::value>, dim3((unsigned)(a.tiles * ceil_div(t.C, 64))), dim3(256), 0, st, a);
+  });
+}
+
+// ---- products -----------------------------------------------------------------------------------
+// Rows of an image of pixels, each the channels (64 cb) of a pixel's sample, moved by the taps of a step. Output row (r, c, n)
+// starts at pixel (r sr + r0, c sc + c0), and tap (i, j) is at (+-i, +-j) from there.
+struct Gather {
+  const __bf16* p;
+  long long bytes;
+  int H, W, N, row;      // row: bytes of a row (pixel and sample)
+  int Wr, M;             // columns of the output's pixels, output rows
+  int sr, sc, r0, c0, dir;
+  FastDiv dN, dW;
+};
+// The steps of a sum over taps (i, j) and blocks of 64 channels; the other operand's rows have taps (k0 + s i) KW + l0 + s j.
+struct Taps {
+  int ni, nj, nc;  // taps, and blocks of 64 channels
+  int k0, l0, si, sj, KW;
+};
+
+template <int L, int NW>
+struct GatherLoader {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int off[L], h[L], w[L];
+  int H, W, pix, dir, nj, nc, i, j, cb;
+  __device__ void init(const Gather& g, const Taps& t, int row0, int step0, int wave, int lane) {
+    rsrc = mma_rsrc(g.p, g.bytes);
+    H = g.H; W = g.W; pix = g.N * g.row; dir = g.dir; nj = t.nj; nc = t.nc;
+    const int tap = step0 / t.nc;
+    cb = step0 - tap * t.nc; i = tap / t.nj; j = tap - i * t.nj;
+#pragma unroll
+    for (int k = 0; k < L; k++) {
+      const int m = row0 + lane_row<NW>(wave, lane, k);
+      const unsigned px = fdiv((unsigned)m, g.dN), n = (unsigned)m - px * g.dN.d, r = fdiv(px, g.dW), c = px - r * g.dW.d;
+      h[k] = (int)r * g.sr + g.r0;
+      w[k] = (int)c * g.sc + g.c0;
+      off[k] = (int)(((unsigned)(h[k] * g.W + w[k]) * (unsigned)g.N + n) * (unsigned)g.row) + lane_chunk(wave, lane) * 16;
+      if (m >= g.M) h[k] = -(1 << 20);  // (no tap leads back into the image from there)
+    }
+  }
+  // (steps are asked for in order)
+  __device__ void issue(int, uint8_t* lds, int wave) {
+    const int di = dir * i, dj = dir * j, move = (di * W + dj) * pix;
+#pragma unroll
+    for (int k = 0; k < L; k++) {
+      const bool in = (unsigned)(h[k] + di) < (unsigned)H && (unsigned)(w[k] + dj) < (unsigned)W;
+      load_lds16(rsrc, lds + (wave + NW * k) * 1024, in ? off[k] + move : kBeyond, cb * kPiece);
+    }
+    if (++cb == nc) {
+      cb = 0;
+      if (++j == nj) { j = 0; i++; }
+    }
+  }
+};
+
+template <int L, int NW>
+struct TapLoader {
+  RowLoader<L, NW> rows;
+  int nj, nc, i, j, cb;
+  Taps t;
+  __device__ void init(const void* p, long long bytes, int row0, int n, int pitch, const Taps& taps, int step0, int wave, int lane) {
+    rows.init(p, bytes, row0, n, pitch, wave, lane);
+    t = taps;
+    const int tap = step0 / t.nc;
+    cb = step0 - tap * t.nc; i = tap / t.nj; j = tap - i * t.nj;
+  }
+  __device__ void issue(int, uint8_t* lds, int wave) {
+    rows.issue(((t.k0 + t.si * i) * t.KW + t.l0 + t.sj * j) * t.nc + cb, lds, wave);
+    if (++cb == t.nc) {
+      cb = 0;
+      if (++j == t.nj) { j = 0; i++; }
+    }
+  }
+};
+
+// dY' [co][pixel][Np]: rows of `pieces` 16-byte pieces, which need not end with a step
+template <int L, int NW>
+struct EndLoader {
+  RowLoader<L, NW> rows;
+  int pieces, chunk;
+  __device__ void init(const void* p, long long bytes, int row0, int n, int count, int wave, int lane) {
+    rows.init(p, bytes, row0, n, count * 16, wave, lane);
+    pieces = count;
+    chunk = lane_chunk(wave, lane);
+  }
+  __device__ void issue(int step, uint8_t* lds, int wave) const {
+    const bool in = step * 8 + chunk < pieces;
+#pragma unroll
+    for (int j = 0; j < L; j++)
+      load_lds16(rows.rsrc, lds + (wave + NW * j) * 1024, in ? rows.off[j] : kBeyond, step * kPiece);
+  }
+};
+
+// X' [ci][H][W][Np] for the columns (kh, kw, ci) of dW: piece q of the sum is samples 8 n8 .. of output pixel q / (Np / 8)
+struct Shift {
+  const __bf16* p;
+  long long bytes;
+  int H, W, Cin, KW, Np, sr, sc, pr, pc;
+  int cols, pieces;  // columns of dW; pieces of a sum
+  FastDiv dC, dK, dN, dW;  // by Cin, KW, Np / 8 and Wo
+};
+template <int L, int NW>
+struct ShiftLoader {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int off[L], h[L], w[L], chunk;
+  const Shift* s;
+  __device__ void init(const Shift& g, int col0, int wave, int lane) {
+    rsrc = mma_rsrc(g.p, g.bytes);
+    s = &g;
+    chunk = lane_chunk(wave, lane);
+#pragma unroll
+    for (int k = 0; k < L; k++) {
+      const int col = col0 + lane_row<NW>(wave, lane, k);
+      const unsigned tap = fdiv((unsigned)col, g.dC), ci = (unsigned)col - tap * g.dC.d, kh = fdiv(tap, g.dK), kw = tap - kh * g.dK.d;
+      h[k] = (int)kh - g.pr;
+      w[k] = (int)kw - g.pc;
+      off[k] = (int)((unsigned)(((int)ci * g.H + h[k]) * g.W + w[k]) * (unsigned)(g.Np * 2));
+      if (col >= g.cols) h[k] = -(1 << 20);
+    }
+  }
+  __device__ void issue(int step, uint8_t* lds, int wave) const {
+    const unsigned q = step * 8 + chunk, px = fdiv(q, s->dN), n8 = q - px * s->dN.d, r = fdiv(px, s->dW), c = px - r * s->dW.d;
+    const int w0 = (int)c * s->sc, h0 = (int)q < s->pieces ? (int)r * s->sr : -(1 << 20);
+    const int at = (int)((r * (unsigned)(s->sr * s->W) + (unsigned)w0) * (unsigned)(s->Np * 2) + n8 * 16u);
+#pragma unroll
+    for (int k = 0; k < L; k++) {
+      const bool in = (unsigned)(h[k] + h0) < (unsigned)s->H && (unsigned)(w[k] + w0) < (unsigned)s->W;
+      load_lds16(rsrc, lds + (wave + NW * k) * 1024, in ? off[k] + at : kBeyond, 0);
+    }
+  }
+};
+
+// Sums times the tensors' scales: the product of the two in fp64 as a mantissa and a power of two, as it may leave fp32's range.
+struct Scale {
+  float m;
+  int e;
+  __device__ float operator()(float v) const { return ldexpf(v * m, e); }
+};
+__device__ __forceinline__ Scale scale_of(const float* a, const float* b) {
+  Scale s;
+  s.m = (float)frexp((double)*a * (double)*b, &s.e);
+  return s;
+}
+
+constexpr int kClasses = 64;  // stride 8 both ways
+
+struct Class {
+  Gather g;
+  Taps t;
+  int first;         // its first tile
+  int h0, w0;        // its pixels are (r sh + h0, c sw + w0)
+};
+
+struct ConvArgs {
+  const __bf16* b;
+  long long b_bytes;
+  int b_pitch, cols;  // bytes of a row of the other operand; its rows, the output's columns
+  float* out;         // or the slices
+  const float *ta, *tb;
+  int slices;
+  long long slice;   // values of a slice
+  int sh, sw, W, N;  // where a class's rows are in the output
+  int tiles, nclass;
+  bool classes;      // rows go by classes (backward data)
+};
+
+// One class's arguments travel in the kernel arguments, several in device memory.
+template <class S>
+__device__ __forceinline__ void conv_tile(const ConvArgs& a, const Class& k, int tile, int z, uint8_t* lds) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tn = (a.cols + S::BN - 1) / S::BN;
+  const int ti = tile / tn, i0 = ti * S::BM, j0 = (tile - ti * tn) * S::BN;
+  const int steps = k.t.ni * k.t.nj * k.t.nc, s0 = (int)((long long)steps * z / a.slices),
+            s1 = (int)((long long)steps * (z + 1) / a.slices);
+  v16f acc[S::TM][S::TN];
+  mma_zero<S>(acc);
+  if (s1 > s0) {
+    GatherLoader<S::LA, S::NW> la;
+    TapLoader<S::LB, S::NW> lb;
+    la.init(k.g, k.t, i0, s0, wave, lane);
+    lb.init(a.b, a.b_bytes, j0, a.cols, a.b_pitch, k.t, s0, wave, lane);
+    mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, wave, lane, acc);
+  }
+  Scale scale{1.0f, 0};
+  if (a.slices == 1) scale = scale_of(a.ta, a.tb);
+  float* const out = a.out + z * (a.slices == 1 ? 0 : a.slice);
+  mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&v)[4]) {
+    const int col = j0 + c;
+    if (col >= a.cols) return;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const int m = i0 + r + e;
+      if (m >= k.g.M) break;
+      long long row = m;
+      if (a.classes) {
+        const unsigned px = fdiv((unsigned)m, k.g.dN), n = (unsigned)m - px * k.g.dN.d, pr = fdiv(px, k.g.dW), pc = px - pr * k.g.dW.d;
+        row = ((long long)((int)pr * a.sh + k.h0) * a.W + (int)pc * a.sw + k.w0) * a.N + n;
+      }
+      out[row * a.cols + col] = a.slices == 1 ? scale(v[e]) : v[e];
+    }
+  });
+}
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS, 2) void nvfp_conv_kernel(const ConvArgs a, const Class k) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles;
+  conv_tile<S>(a, k, b - z * a.tiles, z, lds);
+}
+
+struct WeightArgs {
+  const __bf16* dy;
+  long long dy_bytes;
+  Shift x;
+  int rows;
+  float* out;
+  const float *ta, *tb;
+  int slices, tiles, steps;
+  long long slice;
+};
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS, 2) void nvfp_weight_kernel(const WeightArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles, tile = b - z * a.tiles;
+  const int tn = (a.x.cols + S::BN - 1) / S::BN;
+  const int ti = tile / tn, i0 = ti * S::BM, j0 = (tile - ti * tn) * S::BN;
+  const int s0 = (int)((long long)a.steps * z / a.slices), s1 = (int)((long long)a.steps * (z + 1) / a.slices);
+  v16f acc[S::TM][S::TN];
+  mma_zero<S>(acc);
+  EndLoader<S::LA, S::NW> la;
+  ShiftLoader<S::LB, S::NW> lb;
+  la.init(a.dy, a.dy_bytes, i0, a.rows, a.x.pieces, wave, lane);
+  lb.init(a.x, j0, wave, lane);
+  mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, wave, lane, acc);
+  Scale scale{1.0f, 0};
+  if (a.slices == 1) scale = scale_of(a.ta, a.tb);
+  float* const out = a.out + z * (a.slices == 1 ? 0 : a.slice);
+  mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&v)[4]) {
+    const int col = j0 + c;
+    if (col >= a.x.cols) return;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (i0 + r + e < a.rows) out[(long long)(i0 + r + e) * a.x.cols + col] = a.slices == 1 ? scale(v[e]) : v[e];
+  });
+}
+
+// The slices' sums, added in order (fp64), times the tensors' scales.
+__global__ __launch_bounds__(256) void nvfp_join_kernel(const float* part, float* out, long long n, int slices, const float* ta,
+                                                        const float* tb) {
+  const Scale scale = scale_of(ta, tb);
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    double s = 0;
+    for (int z = 0; z < slices; z++) s += part[z * n + i];
+    out[i] = scale((float)s);
+  }
+}
+
+// ---- plans --------------------------------------------------------------------------------------
+typedef MmaShape<256, 256, 2, 4, 2> Big;
+typedef MmaShape<128, 128, 2, 2, 2> Mid;
+typedef MmaShape<256, 64, 4, 1, 2> Tall;
+typedef MmaShape<64, 64, 2, 2, 3> Small;
+
+// Tiles by the output's extents, and slices along k where these tiles do not fill the chip.
+struct Plan {
+  int shape;  // 0 Big, 1 Mid, 2 Tall, 3 Small
+  int slices;
+};
+const int kBM[4] = {256, 128, 256, 64}, kBN[4] = {256, 128, 64, 64};
+Plan plan_of(long long M, long long N, long long steps) {
+  auto tiles = [&](int s) { return (long long)ceil_div(M, kBM[s]) * ceil_div(N, kBN[s]); };
+  Plan p{3, 1};
+  if (N > 128 && M > 128 && tiles(0) >= 200) p.shape = 0;
+  else if (N <= 64 && M >= 256 && tiles(2) >= 200) p.shape = 2;
+  else if (N > 64 && M > 64 && tiles(1) * std::max(1LL, steps / 8) >= 256) p.shape = 1;
+  const long long t = tiles(p.shape), want = 512 / std::max(1LL, t);
+  // slices of eight steps at least, and no more sums than operands' bytes by far
+  if (want >= 2) p.slices = (int)std::max(1LL, std::min({want, steps / 8, 64LL}));
+  return p;
+}
+
+template <class F>
+void with_shape(int s, F&& f) {
+  switch (s) {
+    case 0: f(Big{}); break;
+    case 1: f(Mid{}); break;
+    case 2: f(Tall{}); break;
+    default: f(Small{}); break;
+  }
+}
+
+struct Sizes {
+  long long a, b, part;  // bytes of the operands and the slices
+  Plan plan;
+};
+
+// the longest sum of a class of rows
+int class_taps(int k, int stride) { return ceil_div(k, stride); }
+
+Sizes sizes_of(const Conv& c, int op) {
+  const long long ho = c.ho(), wo = c.wo(), taps = (long long)c.kh * c.kw;
+  Sizes s{};
+  long long out;
+  if (op == 0) {
+    const long long cp = up(c.cin, 64);
+    s.a = (long long)c.h * c.w * c.n * cp * 2;
+    s.b = c.cout * taps * cp * 2;
+    s.plan = plan_of(ho * wo * c.n, c.cout, taps * (cp / 64));
+    out = ho * wo * c.n * c.cout;
+  } else if (op == 1) {
+    const long long kp = up(c.cout, 64);
+    s.a = ho * wo * c.n * kp * 2;
+    s.b = c.cin * taps * kp * 2;
+    s.plan = plan_of((long long)c.h * c.w * c.n, c.cin, (long long)class_taps(c.kh, c.sh) * class_taps(c.kw, c.sw) * (kp / 64));
+    out = (long long)c.h * c.w * c.n * c.cin;
+  } else {
+    const long long np = up(c.n, 8);
+    s.a = c.cout * ho * wo * np * 2;
+    s.b = (long long)c.cin * c.h * c.w * np * 2;
+    s.plan = plan_of(c.cout, taps * c.cin, (ho * wo * np + 63) / 64);
+    out = c.cout * taps * c.cin;
+  }
+  s.part = s.plan.slices > 1 ? out * 4 * s.plan.slices : 0;
+  return s;
+}
+
+}  // namespace
+
+bool nvfp_gemm_ok(const Conv& c, int op) {
+  const Sizes s = sizes_of(c, op);
+  return s.a < kBeyond && s.b < kBeyond;
+}
+
+size_t nvfp_gemm_workspace_bytes(const Conv& c, int op) {
+  const Sizes s = sizes_of(c, op);
+  return (size_t)(up(s.a, 256) + up(s.b, 256) + s.part);
+}
+
+static hipError_t join(const Sizes& s, const float* part, float* out, long long n, const float* ta, const float* tb, hipStream_t st) {
+  if (s.plan.slices == 1) return hipSuccess;
+  hipLaunchKernelGGL(nvfp_join_kernel, dim3((unsigned)std::min<long long>(ceil_div(n, 256), 4096)), dim3(256), 0, st, part, out, n,
+                     s.plan.slices, ta, tb);
+  return launch_check();
+}
+
+hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView& w, float* y, void* ws, hipStream_t st) {
+  const Sizes s = sizes_of(c, 0);
+  const int cp = (int)up(c.cin, 64), taps = c.kh * c.kw, ho = c.ho(), wo = c.wo();
+  __bf16* const xb = static_cast<__bf16*>(ws);
+  __bf16* const wb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
+  hipError_t e = launch_rows(codes_of(x, c.h * c.w, c.n, 1, c.cin), xb, st);
+  if (e != hipSuccess) return e;
+  if ((e = launch_rows(codes_of(w, 1, c.cout, taps, c.cin), wb, st)) != hipSuccess) return e;
+  Class k{};
+  k.g = Gather{xb, s.a, c.h, c.w, c.n, cp * 2, wo, ho * wo * c.n, c.sh, c.sw, -c.ph, -c.pw, 1, make_fastdiv(c.n), make_fastdiv(wo)};
+  k.t = Taps{c.kh, c.kw, cp / 64, 0, 0, 1, 1, c.kw};
+  ConvArgs a{};
+  a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * cp * 2; a.cols = c.cout;
+  a.slices = s.plan.slices; a.slice = (long long)k.g.M * c.cout;
+  a.out = a.slices > 1 ? part : y;
+  a.ta = x.tensor; a.tb = w.tensor;
+  a.tiles = ceil_div(k.g.M, kBM[s.plan.shape]) * ceil_div(c.cout, kBN[s.plan.shape]);
+  with_shape(s.plan.shape, [&](auto shape) {
+    typedef decltype(shape) S;
+    hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a, k);
+  });
+  if ((e = launch_check()) != hipSuccess) return e;
+  return join(s, part, y, a.slice, a.ta, a.tb, st);
+}
+
+hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const NvfpView& w, float* dx, void* ws, hipStream_t st) {
+  const Sizes s = sizes_of(c, 1);
+  const int kp = (int)up(c.cout, 64), taps = c.kh * c.kw, ho = c.ho(), wo = c.wo();
+  __bf16* const yb = static_cast<__bf16*>(ws);
+  __bf16* const wb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
+  hipError_t e = launch_rows(codes_of(dy, ho * wo, c.n, 1, c.cout), yb, st);
+  if (e != hipSuccess) return e;
+  if ((e = launch_across(codes_of(w, 1, c.cout, taps, c.cin), wb, 64, st)) != hipSuccess) return e;
+  ConvArgs a{};
+  a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * kp * 2; a.cols = c.cin;
+  a.slices = s.plan.slices; a.slice = (long long)c.h * c.w * c.n * c.cin;
+  a.out = a.slices > 1 ? part : dx;
+  a.ta = dy.tensor; a.tb = w.tensor;
+  a.sh = c.sh; a.sw = c.sw; a.W = c.w; a.N = c.n;
+  a.classes = c.sh > 1 || c.sw > 1;
+  for (int h = 0; h < std::min(c.sh, c.h); h++)
+    for (int v = 0; v < std::min(c.sw, c.w); v++) {
+      const int k0 = (h + c.ph) % c.sh, l0 = (v + c.pw) % c.sw;
+      const int rows = ceil_div(c.h - h, c.sh), cols = ceil_div(c.w - v, c.sw);
+      Class k{};
+      k.h0 = h; k.w0 = v;
+      k.g = Gather{yb, s.a, ho, wo, c.n, kp * 2, cols, rows * cols * c.n, 1, 1, (h + c.ph - k0) / c.sh, (v + c.pw - l0) / c.sw, -1,
+                   make_fastdiv(c.n), make_fastdiv(cols)};
+      k.t = Taps{k0 < c.kh ? ceil_div(c.kh - k0, c.sh) : 0, l0 < c.kw ? ceil_div(c.kw - l0, c.sw) : 0, kp / 64, k0, l0, c.sh, c.sw, c.kw};
+      if (k.t.ni == 0 || k.t.nj == 0) k.t.ni = 0, k.t.nj = 1;  // (no tap reaches these pixels: zeros)
+      a.tiles = ceil_div(k.g.M, kBM[s.plan.shape]) * ceil_div(c.cin, kBN[s.plan.shape]);
+      with_shape(s.plan.shape, [&](auto shape) {
+        typedef decltype(shape) S;
+        hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a, k);
+      });
+      if ((e = launch_check()) != hipSuccess) return e;
+    }
+  return join(s, part, dx, a.slice, a.ta, a.tb, st);
+}
+
+hipError_t launch_nvfp_backward_weight(const Conv& c, const NvfpView& dy, const NvfpView& x, float* dw, void* ws, hipStream_t st) {
+  const Sizes s = sizes_of(c, 2);
+  const int np = (int)up(c.n, 8), taps = c.kh * c.kw, ho = c.ho(), wo = c.wo();
+  __bf16* const yb = static_cast<__bf16*>(ws);
+  __bf16* const xb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
+  hipError_t e = launch_across(codes_of(dy, ho * wo, c.n, 1, c.cout), yb, 8, st);
+  if (e != hipSuccess) return e;
+  if ((e = launch_across(codes_of(x, c.h * c.w, c.n, 1, c.cin), xb, 8, st)) != hipSuccess) return e;
+  WeightArgs a{};
+  a.dy = yb; a.dy_bytes = s.a; a.rows = c.cout;
+  a.x = Shift{xb, s.b, c.h, c.w, c.cin, c.kw, np, c.sh, c.sw, c.ph, c.pw, taps * c.cin, ho * wo * (np / 8), make_fastdiv(c.cin),
+              make_fastdiv(c.kw), make_fastdiv(np / 8), make_fastdiv(wo)};
+  a.slices = s.plan.slices; a.slice = (long long)c.cout * taps * c.cin;
+  a.out = a.slices > 1 ? part : dw;
+  a.ta = dy.tensor; a.tb = x.tensor;
+  a.steps = ceil_div(a.x.pieces, 8);
+  a.tiles = ceil_div(c.cout, kBM[s.plan.shape]) * ceil_div(a.x.cols, kBN[s.plan.shape]);
+  with_shape(s.plan.shape, [&](auto shape) {
+    typedef decltype(shape) S;
+    hipLaunchKernelGGL(nvfp_weight_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a);
+  });
+  if ((e = launch_check()) != hipSuccess) return e;
+  return join(s, part, dw, a.slice, a.ta, a.tb, st);
+}
+
+}  // namespace mq

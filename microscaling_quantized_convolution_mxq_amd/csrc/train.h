@@ -20,6 +20,19 @@ hipError_t launch_layer_norm_backward(const LnShape& s, const float* dy, const f
                                       const float* mean, const float* rstd, const float* dskip, float* dx,
                                       const MxOutView& dxq, float* dgamma, float* dbeta, void* ws, hipStream_t st);
 
+// An operand of the two-level products.
+struct NvfpView {
+  const uint8_t *codes, *scales;
+  const float* tensor;
+  int fmt;
+};
+// whether the products' 16-bit operands stay within 32-bit offsets; op 0 forward, 1 backward data, 2 backward weight
+bool nvfp_gemm_ok(const Conv& c, int op);
+size_t nvfp_gemm_workspace_bytes(const Conv& c, int op);
+hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView& w, float* y, void* ws, hipStream_t st);
+hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const NvfpView& w, float* dx, void* ws, hipStream_t st);
+hipError_t launch_nvfp_backward_weight(const Conv& c, const NvfpView& dy, const NvfpView& x, float* dw, void* ws, hipStream_t st);
+
 // The weight update: Newton-Schulz steps, and the optimizer around them.
 constexpr int kUpdateGroup = 32;  // MQ_UPDATE_GROUP_MAX
 struct UpdateSpec {

@@ -61,6 +61,23 @@ int layer_norm_backward(const mq_layer_norm* ln, const float* dy, const float* x
                                                dgamma, dbeta, ws, (hipStream_t)stream));
 }
 
+int check_nvfp(const mq_nvfp& t, mq_role role, int32_t d0, int32_t d1, int32_t d2, int32_t d3, NvfpView* v) {
+  if (!t.codes || !t.block_scales || !t.tensor_scale) return MQ_ERR_NULL;
+  if (!fmt_ok(t.fmt) || t.role != role) return MQ_ERR_FORMAT;
+  if (t.d0 != d0 || t.d1 != d1 || t.d2 != d2 || t.d3 != d3) return MQ_ERR_SHAPE;
+  if (!aligned16(t.codes) || !aligned4(t.tensor_scale)) return MQ_ERR_ALIGN;
+  *v = NvfpView{static_cast<const uint8_t*>(t.codes), t.block_scales, t.tensor_scale, t.fmt};
+  return MQ_OK;
+}
+
+int check_product(const mq_conv* cv, int op, const float* out, const void* ws, size_t ws_bytes) {
+  if (!nvfp_gemm_ok(to_conv(cv), op)) return MQ_ERR_SHAPE;
+  if (!out) return MQ_ERR_NULL;
+  if (!aligned4(out)) return MQ_ERR_ALIGN;
+  if (!ws || ws_bytes < nvfp_gemm_workspace_bytes(to_conv(cv), op)) return MQ_ERR_WORKSPACE;
+  return aligned16(ws) ? MQ_OK : MQ_ERR_ALIGN;
+}
+
 // Whether the steps stay where the stored values are in range (newton.hip):
 // |x| and |x|^2 below 2, the factor of a step below 4, with room for rounding.
 bool newton_in_range(const mq_newton& p) {
@@ -153,6 +170,48 @@ int mqconv_layer_norm_backward_mx(const mq_layer_norm* ln, const float* dy, cons
                                   const float* mean, const float* rstd, const float* dskip, mq_mx dxq, float* dgamma,
                                   float* dbeta, void* ws, size_t ws_bytes, void* stream) {
   return layer_norm_backward(ln, dy, x, gamma, mean, rstd, dskip, nullptr, &dxq, dgamma, dbeta, ws, ws_bytes, stream);
+}
+
+size_t mqconv_nvfp_gemm_workspace_bytes(const mq_conv* cv, int op, mq_elem fa, mq_elem fb) {
+  if (!conv_ok(cv) || op < 0 || op > 2 || !fmt_ok(fa) || !fmt_ok(fb) || !nvfp_gemm_ok(to_conv(cv), op)) return 0;
+  return nvfp_gemm_workspace_bytes(to_conv(cv), op);
+}
+
+int mqconv_nvfp_forward(const mq_conv* cv, mq_nvfp xq, mq_nvfp wq, float* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!cv) return MQ_ERR_NULL;
+  if (!conv_ok(cv)) return MQ_ERR_SHAPE;
+  NvfpView x, w;
+  int e = check_nvfp(xq, MQ_ROLE_ACT, cv->h, cv->w, cv->n, cv->cin, &x);
+  if (e != MQ_OK) return e;
+  if ((e = check_nvfp(wq, MQ_ROLE_WEIGHT, cv->cout, cv->kh, cv->kw, cv->cin, &w)) != MQ_OK) return e;
+  if ((e = check_product(cv, 0, y, ws, ws_bytes)) != MQ_OK) return e;
+  return hip_status(launch_nvfp_forward(to_conv(cv), x, w, y, ws, (hipStream_t)stream));
+}
+
+int mqconv_nvfp_backward_data(const mq_conv* cv, mq_nvfp dyq, mq_nvfp wq, float* dx, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (!cv) return MQ_ERR_NULL;
+  if (!conv_ok(cv)) return MQ_ERR_SHAPE;
+  const Conv c = to_conv(cv);
+  NvfpView dy, w;
+  int e = check_nvfp(dyq, MQ_ROLE_GRAD, c.ho(), c.wo(), c.n, c.cout, &dy);
+  if (e != MQ_OK) return e;
+  if ((e = check_nvfp(wq, MQ_ROLE_WEIGHT, c.cout, c.kh, c.kw, c.cin, &w)) != MQ_OK) return e;
+  if ((e = check_product(cv, 1, dx, ws, ws_bytes)) != MQ_OK) return e;
+  return hip_status(launch_nvfp_backward_data(c, dy, w, dx, ws, (hipStream_t)stream));
+}
+
+int mqconv_nvfp_backward_weight(const mq_conv* cv, mq_nvfp dyq, mq_nvfp xq, float* dw, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (!cv) return MQ_ERR_NULL;
+  if (!conv_ok(cv)) return MQ_ERR_SHAPE;
+  const Conv c = to_conv(cv);
+  NvfpView dy, x;
+  int e = check_nvfp(dyq, MQ_ROLE_GRAD, c.ho(), c.wo(), c.n, c.cout, &dy);
+  if (e != MQ_OK) return e;
+  if ((e = check_nvfp(xq, MQ_ROLE_ACT, c.h, c.w, c.n, c.cin, &x)) != MQ_OK) return e;
+  if ((e = check_product(cv, 2, dw, ws, ws_bytes)) != MQ_OK) return e;
+  return hip_status(launch_nvfp_backward_weight(c, dy, x, dw, ws, (hipStream_t)stream));
 }
 
 size_t mqconv_orthogonalize_workspace_bytes(int32_t count, const int32_t* rows, const int32_t* cols) {

@@ -1,10 +1,11 @@
-"""Binding of include/mqconv_train.h: layer norm and the orthogonalised weight
-update. Same names as the C entry points; only arguments are marshalled here.
+"""Binding of include/mqconv_train.h: layer norm, the products of two-level
+codes and the orthogonalised weight update. Same names as the C entry points; only arguments are marshalled here.
 Descriptors may be kept and used again by the program that made them."""
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+import dataclasses
+from typing import Optional, Sequence, Tuple
 
 import microscaling_quantized_convolution_mxq_amd as _mq
 
@@ -18,6 +19,12 @@ class mq_layer_norm(ctypes.Structure):
 
     def __init__(self, h: int, w: int, n: int, c: int, eps: float = 1e-5):
         super().__init__(*_int32("mq_layer_norm", h, w, n, c), eps)
+
+
+class mq_nvfp(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("block_scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p),
+                ("fmt", ctypes.c_int32), ("role", ctypes.c_int32), ("d0", ctypes.c_int32), ("d1", ctypes.c_int32),
+                ("d2", ctypes.c_int32), ("d3", ctypes.c_int32)]
 
 
 MUON_SCALE_NONE, MUON_SCALE_ASPECT, MUON_SCALE_RMS = 0, 1, 2
@@ -49,7 +56,8 @@ class mq_muon(ctypes.Structure):
 
 EXPORTED_TRAIN = (
     "mqconv_layer_norm_workspace_bytes", "mqconv_layer_norm", "mqconv_layer_norm_mx", "mqconv_layer_norm_backward",
-    "mqconv_layer_norm_backward_mx", "mqconv_orthogonalize_workspace_bytes", "mqconv_orthogonalize", "mqconv_muon_update")
+    "mqconv_layer_norm_backward_mx", "mqconv_nvfp_gemm_workspace_bytes", "mqconv_nvfp_forward",
+    "mqconv_nvfp_backward_data", "mqconv_nvfp_backward_weight", "mqconv_orthogonalize_workspace_bytes", "mqconv_orthogonalize", "mqconv_muon_update")
 
 _fns = None
 
@@ -69,7 +77,12 @@ def _lib():
             "mqconv_layer_norm_backward_mx": (I, [LN, P, P, P, P, P, P, MX, P, P, P, S, P]),
         }
         NE, MU = ctypes.POINTER(mq_newton), ctypes.POINTER(mq_muon)
+        CV, NV = ctypes.POINTER(_mq.mq_conv), mq_nvfp
         sig |= {
+            "mqconv_nvfp_gemm_workspace_bytes": (S, [CV, I, I, I]),
+            "mqconv_nvfp_forward": (I, [CV, NV, NV, P, P, S, P]),
+            "mqconv_nvfp_backward_data": (I, [CV, NV, NV, P, P, S, P]),
+            "mqconv_nvfp_backward_weight": (I, [CV, NV, NV, P, P, S, P]),
             "mqconv_orthogonalize_workspace_bytes": (S, [I, P, P]),
             "mqconv_orthogonalize": (I, [NE, I, P, P, P, P, P, S, P]),
             "mqconv_muon_update": (I, [MU, I, P, P, P, P, P, P, S, P]),
@@ -144,6 +157,72 @@ def mqconv_layer_norm_backward_mx(norm: mq_layer_norm, dy, x, gamma, mean, rstd,
         ctypes.byref(s), *_layer_grad_inputs(s, dy, x, gamma, mean, rstd, dskip), dxq.c_struct("dxq"),
         _maybe(dgamma, s.c, "dgamma"), _maybe(dbeta, s.c, "dbeta"), p, nb, _mq._stream(stream)),
         "mqconv_layer_norm_backward_mx")
+
+
+# ---- products of two-level codes ----------------------------------------------------------------
+@dataclasses.dataclass
+class NvfpTensor:
+    """A two-level tensor on the device, as mqconv_nvfp_quantize writes it."""
+    codes: object  # torch.uint8 tensor
+    scales: object  # torch.uint8 tensor: the blocks' E4M3 bytes
+    tensor_scale: object  # torch.float32 tensor of one value
+    fmt: int
+    role: int
+    dims: Tuple[int, int, int, int]
+
+    @staticmethod
+    def empty(role: int, fmt: int, dims: Sequence[int], device="cuda") -> "NvfpTensor":
+        import torch
+        d = _int32("NvfpTensor.empty", *(int(v) for v in dims))
+        nc, ns = _mq.mqconv_codes_bytes(role, fmt, *d), _mq.mqconv_nvfp_scales_bytes(role, *d)
+        if nc == 0 or ns == 0:
+            raise _mq.MqConvError(_mq.MQ_ERR_SHAPE, "NvfpTensor.empty")
+        return NvfpTensor(torch.empty(nc, dtype=torch.uint8, device=device),
+                          torch.empty(ns, dtype=torch.uint8, device=device),
+                          torch.empty(1, dtype=torch.float32, device=device), fmt, role, d)
+
+    def quantize(self, src, ws, stream=None) -> None:
+        """mqconv_nvfp_quantize of src into this tensor (ws: mqconv_nvfp_workspace_bytes() bytes)."""
+        _mq.mqconv_nvfp_quantize(src, self.role, self.fmt, self.dims, self.codes, self.scales, self.tensor_scale, ws, stream)
+
+    def c_struct(self, what: str = "NvfpTensor") -> mq_nvfp:
+        """The C view; tensor buffers are checked against the sizes the layout needs."""
+        d = _int32(what, *self.dims)
+        return mq_nvfp(_mq._buf(self.codes, _mq.mqconv_codes_bytes(self.role, self.fmt, *d), "uint8", what + ".codes"),
+                       _mq._buf(self.scales, _mq.mqconv_nvfp_scales_bytes(self.role, *d), "uint8", what + ".scales"),
+                       _mq._f32(self.tensor_scale, 1, what + ".tensor_scale"), self.fmt, self.role, *d)
+
+
+def _conv32(shape) -> _mq.mq_conv:
+    t = shape.as_tuple() if hasattr(shape, "as_tuple") else tuple(shape)
+    return _mq.mq_conv(*_int32("shape", *t))
+
+
+def mqconv_nvfp_gemm_workspace_bytes(shape, op: int, fa: int, fb: int) -> int:
+    return _lib().mqconv_nvfp_gemm_workspace_bytes(ctypes.byref(_conv32(shape)), op, fa, fb)
+
+
+def mqconv_nvfp_forward(shape, xq: NvfpTensor, wq: NvfpTensor, y, ws=None, stream=None) -> None:
+    c = _conv32(shape)
+    p, n = _mq._ws(ws)
+    _mq._check(_lib().mqconv_nvfp_forward(ctypes.byref(c), xq.c_struct("xq"), wq.c_struct("wq"),
+                                          _floats(y, _mq._ny(shape), "y"), p, n, _mq._stream(stream)), "mqconv_nvfp_forward")
+
+
+def mqconv_nvfp_backward_data(shape, dyq: NvfpTensor, wq: NvfpTensor, dx, ws=None, stream=None) -> None:
+    c = _conv32(shape)
+    p, n = _mq._ws(ws)
+    _mq._check(_lib().mqconv_nvfp_backward_data(ctypes.byref(c), dyq.c_struct("dyq"), wq.c_struct("wq"),
+                                                _floats(dx, _mq._nx(shape), "dx"), p, n, _mq._stream(stream)),
+               "mqconv_nvfp_backward_data")
+
+
+def mqconv_nvfp_backward_weight(shape, dyq: NvfpTensor, xq: NvfpTensor, dw, ws=None, stream=None) -> None:
+    c = _conv32(shape)
+    p, n = _mq._ws(ws)
+    _mq._check(_lib().mqconv_nvfp_backward_weight(ctypes.byref(c), dyq.c_struct("dyq"), xq.c_struct("xq"),
+                                                  _floats(dw, _mq._nw(shape), "dw"), p, n, _mq._stream(stream)),
+               "mqconv_nvfp_backward_weight")
 
 
 # ---- orthogonalised weight update ---------------------------------------------------------------

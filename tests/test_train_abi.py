@@ -73,6 +73,63 @@ def test_layer_norm_refusals():
     assert L.mqconv_layer_norm_backward(None, FAKE, FAKE, None, FAKE, FAKE, None, FAKE, None, None, FAKE, 1 << 20, None) == NULL
 
 
+# ---- products of two-level codes ----------------------------------------------------------------
+CONV = (3, 24, 8, 9, 40, 3, 3, 2, 2, 1, 1)  # n, cin, h, w, cout, kh, kw, strides, pads: an output of 4 x 5
+OPERANDS = {"x": (mq.ROLE_ACT, (8, 9, 3, 24)), "w": (mq.ROLE_WEIGHT, (40, 3, 3, 24)), "dy": (mq.ROLE_GRAD, (4, 5, 3, 40))}
+
+
+def _nv(which, fmt=4, codes=FAKE, scales=FAKE, t=FAKE, role=None, dims=None):
+    r, d = OPERANDS[which]
+    return mq.NvfpTensor(codes, scales, t, fmt, r if role is None else role, d if dims is None else dims)
+
+
+def test_product_workspace_sizes():
+    ws = mq.mqconv_nvfp_gemm_workspace_bytes
+    up = lambda v, m: -(-v // m) * m  # noqa: E731
+    for s in (CONV, (1, 4096, 1, 1, 4096, 1, 1, 1, 1, 0, 0), (16, 64, 80, 80, 64, 3, 3, 1, 1, 1, 1), (128, 256, 20, 20, 256, 3, 3, 1, 1, 1, 1)):
+        n, cin, h, w, cout, kh, kw, sh, sw, ph, pw = s
+        ho, wo = (h + 2 * ph - kh) // sh + 1, (w + 2 * pw - kw) // sw + 1
+        ops = (h * w * n * up(cin, 64) + cout * kh * kw * up(cin, 64), ho * wo * n * up(cout, 64) + cin * kh * kw * up(cout, 64),
+               up(n, 8) * (cout * ho * wo + cin * h * w))
+        outs = (ho * wo * n * cout, h * w * n * cin, cout * kh * kw * cin)
+        for op in range(3):
+            assert 0 < ws(s, op, 4, 4) <= 2 * ops[op] + 512 + 64 * 4 * outs[op], (s, op)
+    for bad in ((CONV, 3, 4, 4), (CONV, -1, 4, 4), (CONV, 0, 5, 4), (CONV, 0, 4, -1), ((0, *CONV[1:]), 0, 4, 4),
+                # 2^24 rows of 3 channels, which the products round up to 64; 2^27 pixels of one sample, rounded up to 8
+                ((1, 3, 4096, 4096, 8, 1, 1, 1, 1, 0, 0), 0, 4, 4), ((1, 8, 4096, 4096, 8, 1, 1, 1, 1, 0, 0), 2, 4, 4)):
+        assert ws(*bad) == 0, bad
+    with pytest.raises(mq.MqConvError):
+        ws((2**32 + 3, *CONV[1:]), 0, 4, 4)
+
+
+def test_product_refusals():
+    ws = FakeWorkspace(1 << 24)
+    calls = {mq.mqconv_nvfp_forward: ("x", "w"), mq.mqconv_nvfp_backward_data: ("dy", "w"), mq.mqconv_nvfp_backward_weight: ("dy", "x")}
+    for op, (fn, names) in enumerate(calls.items()):
+        run = lambda a=None, b=None, out=FAKE, s=CONV, w=ws: _status(  # noqa: E731
+            fn, s, a or _nv(names[0]), b or _nv(names[1]), out, w)
+        for k, name in enumerate(names):
+            one = lambda **kw: run(**{"ab"[k]: _nv(name, **kw)})  # noqa: E731,B023
+            assert one(codes=0) == NULL and one(scales=0) == NULL and one(t=0) == NULL
+            assert one(fmt=5) == FORMAT and one(fmt=-1) == FORMAT
+            assert one(role=(OPERANDS[name][0] + 1) % 3) == FORMAT
+            d = list(OPERANDS[name][1])
+            d[3] += 1
+            assert one(dims=tuple(d)) == SHAPE
+            assert one(codes=FAKE + 8) == ALIGN and one(t=FAKE + 2) == ALIGN
+        assert run(out=0) == NULL and run(out=FAKE + 2) == ALIGN
+        assert run(w=None) == WORKSPACE and run(w=FakeWorkspace(64)) == WORKSPACE and run(w=FakeWorkspace(1 << 24, FAKE + 8)) == ALIGN
+        assert run(s=(0, *CONV[1:])) == SHAPE and run(s=(*CONV[:7], 9, *CONV[8:])) == SHAPE
+        L = mq.train._lib()
+        a, b = (_nv(n).c_struct() for n in names)
+        assert getattr(L, fn.__name__)(None, a, b, FAKE, FAKE, 1 << 24, None) == NULL
+    # an operand whose rounded-up size is too large for the products
+    s = (1, 3, 4096, 4096, 8, 1, 1, 1, 1, 0, 0)
+    x = mq.NvfpTensor(FAKE, FAKE, FAKE, 4, mq.ROLE_ACT, (4096, 4096, 1, 3))
+    w = mq.NvfpTensor(FAKE, FAKE, FAKE, 4, mq.ROLE_WEIGHT, (8, 1, 1, 3))
+    assert _status(mq.mqconv_nvfp_forward, s, x, w, FAKE, ws) == SHAPE
+
+
 # ---- orthogonalised update ----------------------------------------------------------------------
 class FakeMatrix(FakeWorkspace):
     """An fp32 weight as the binding sees one, at an address that is never used."""
