@@ -33,6 +33,7 @@ struct Mat {
   const float* g;
   float *mom, *out;
   long long at;            // byte offset of its planes in the workspace
+  long long part;          // its slices' sums, from Group::part on
   int rows, cols, mp, np;  // mp, np: the smaller and the larger extent, rounded up to 32
   int chunk;               // elements of a partial sum
   float scale;             // factor of the orthogonalised matrix in the weight's update
@@ -41,6 +42,8 @@ struct Mat {
 struct Group {
   Mat m[kUpdateGroup];
   int start[kUpdateGroup + 1];  // first workgroup of every matrix
+  int tiles[kUpdateGroup], slices[kUpdateGroup];  // of the present product
+  float4* part;                 // sums of slices
   int count;
   uint8_t* ws;
   double* parts;  // [count][kMaxParts]
@@ -60,10 +63,12 @@ __device__ __forceinline__ uint8_t* a_of(const Group& g, const Mat& m, int k) {
   return g.ws + m.at + 3 * plane_x(m) + k * plane_a(m);
 }
 
-// the matrix of workgroup b, and its number within that
+// The matrix of workgroup b, and its number within that. A lane compares with
+// one start: one after the other they cost 3 us at 27 matrices.
 __device__ __forceinline__ int matrix_of(const Group& g, int b, int& local) {
-  int i = 0;
-  while (i + 1 < g.count && b >= g.start[i + 1]) i++;
+  const int lane = threadIdx.x & 63;
+  const bool behind = lane + 1 < g.count && b >= g.start[lane + 1 < kUpdateGroup ? lane + 1 : 0];
+  const int i = __builtin_amdgcn_readfirstlane(__builtin_popcountll(__builtin_amdgcn_ballot_w64(behind)));
   local = b - g.start[i];
   return i;
 }
@@ -133,6 +138,7 @@ __global__ __launch_bounds__(256) void init_kernel(const Group g) {
   const double inv = (double)kUp / (sqrt((red[0] + red[1]) + (red[2] + red[3])) + (double)g.eps);
   // read along the matrix's own rows
   const int r0 = tall ? j0 : i0, c0 = tall ? i0 : j0;
+#pragma unroll 8
   for (int t = threadIdx.x; t < kTile * kTile; t += 256) {
     const int r = r0 + t / kTile, c = c0 + t % kTile;
     float v = 0;
@@ -191,126 +197,237 @@ __device__ __forceinline__ void store_down(uint8_t* p, int ld, int r, int c, con
 
 enum { kGram, kPoly, kApply, kLast };
 
-// number of the pair (i, j), i <= j, in rows of the upper triangle of t x t tiles
-__device__ __forceinline__ void triangle(int k, int t, int& i, int& j) {
+// Tile k of a symmetric product: those of t x u tiles, q columns of tiles as wide as a row of tiles is high, that lie on or
+// above the diagonal. (The blocks on it are whole, so theirs is a store of one side alone.)
+__device__ __forceinline__ void triangle(int k, int u, int q, int& i, int& j) {
   i = 0;
-  while (k >= t - i) {
-    k -= t - i;
+  while (k >= u - i * q) {
+    k -= u - i * q;
     i++;
   }
-  j = i + k;
+  j = i * q + k;
+}
+
+// What becomes of four sums down a column, (row .., col) of the product of kind KIND.
+struct Last {
+  bool tall;
+  float keep, step;
+  int real_m, real_n;
+};
+__device__ __forceinline__ Last last_of(const Group& g, const Mat& m) {
+  const float lr = g.rate ? g.lr * *g.rate : g.lr;
+  return Last{m.rows > m.cols, __builtin_fmaf(-lr, g.decay, 1.0f), -lr * m.scale, min(m.rows, m.cols), max(m.rows, m.cols)};
+}
+template <int KIND>
+__device__ __forceinline__ void finish(const Group& g, const Mat& m, const Last& last, int row, int col, bool both, const float (&s)[4]) {
+  const int mp = m.mp, np = m.np;
+  if (row >= mp || col >= (KIND <= kPoly ? mp : np)) return;
+  float v[4];
+  if constexpr (KIND <= kPoly) {
+    uint8_t* const to = a_of(g, m, KIND == kPoly ? 1 : 0);
+    if constexpr (KIND == kGram) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) v[e] = s[e] * (1.0f / kUp);
+    } else {
+      // b A + c A^2, and a on the diagonal, so that the next product is a whole step (A is symmetric: its row is
+      // read along the columns here)
+      const uint8_t* const from = a_of(g, m, 0) + at_of(col, row, mp);
+      const half4 hi = *reinterpret_cast<const half4*>(from), lo = *reinterpret_cast<const half4*>(from + 64);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const float a = (float)hi[e] + (float)lo[e];
+        v[e] = __builtin_fmaf(g.b * 0.5f, a, s[e] * (g.c * (0.5f / kUp)));
+        if (row + e == col && col < last.real_m) v[e] += g.a * (0.5f * kUp);
+      }
+    }
+    store_across(to, mp, row, col, v);
+    if (both) store_down(to, mp, row, col, v);
+  } else if constexpr (KIND == kApply) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = s[e] * (2.0f / kUp);
+    store_across(xt_of(g, m, g.from ^ 1), mp, row, col, v);
+    store_down(x_of(g, m), np, row, col, v);
+  } else {
+    if (col >= last.real_n) return;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      if (row + e >= last.real_m) break;
+      const long long i = last.tall ? (long long)col * m.cols + row + e : (long long)(row + e) * m.cols + col;
+      const float o = s[e] * (2.0f / kUp / kUp);
+      m.out[i] = g.update ? __builtin_fmaf(last.step, o, m.out[i] * last.keep) : o;
+    }
+  }
+}
+
+// The place of tile `tile` of a matrix's product.
+template <int KIND, class S>
+__device__ __forceinline__ void place(const Mat& m, int tile, int& i0, int& j0, bool& both) {
+  int ti, tj;
+  if constexpr (KIND <= kPoly) {
+    constexpr int Q = S::BM / S::BN;
+    triangle(tile, (m.mp + S::BN - 1) / S::BN, Q, ti, tj);
+    both = tj >= (ti + 1) * Q;
+  } else {
+    const int tm = (m.mp + S::BM - 1) / S::BM;  // neighbours: tiles of one column, which share X's rows
+    tj = tile / tm;
+    ti = tile - tj * tm;
+    both = false;
+  }
+  i0 = ti * S::BM;
+  j0 = tj * S::BN;
 }
 
 template <int KIND, class S>
-__global__ __launch_bounds__(S::THREADS, 2) void newton_kernel(const Group g) {
+__global__ __launch_bounds__(S::THREADS, S::TM * S::TN >= 8 ? 1 : 2) void newton_kernel(const Group g) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const MmaWave<S> me;
+  const int lane = me.lane, wave = me.wave;
   int local;
-  const Mat& m = g.m[matrix_of(g, xcd_tile(blockIdx.x, gridDim.x), local)];
-  const int mp = m.mp, np = m.np;
-  int ti, tj;
-  if (KIND <= kPoly) triangle(local, (mp + S::BM - 1) / S::BM, ti, tj);
-  else {
-    const int tm = (mp + S::BM - 1) / S::BM;  // neighbours: tiles of one column, which share X's rows
-    tj = local / tm;
-    ti = local - tj * tm;
-  }
-  const int i0 = ti * S::BM, j0 = tj * S::BN;
-  const uint8_t* const x = x_of(g, m);
-  const uint8_t* const left = KIND == kGram ? x : a_of(g, m, KIND == kPoly ? 0 : 1);
-  const uint8_t* const right = KIND == kGram ? x : (KIND == kPoly ? left : xt_of(g, m, g.from));
-  const int k = KIND == kGram ? np : mp, rows_r = KIND <= kPoly ? mp : np;
+  const int which = matrix_of(g, xcd_tile(blockIdx.x, gridDim.x), local);
+  const Mat& m = g.m[which];
+  const int slices = g.slices[which], nt = g.tiles[which], z = local / nt, tile = local - z * nt;
+  int i0, j0;
+  bool both;
+  place<KIND, S>(m, tile, i0, j0, both);
+  const int mp = m.mp, k = KIND == kGram ? m.np : mp, rows_r = KIND <= kPoly ? mp : m.np;
+  const uint8_t* const left = KIND == kGram ? x_of(g, m) : a_of(g, m, KIND == kPoly ? 0 : 1);
+  const uint8_t* const right = KIND <= kPoly ? left : xt_of(g, m, g.from);
   RowLoader<S::LA, S::NW> la;
   RowLoader<S::LB, S::NW> lb;
   la.init(left, (long long)mp * k * 4, i0, mp, k * 4, wave, lane);
   lb.init(right, (long long)rows_r * k * 4, j0, rows_r, k * 4, wave, lane);
   v16f acc[S::TM][S::TN];
   mma_zero<S>(acc);
-  mma_loop<Split, S>(lds, la, lb, 0, k / 32, wave, lane, acc);
+  const int all = k / 32, s0 = (int)((long long)all * z / slices), steps = (int)((long long)all * (z + 1) / slices) - s0;
+  if constexpr (S::TM * S::TN >= 8) mma_loop_wide<Split, S>(lds, la, lb, s0, steps, me, acc);
+  else mma_loop<Split, S>(lds, la, lb, s0 + me.first(steps), me.count(steps), me.most(steps), me, acc);
+  if (me.group != 0) return;
+  if (slices > 1) {
+    // lane by lane: the kernel behind this one has the same order
+    float4* const to = g.part + m.part + ((long long)tile * slices + z) * (S::BM * S::BN / 4) + wave * (S::TM * S::TN * 256) + lane;
+#pragma unroll
+    for (int i = 0; i < S::TM; i++)
+#pragma unroll
+      for (int j = 0; j < S::TN; j++, __builtin_amdgcn_sched_barrier(0))
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          to[((i * S::TN + j) * 4 + e) * 64] =
+              make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
+    return;
+  }
+  const Last last = last_of(g, m);
+  mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&s)[4]) { finish<KIND>(g, m, last, i0 + r, j0 + c, both, s); });
+}
 
-  if constexpr (KIND <= kPoly) {
-    uint8_t* const to = a_of(g, m, KIND == kPoly ? 1 : 0);
-    mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&s)[4]) {
-      const int row = i0 + r, col = j0 + c;
-      if (row >= mp || col >= mp) return;
-      float v[4];
-      if constexpr (KIND == kGram) {
+// The slices' sums, added in order; a wave takes 32 x 32 of a tile.
+template <int KIND, class S>
+__global__ __launch_bounds__(256) void join_kernel(const Group g) {
+  constexpr int PER = S::NW * S::TM * S::TN;  // parts of a tile
+  const int lane = threadIdx.x & 63;
+  int local;
+  const int which = matrix_of(g, (int)blockIdx.x, local);
+  const Mat& m = g.m[which];
+  const int p = __builtin_amdgcn_readfirstlane(local * 4 + (threadIdx.x >> 6)), tile = p / PER, part = p - tile * PER;
+  const int slices = g.slices[which];
+  int i0, j0;
+  bool both;
+  place<KIND, S>(m, tile, i0, j0, both);
+  const int wave = part / (S::TM * S::TN), ij = part - wave * (S::TM * S::TN), i = ij / S::TN, j = ij - i * S::TN;
+  const int r0 = i0 + ((wave / S::WN) * S::TM + i) * 32, c0 = j0 + ((wave % S::WN) * S::TN + j) * 32;
+  if (r0 >= m.mp || c0 >= (KIND <= kPoly ? m.mp : m.np)) return;  // (whole waves)
+  const float4* const from = g.part + m.part + (long long)tile * slices * (S::BM * S::BN / 4) + part * 256 + lane;
+  float4 sum[4];
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = s[e] * (1.0f / kUp);
-      } else {
-        // b A + c A^2, and a on the diagonal, so that the next product is a whole step (A is symmetric: its row is
-        // read along the columns here)
-        const uint8_t* const from = left + at_of(col, row, mp);
-        const half4 hi = *reinterpret_cast<const half4*>(from), lo = *reinterpret_cast<const half4*>(from + 64);
-        const int real = min(m.rows, m.cols);
+  for (int e = 0; e < 4; e++) sum[e] = from[e * 64];
+  for (int z = 1; z < slices; z++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const float a = (float)hi[e] + (float)lo[e];
-          v[e] = __builtin_fmaf(g.b * 0.5f, a, s[e] * (g.c * (0.5f / kUp)));
-          if (row + e == col && col < real) v[e] += g.a * (0.5f * kUp);
-        }
-      }
-      store_across(to, mp, row, col, v);
-      if (ti != tj) store_down(to, mp, row, col, v);
-    });
-  } else if constexpr (KIND == kApply) {
-    uint8_t* const xo = x_of(g, m);
-    uint8_t* const xt = xt_of(g, m, g.from ^ 1);
-    mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&s)[4]) {
-      const int row = i0 + r, col = j0 + c;
-      if (row >= mp || col >= np) return;
-      float v[4];
+    for (int e = 0; e < 4; e++) {
+      const float4 v = from[(long long)z * (S::BM * S::BN / 4) + e * 64];
+      sum[e].x += v.x; sum[e].y += v.y; sum[e].z += v.z; sum[e].w += v.w;
+    }
+  const Last last = last_of(g, m);
 #pragma unroll
-      for (int e = 0; e < 4; e++) v[e] = s[e] * (2.0f / kUp);
-      store_across(xt, mp, row, col, v);
-      store_down(xo, np, row, col, v);
-    });
-  } else {
-    const bool tall = m.rows > m.cols;
-    const float lr = g.rate ? g.lr * *g.rate : g.lr;
-    const float keep = __builtin_fmaf(-lr, g.decay, 1.0f), step = -lr * m.scale;
-    const int real_m = min(m.rows, m.cols), real_n = max(m.rows, m.cols);
-    mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&s)[4]) {
-      const int row = i0 + r, col = j0 + c;
-      if (col >= real_n) return;
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        if (row + e >= real_m) break;
-        const long long i = tall ? (long long)col * m.cols + row + e : (long long)(row + e) * m.cols + col;
-        const float o = s[e] * (2.0f / kUp / kUp);
-        m.out[i] = g.update ? __builtin_fmaf(step, o, m.out[i] * keep) : o;
-      }
-    });
+  for (int e = 0; e < 4; e++) {
+    const float s[4] = {sum[e].x, sum[e].y, sum[e].z, sum[e].w};
+    finish<KIND>(g, m, last, r0 + 8 * e + 4 * (lane >> 5), c0 + (lane & 31), both, s);
   }
 }
 
-typedef MmaShape<64, 64, 2, 2, 3> Small;
-typedef MmaShape<128, 128, 2, 2, 2> Large;
+// ---- plans --------------------------------------------------------------------------------------
+// A matrix's tiles and slices are chosen by its own extents alone, so its
+// result does not depend on what else a call holds.
+typedef MmaShape<64, 64, 2, 2, 3> Small;        // several workgroups a compute unit
+typedef MmaShape<64, 64, 2, 2, 4, 2> SmallLong; // for A's few tiles and long sums
+typedef MmaShape<256, 128, 2, 2, 3> Wide;
 
 int tiles(int n, int b) { return (n + b - 1) / b; }
 
 template <int KIND, class S>
-hipError_t launch_product(Group& g, hipStream_t st) {
-  int total = 0;
-  for (int i = 0; i < g.count; i++) {
-    g.start[i] = total;
-    const int tm = tiles(g.m[i].mp, S::BM);
-    total += KIND <= kPoly ? tm * (tm + 1) / 2 : tm * tiles(g.m[i].np, S::BN);
+int tiles_of(const Mat& m) {
+  const int tm = tiles(m.mp, S::BM);
+  if (KIND > kPoly) return tm * tiles(m.np, S::BN);
+  const int u = tiles(m.mp, S::BN), q = S::BM / S::BN;
+  int n = 0;
+  for (int i = 0; i < tm; i++) n += u - i * q;
+  return n;
+}
+
+struct Plan {
+  bool wide;
+  int tiles, slices;
+};
+template <int KIND>
+Plan plan_of(const Mat& m) {
+  const int steps = (KIND == kGram ? m.np : m.mp) / 32;
+  Plan p{};
+  p.wide = m.mp >= (KIND == kPoly ? 1536 : 512);
+  if (p.wide) {
+    // one workgroup a compute unit; slices of 16 steps at least
+    p.tiles = tiles_of<KIND, Wide>(m);
+    p.slices = std::max(1, std::min({256 / p.tiles, steps / 16, 32}));
+  } else {
+    p.tiles = KIND == kGram ? tiles_of<KIND, SmallLong>(m) : tiles_of<KIND, Small>(m);
+    p.slices = std::max(1, std::min({256 / p.tiles, steps / 48, 32}));
   }
+  return p;
+}
+template <int KIND>
+long long part_of(const Mat& m) {  // float4 of its slices
+  const Plan p = plan_of<KIND>(m);
+  return p.slices == 1 ? 0 : (long long)p.tiles * p.slices * (p.wide ? Wide::BM * Wide::BN : Small::BM * Small::BN) / 4;
+}
+long long part_size(const Mat& m) { return std::max({part_of<kGram>(m), part_of<kPoly>(m), part_of<kApply>(m)}); }
+
+template <int KIND, class S>
+hipError_t launch_class(Group& g, bool wide, hipStream_t st) {
+  int total = 0, join = 0, joins[kUpdateGroup];
+  for (int i = 0; i < g.count; i++) {
+    const Plan p = plan_of<KIND>(g.m[i]);
+    const bool in = p.wide == wide;
+    g.start[i] = total;
+    g.tiles[i] = std::max(1, p.tiles);
+    g.slices[i] = p.slices;
+    total += in ? p.tiles * p.slices : 0;
+    joins[i] = join;
+    join += in && p.slices > 1 ? p.tiles * (S::NW * S::TM * S::TN / 4) : 0;
+  }
+  if (total == 0) return hipSuccess;
   g.start[g.count] = total;
   hipLaunchKernelGGL((newton_kernel<KIND, S>), dim3((unsigned)total), dim3(S::THREADS), 0, st, g);
+  const hipError_t e = launch_check();
+  if (e != hipSuccess || join == 0) return e;
+  std::copy(joins, joins + g.count, g.start);
+  g.start[g.count] = join;
+  hipLaunchKernelGGL((join_kernel<KIND, S>), dim3((unsigned)join), dim3(256), 0, st, g);
   return launch_check();
 }
 
 template <int KIND>
 hipError_t launch_product(Group& g, hipStream_t st) {
-  // tiles of 128 x 128 where there are enough of them to fill the chip
-  long long large = 0;
-  for (int i = 0; i < g.count; i++) {
-    const long long tm = tiles(g.m[i].mp, 128);
-    large += KIND <= kPoly ? tm * (tm + 1) / 2 : tm * tiles(g.m[i].np, 128);
-  }
-  return large >= 128 ? launch_product<KIND, Large>(g, st) : launch_product<KIND, Small>(g, st);
+  const hipError_t e = launch_class<KIND, Wide>(g, true, st);
+  if (e != hipSuccess) return e;
+  if constexpr (KIND == kGram) return launch_class<KIND, SmallLong>(g, false, st);
+  else return launch_class<KIND, Small>(g, false, st);
 }
 
 Mat make_mat(int rows, int cols) {
@@ -334,7 +451,10 @@ bool newton_shape_ok(int rows, int cols) {
 
 size_t newton_workspace_bytes(int count, const int* rows, const int* cols) {
   size_t n = parts_bytes(count);
-  for (int i = 0; i < count; i++) n += (size_t)planes_bytes(make_mat(rows[i], cols[i]));
+  for (int i = 0; i < count; i++) {
+    const Mat m = make_mat(rows[i], cols[i]);
+    n += (size_t)planes_bytes(m) + (size_t)part_size(m) * sizeof(float4);
+  }
   return n;
 }
 
@@ -347,7 +467,7 @@ hipError_t launch_newton(const UpdateSpec& u, int count, const int* rows, const 
   g.a = u.a; g.b = u.b; g.c = u.c; g.eps = u.eps;
   g.update = mom != nullptr;
   g.momentum = u.momentum; g.decay = u.decay; g.lr = u.lr; g.nesterov = u.nesterov; g.rate = u.rate;
-  long long at = 0;
+  long long at = 0, part = 0;
   int norm_groups = 0, init_groups = 0;
   int norm_start[kUpdateGroup], init_start[kUpdateGroup];
   for (int i = 0; i < count; i++) {
@@ -358,11 +478,14 @@ hipError_t launch_newton(const UpdateSpec& u, int count, const int* rows, const 
                                          : 1.0f;
     m.at = at;
     at += planes_bytes(m);
+    m.part = part;
+    part += part_size(m);
     norm_start[i] = norm_groups;
     norm_groups += (int)(((long long)m.rows * m.cols + m.chunk - 1) / m.chunk);
     init_start[i] = init_groups;
     init_groups += tiles(m.mp, kTile) * tiles(m.np, kTile);
   }
+  g.part = reinterpret_cast<float4*>(g.ws + at);
   std::copy(norm_start, norm_start + count, g.start);
   hipLaunchKernelGGL(norm_kernel, dim3((unsigned)norm_groups), dim3(256), 0, st, g);
   hipError_t e = launch_check();

@@ -24,6 +24,7 @@
 
 #include <algorithm>
 
+#include "block_common.h"
 #include "mma_core.h"
 #include "train.h"
 
@@ -101,34 +102,46 @@ __device__ __forceinline__ bhalf8 values8(const Codes& t, long long row, int ab,
   return o;
 }
 
-// out[row][Cp], Cp a multiple of 64: 8 channels a thread.
-struct RowsArgs {
+// f(the format as a constant); the format is the same for a whole workgroup
+template <class L>
+__device__ __forceinline__ void by_format(int fmt, L&& f) {
+  switch (fmt) {
+    case 0: f(std::integral_constant<int, 0>{}); break;
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 3: f(std::integral_constant<int, 3>{}); break;
+    default: f(std::integral_constant<int, 4>{}); break;
+  }
+}
+
+// An operand as bf16, either
+//   out[row][Cp], Cp a multiple of 64: 8 channels a thread, or
+//   out[c][ab][Pp], Pp a multiple of 8: tiles of 64 channels x 64 of the (ab, p).
+struct Task {
   Codes t;
   __bf16* out;
-  int n;  // pieces of 8 channels
+  bool across;
+  int groups;            // workgroups
+  int n;                 // pieces of 8 channels
   FastDiv pieces, dP, dB;
+  int Pp, S, tiles;      // S = A B Pp; tiles along S
+  FastDiv dPp;
 };
+
 template <int F>
-__global__ __launch_bounds__(256) void nvfp_rows_kernel(const RowsArgs a) {
-  const unsigned i = blockIdx.x * 256u + threadIdx.x;
+__device__ __forceinline__ void make_rows(const Task& a, int group) {
+  const unsigned i = group * 256u + threadIdx.x;
   if (i >= (unsigned)a.n) return;
   const unsigned row = fdiv(i, a.pieces), ch = i - row * a.pieces.d;
   const unsigned q = fdiv(row, a.dB), b = row - q * a.dB.d, aa = fdiv(q, a.dP), p = q - aa * a.dP.d;
   *reinterpret_cast<bhalf8*>(a.out + (long long)i * 8) = values8<F>(a.t, row, (int)(aa * a.dB.d + b), (int)p, (int)ch);
 }
 
-// out[c][ab][Pp], Pp a multiple of 8: tiles of 64 channels x 64 of the (ab, p).
-struct AcrossArgs {
-  Codes t;
-  __bf16* out;
-  int Pp, S, tiles;  // S = A B Pp; tiles along S
-  FastDiv dPp, dB;
-};
+constexpr int kAcross = 66;  // a column of the tile (eight threads of one slot write 8 channels each, 264 dwords apart: eight banks)
 template <int F>
-__global__ __launch_bounds__(256) void nvfp_across_kernel(const AcrossArgs a) {
-  constexpr int PITCH = 66;  // (eight threads of one slot write 8 channels each: 264 dwords apart, eight banks)
-  __shared__ __attribute__((aligned(16))) __bf16 tile[64 * PITCH];
-  const int ct = blockIdx.x / a.tiles, s0 = (blockIdx.x - ct * a.tiles) * 64, c0 = ct * 64;
+__device__ __forceinline__ void make_across(const Task& a, int group, __bf16* tile) {
+  const int ct = group / a.tiles, s0 = (group - ct * a.tiles) * 64, c0 = ct * 64;
+#pragma unroll
   for (int i = threadIdx.x; i < 512; i += 256) {
     const int ch = i & 7, slot = i >> 3, s = s0 + slot;
     bhalf8 v;
@@ -142,47 +155,55 @@ __global__ __launch_bounds__(256) void nvfp_across_kernel(const AcrossArgs a) {
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; e++) tile[(8 * ch + e) * PITCH + slot] = v[e];
+    for (int e = 0; e < 8; e++) tile[(8 * ch + e) * kAcross + slot] = v[e];
   }
   __syncthreads();
+#pragma unroll
   for (int i = threadIdx.x; i < 512; i += 256) {
     const int k = i & 7, c = i >> 3, s = s0 + 8 * k;
     if (c0 + c >= a.t.C || s >= a.S) continue;
-    uint4 w;
-    const uint32_t* const from = reinterpret_cast<const uint32_t*>(tile + c * PITCH + 8 * k);
-    w.x = from[0]; w.y = from[1]; w.z = from[2]; w.w = from[3];
-    *reinterpret_cast<uint4*>(a.out + (long long)(c0 + c) * a.S + s) = w;
+    const uint32_t* const from = reinterpret_cast<const uint32_t*>(tile + c * kAcross + 8 * k);
+    *reinterpret_cast<uint4*>(a.out + (long long)(c0 + c) * a.S + s) = make_uint4(from[0], from[1], from[2], from[3]);
   }
 }
 
-template <class L>
-hipError_t with_format(int fmt, L&& launch) {
-  switch (fmt) {
-    case 0: launch(std::integral_constant<int, 0>{}); break;
-    case 1: launch(std::integral_constant<int, 1>{}); break;
-    case 2: launch(std::integral_constant<int, 2>{}); break;
-    case 3: launch(std::integral_constant<int, 3>{}); break;
-    default: launch(std::integral_constant<int, 4>{}); break;
-  }
-  return launch_check();
+// Both operands in one launch.
+__global__ __launch_bounds__(256) void nvfp_values_kernel(const Task a, const Task b) {
+  __shared__ __attribute__((aligned(16))) __bf16 tile[64 * kAcross];
+  const bool first = (int)blockIdx.x < a.groups;
+  const Task& t = first ? a : b;
+  const int group = first ? (int)blockIdx.x : (int)blockIdx.x - a.groups;
+  by_format(t.t.fmt, [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    if (t.across) make_across<F>(t, group, tile);
+    else make_rows<F>(t, group);
+  });
 }
 
 long long up(long long v, int m) { return (v + m - 1) / m * m; }
 
-hipError_t launch_rows(const Codes& t, __bf16* out, hipStream_t st) {
+Task rows_task(const Codes& t, __bf16* out) {
   const int cp = (int)up(t.C, 64);
-  RowsArgs a{t, out, (int)((long long)t.A * t.P * t.B * (cp / 8)), make_fastdiv(cp / 8), make_fastdiv(t.P), make_fastdiv(t.B)};
-  return with_format(t.fmt, [&](auto f) {
-    hipLaunchKernelGGL(nvfp_rows_kernel<decltype(f)::value>, dim3((unsigned)((a.n + 255LL) / 256)), dim3(256), 0, st, a);
-  });
+  Task a{};
+  a.t = t; a.out = out;
+  a.n = (int)((long long)t.A * t.P * t.B * (cp / 8));
+  a.groups = ceil_div(a.n, 256);
+  a.pieces = make_fastdiv(cp / 8); a.dP = make_fastdiv(t.P); a.dB = make_fastdiv(t.B);
+  return a;
 }
-hipError_t launch_across(const Codes& t, __bf16* out, int pad, hipStream_t st) {
-  AcrossArgs a{t, out, (int)up(t.P, pad), 0, 0, make_fastdiv((unsigned)up(t.P, pad)), make_fastdiv(t.B)};
+Task across_task(const Codes& t, __bf16* out, int pad) {
+  Task a{};
+  a.t = t; a.out = out; a.across = true;
+  a.Pp = (int)up(t.P, pad);
   a.S = t.A * t.B * a.Pp;
   a.tiles = ceil_div(a.S, 64);
-  return with_format(t.fmt, [&](auto f) {
-    hipLaunchKernelGGL(nvfp_across_kernel<decltype(f)::value>, dim3((unsigned)(a.tiles * ceil_div(t.C, 64))), dim3(256), 0, st, a);
-  });
+  a.groups = a.tiles * ceil_div(t.C, 64);
+  a.dPp = make_fastdiv((unsigned)a.Pp); a.dB = make_fastdiv(t.B);
+  return a;
+}
+hipError_t launch_values(const Task& a, const Task& b, hipStream_t st) {
+  hipLaunchKernelGGL(nvfp_values_kernel, dim3((unsigned)(a.groups + b.groups)), dim3(256), 0, st, a, b);
+  return launch_check();
 }
 
 // ---- products -----------------------------------------------------------------------------------
@@ -326,14 +347,13 @@ __device__ __forceinline__ Scale scale_of(const float* a, const float* b) {
   return s;
 }
 
-constexpr int kClasses = 64;  // stride 8 both ways
-
 struct Class {
   Gather g;
   Taps t;
-  int first;         // its first tile
-  int h0, w0;        // its pixels are (r sh + h0, c sw + w0)
+  int h0, w0;  // its pixels are (r sh + h0, c sw + w0)
+  int first, tiles;  // its tiles among all
 };
+constexpr int kClasses = 8;  // of a launch
 
 struct ConvArgs {
   const __bf16* b;
@@ -341,18 +361,76 @@ struct ConvArgs {
   int b_pitch, cols;  // bytes of a row of the other operand; its rows, the output's columns
   float* out;         // or the slices
   const float *ta, *tb;
-  int slices;
-  long long slice;   // values of a slice
-  int sh, sw, W, N;  // where a class's rows are in the output
-  int tiles, nclass;
-  bool classes;      // rows go by classes (backward data)
+  int slices, tiles;
+  long long slice;    // values of a slice
+  int sh, sw, W, N;   // where a class's rows are in the output
+  int nclass;
+  bool classes;       // rows go by classes (backward data)
+  Class k[kClasses];
 };
 
-// One class's arguments travel in the kernel arguments, several in device memory.
+// A wave's results through LDS, 32 rows at a time, to whole pieces of rows: `rows` has the tile's rows in the output (-1: none).
 template <class S>
-__device__ __forceinline__ void conv_tile(const ConvArgs& a, const Class& k, int tile, int z, uint8_t* lds) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tn = (a.cols + S::BN - 1) / S::BN;
+__device__ __forceinline__ void store_results(float* strips, const int* rows, v16f (&acc)[S::TM][S::TN], const MmaWave<S>& me,
+                                              const Scale& scale, float* out, int cols, int j0) {
+  constexpr int WIDE = S::TN * 32, PITCH = WIDE + 8;  // (rows r and r + 4 are written together: the other half of the banks)
+  const int lane = me.lane, wm = me.wave / S::WN, wn = me.wave % S::WN;
+  float* const strip = strips + me.wave * 32 * PITCH;
+  constexpr int LPR = WIDE / 4, RPI = 64 / LPR;  // lanes of a row, rows of a store
+  const int c = (lane % LPR) * 4, col = j0 + wn * WIDE + c;
+#pragma unroll
+  for (int i = 0; i < S::TM; i++) {
+#pragma unroll
+    for (int j = 0; j < S::TN; j++)
+#pragma unroll
+      for (int e = 0; e < 16; e++)
+        strip[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * PITCH + j * 32 + (lane & 31)] = scale(acc[i][j][e]);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the strip is written (one wave's)
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < 32; r += RPI) {
+      const int rr = r + lane / LPR;
+      const int row = rows[(wm * S::TM + i) * 32 + rr];
+      const f4u v = *reinterpret_cast<const f4u*>(strip + rr * PITCH + c);
+      if (row < 0 || col >= cols) continue;
+      float* const to = out + (long long)row * cols + col;
+      if (col + 4 <= cols) {
+        __builtin_nontemporal_store(v, reinterpret_cast<f4u*>(to));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; e++)
+          if (col + e < cols) to[e] = v[e];
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // (and read, before the next one)
+    asm volatile("" ::: "memory");
+  }
+}
+
+template <class S>
+constexpr int strips_of() {  // bytes of the strips; the tile's rows are behind them
+  static_assert(S::NW * 32 * (S::TN * 32 + 8) * 4 + S::BM * 4 <= S::LDS, "the strips and the rows take the ring's place");
+  return S::NW * 32 * (S::TN * 32 + 8) * 4;
+}
+template <class S>
+constexpr bool wide_of() {
+  return S::TM * S::TN >= 8 && S::NW == 4;
+}
+template <class S>
+constexpr int waves_of() {  // a SIMD's, for the register budget
+  return wide_of<S>() ? 1 : 2;
+}
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_conv_kernel(const ConvArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  const MmaWave<S> me;
+  const int lane = me.lane, wave = me.wave;
+  const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles, at = b - z * a.tiles;
+  int which = 0;
+  while (which + 1 < a.nclass && at >= a.k[which + 1].first) which++;
+  const Class& k = a.k[which];
+  const int tile = at - k.first, tn = (a.cols + S::BN - 1) / S::BN;
   const int ti = tile / tn, i0 = ti * S::BM, j0 = (tile - ti * tn) * S::BN;
   const int steps = k.t.ni * k.t.nj * k.t.nc, s0 = (int)((long long)steps * z / a.slices),
             s1 = (int)((long long)steps * (z + 1) / a.slices);
@@ -363,33 +441,24 @@ __device__ __forceinline__ void conv_tile(const ConvArgs& a, const Class& k, int
     TapLoader<S::LB, S::NW> lb;
     la.init(k.g, k.t, i0, s0, wave, lane);
     lb.init(a.b, a.b_bytes, j0, a.cols, a.b_pitch, k.t, s0, wave, lane);
-    mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, wave, lane, acc);
+    if constexpr (wide_of<S>()) mma_loop_wide<Bf16, S>(lds, la, lb, s0, s1 - s0, me, acc);
+    else mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, s1 - s0, me, acc);
   }
+  stage_ready<0>();  // the ring is free
+  int* const rows = reinterpret_cast<int*>(lds + strips_of<S>());
+  for (int r = threadIdx.x; r < S::BM; r += S::THREADS) {
+    const int m = i0 + r;
+    int row = m < k.g.M ? m : -1;
+    if (a.classes && row >= 0) {
+      const unsigned px = fdiv((unsigned)m, k.g.dN), n = (unsigned)m - px * k.g.dN.d, pr = fdiv(px, k.g.dW), pc = px - pr * k.g.dW.d;
+      row = (((int)pr * a.sh + k.h0) * a.W + (int)pc * a.sw + k.w0) * a.N + (int)n;
+    }
+    rows[r] = row;
+  }
+  __syncthreads();
   Scale scale{1.0f, 0};
   if (a.slices == 1) scale = scale_of(a.ta, a.tb);
-  float* const out = a.out + z * (a.slices == 1 ? 0 : a.slice);
-  mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&v)[4]) {
-    const int col = j0 + c;
-    if (col >= a.cols) return;
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      const int m = i0 + r + e;
-      if (m >= k.g.M) break;
-      long long row = m;
-      if (a.classes) {
-        const unsigned px = fdiv((unsigned)m, k.g.dN), n = (unsigned)m - px * k.g.dN.d, pr = fdiv(px, k.g.dW), pc = px - pr * k.g.dW.d;
-        row = ((long long)((int)pr * a.sh + k.h0) * a.W + (int)pc * a.sw + k.w0) * a.N + n;
-      }
-      out[row * a.cols + col] = a.slices == 1 ? scale(v[e]) : v[e];
-    }
-  });
-}
-
-template <class S>
-__global__ __launch_bounds__(S::THREADS, 2) void nvfp_conv_kernel(const ConvArgs a, const Class k) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
-  const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles;
-  conv_tile<S>(a, k, b - z * a.tiles, z, lds);
+  store_results<S>(reinterpret_cast<float*>(lds), rows, acc, me, scale, a.out + (a.slices == 1 ? 0 : z * a.slice), a.cols, j0);
 }
 
 struct WeightArgs {
@@ -404,9 +473,10 @@ struct WeightArgs {
 };
 
 template <class S>
-__global__ __launch_bounds__(S::THREADS, 2) void nvfp_weight_kernel(const WeightArgs a) {
+__global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_weight_kernel(const WeightArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const MmaWave<S> me;
+  const int lane = me.lane, wave = me.wave;
   const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles, tile = b - z * a.tiles;
   const int tn = (a.x.cols + S::BN - 1) / S::BN;
   const int ti = tile / tn, i0 = ti * S::BM, j0 = (tile - ti * tn) * S::BN;
@@ -417,17 +487,15 @@ __global__ __launch_bounds__(S::THREADS, 2) void nvfp_weight_kernel(const Weight
   ShiftLoader<S::LB, S::NW> lb;
   la.init(a.dy, a.dy_bytes, i0, a.rows, a.x.pieces, wave, lane);
   lb.init(a.x, j0, wave, lane);
-  mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, wave, lane, acc);
+  if constexpr (wide_of<S>()) mma_loop_wide<Bf16, S>(lds, la, lb, s0, s1 - s0, me, acc);
+  else mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, s1 - s0, me, acc);
+  stage_ready<0>();
+  int* const rows = reinterpret_cast<int*>(lds + strips_of<S>());
+  for (int r = threadIdx.x; r < S::BM; r += S::THREADS) rows[r] = i0 + r < a.rows ? i0 + r : -1;
+  __syncthreads();
   Scale scale{1.0f, 0};
   if (a.slices == 1) scale = scale_of(a.ta, a.tb);
-  float* const out = a.out + z * (a.slices == 1 ? 0 : a.slice);
-  mma_results<S>(acc, wave, lane, [&](int r, int c, const float (&v)[4]) {
-    const int col = j0 + c;
-    if (col >= a.x.cols) return;
-#pragma unroll
-    for (int e = 0; e < 4; e++)
-      if (i0 + r + e < a.rows) out[(long long)(i0 + r + e) * a.x.cols + col] = a.slices == 1 ? scale(v[e]) : v[e];
-  });
+  store_results<S>(reinterpret_cast<float*>(lds), rows, acc, me, scale, a.out + (a.slices == 1 ? 0 : z * a.slice), a.x.cols, j0);
 }
 
 // The slices' sums, added in order (fp64), times the tensors' scales.
@@ -442,35 +510,40 @@ __global__ __launch_bounds__(256) void nvfp_join_kernel(const float* part, float
 }
 
 // ---- plans --------------------------------------------------------------------------------------
-typedef MmaShape<256, 256, 2, 4, 2> Big;
+typedef MmaShape<256, 256, 2, 2, 2> Big;
+typedef MmaShape<256, 128, 2, 2, 3> Wide;
 typedef MmaShape<128, 128, 2, 2, 2> Mid;
 typedef MmaShape<256, 64, 4, 1, 2> Tall;
 typedef MmaShape<64, 64, 2, 2, 3> Small;
+enum { kBig, kWide, kMid, kTall, kSmall };
 
 // Tiles by the output's extents, and slices along k where these tiles do not fill the chip.
 struct Plan {
-  int shape;  // 0 Big, 1 Mid, 2 Tall, 3 Small
-  int slices;
+  int shape, slices;
 };
-const int kBM[4] = {256, 128, 256, 64}, kBN[4] = {256, 128, 64, 64};
-Plan plan_of(long long M, long long N, long long steps) {
+const int kBM[5] = {256, 256, 128, 256, 64}, kBN[5] = {256, 128, 128, 64, 64};
+Plan plan_of(int op, long long M, long long N, long long steps) {
   auto tiles = [&](int s) { return (long long)ceil_div(M, kBM[s]) * ceil_div(N, kBN[s]); };
-  Plan p{3, 1};
-  if (N > 128 && M > 128 && tiles(0) >= 200) p.shape = 0;
-  else if (N <= 64 && M >= 256 && tiles(2) >= 200) p.shape = 2;
-  else if (N > 64 && M > 64 && tiles(1) * std::max(1LL, steps / 8) >= 256) p.shape = 1;
-  const long long t = tiles(p.shape), want = 512 / std::max(1LL, t);
+  Plan p{kSmall, 1};
+  if (op < 2 && N > 128 && M > 128 && tiles(kBig) >= 200) p.shape = kBig;
+  else if (M > 128 && N > 64 && steps >= 32 && tiles(kWide) * (steps / 16) >= 200) p.shape = kWide;
+  else if (N <= 64 && M >= 256 && tiles(kTall) >= 200) p.shape = kTall;
+  else if (N > 64 && M > 64 && tiles(kMid) * std::max(1LL, steps / 8) >= 256) p.shape = kMid;
+  const long long t = tiles(p.shape), want = (p.shape == kWide ? 256 : 512) / std::max(1LL, t);
   // slices of eight steps at least, and no more sums than operands' bytes by far
   if (want >= 2) p.slices = (int)std::max(1LL, std::min({want, steps / 8, 64LL}));
   return p;
 }
 
-template <class F>
+template <int OP, class F>
 void with_shape(int s, F&& f) {
   switch (s) {
-    case 0: f(Big{}); break;
-    case 1: f(Mid{}); break;
-    case 2: f(Tall{}); break;
+    case kBig:
+      if constexpr (OP < 2) f(Big{});  // (the weight gradient's loader leaves no registers for it)
+      break;
+    case kWide: f(Wide{}); break;
+    case kMid: f(Mid{}); break;
+    case kTall: f(Tall{}); break;
     default: f(Small{}); break;
   }
 }
@@ -491,19 +564,19 @@ Sizes sizes_of(const Conv& c, int op) {
     const long long cp = up(c.cin, 64);
     s.a = (long long)c.h * c.w * c.n * cp * 2;
     s.b = c.cout * taps * cp * 2;
-    s.plan = plan_of(ho * wo * c.n, c.cout, taps * (cp / 64));
+    s.plan = plan_of(op, ho * wo * c.n, c.cout, taps * (cp / 64));
     out = ho * wo * c.n * c.cout;
   } else if (op == 1) {
     const long long kp = up(c.cout, 64);
     s.a = ho * wo * c.n * kp * 2;
     s.b = c.cin * taps * kp * 2;
-    s.plan = plan_of((long long)c.h * c.w * c.n, c.cin, (long long)class_taps(c.kh, c.sh) * class_taps(c.kw, c.sw) * (kp / 64));
+    s.plan = plan_of(op, (long long)c.h * c.w * c.n, c.cin, (long long)class_taps(c.kh, c.sh) * class_taps(c.kw, c.sw) * (kp / 64));
     out = (long long)c.h * c.w * c.n * c.cin;
   } else {
     const long long np = up(c.n, 8);
     s.a = c.cout * ho * wo * np * 2;
     s.b = (long long)c.cin * c.h * c.w * np * 2;
-    s.plan = plan_of(c.cout, taps * c.cin, (ho * wo * np + 63) / 64);
+    s.plan = plan_of(op, c.cout, taps * c.cin, (ho * wo * np + 63) / 64);
     out = c.cout * taps * c.cin;
   }
   s.part = s.plan.slices > 1 ? out * 4 * s.plan.slices : 0;
@@ -535,21 +608,22 @@ hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView&
   __bf16* const xb = static_cast<__bf16*>(ws);
   __bf16* const wb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
-  hipError_t e = launch_rows(codes_of(x, c.h * c.w, c.n, 1, c.cin), xb, st);
+  hipError_t e = launch_values(rows_task(codes_of(x, c.h * c.w, c.n, 1, c.cin), xb),
+                               rows_task(codes_of(w, 1, c.cout, taps, c.cin), wb), st);
   if (e != hipSuccess) return e;
-  if ((e = launch_rows(codes_of(w, 1, c.cout, taps, c.cin), wb, st)) != hipSuccess) return e;
-  Class k{};
-  k.g = Gather{xb, s.a, c.h, c.w, c.n, cp * 2, wo, ho * wo * c.n, c.sh, c.sw, -c.ph, -c.pw, 1, make_fastdiv(c.n), make_fastdiv(wo)};
-  k.t = Taps{c.kh, c.kw, cp / 64, 0, 0, 1, 1, c.kw};
   ConvArgs a{};
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * cp * 2; a.cols = c.cout;
-  a.slices = s.plan.slices; a.slice = (long long)k.g.M * c.cout;
+  a.slices = s.plan.slices; a.slice = (long long)ho * wo * c.n * c.cout;
   a.out = a.slices > 1 ? part : y;
   a.ta = x.tensor; a.tb = w.tensor;
+  a.nclass = 1;
+  Class& k = a.k[0];
+  k.g = Gather{xb, s.a, c.h, c.w, c.n, cp * 2, wo, ho * wo * c.n, c.sh, c.sw, -c.ph, -c.pw, 1, make_fastdiv(c.n), make_fastdiv(wo)};
+  k.t = Taps{c.kh, c.kw, cp / 64, 0, 0, 1, 1, c.kw};
   a.tiles = ceil_div(k.g.M, kBM[s.plan.shape]) * ceil_div(c.cout, kBN[s.plan.shape]);
-  with_shape(s.plan.shape, [&](auto shape) {
+  with_shape<0>(s.plan.shape, [&](auto shape) {
     typedef decltype(shape) S;
-    hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a, k);
+    hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a);
   });
   if ((e = launch_check()) != hipSuccess) return e;
   return join(s, part, y, a.slice, a.ta, a.tb, st);
@@ -561,9 +635,9 @@ hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const Nv
   __bf16* const yb = static_cast<__bf16*>(ws);
   __bf16* const wb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
-  hipError_t e = launch_rows(codes_of(dy, ho * wo, c.n, 1, c.cout), yb, st);
+  hipError_t e = launch_values(rows_task(codes_of(dy, ho * wo, c.n, 1, c.cout), yb),
+                               across_task(codes_of(w, 1, c.cout, taps, c.cin), wb, 64), st);
   if (e != hipSuccess) return e;
-  if ((e = launch_across(codes_of(w, 1, c.cout, taps, c.cin), wb, 64, st)) != hipSuccess) return e;
   ConvArgs a{};
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * kp * 2; a.cols = c.cin;
   a.slices = s.plan.slices; a.slice = (long long)c.h * c.w * c.n * c.cin;
@@ -571,23 +645,28 @@ hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const Nv
   a.ta = dy.tensor; a.tb = w.tensor;
   a.sh = c.sh; a.sw = c.sw; a.W = c.w; a.N = c.n;
   a.classes = c.sh > 1 || c.sw > 1;
-  for (int h = 0; h < std::min(c.sh, c.h); h++)
-    for (int v = 0; v < std::min(c.sw, c.w); v++) {
-      const int k0 = (h + c.ph) % c.sh, l0 = (v + c.pw) % c.sw;
-      const int rows = ceil_div(c.h - h, c.sh), cols = ceil_div(c.w - v, c.sw);
-      Class k{};
-      k.h0 = h; k.w0 = v;
-      k.g = Gather{yb, s.a, ho, wo, c.n, kp * 2, cols, rows * cols * c.n, 1, 1, (h + c.ph - k0) / c.sh, (v + c.pw - l0) / c.sw, -1,
-                   make_fastdiv(c.n), make_fastdiv(cols)};
-      k.t = Taps{k0 < c.kh ? ceil_div(c.kh - k0, c.sh) : 0, l0 < c.kw ? ceil_div(c.kw - l0, c.sw) : 0, kp / 64, k0, l0, c.sh, c.sw, c.kw};
-      if (k.t.ni == 0 || k.t.nj == 0) k.t.ni = 0, k.t.nj = 1;  // (no tap reaches these pixels: zeros)
-      a.tiles = ceil_div(k.g.M, kBM[s.plan.shape]) * ceil_div(c.cin, kBN[s.plan.shape]);
-      with_shape(s.plan.shape, [&](auto shape) {
-        typedef decltype(shape) S;
-        hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a, k);
-      });
-      if ((e = launch_check()) != hipSuccess) return e;
-    }
+  const int nh = std::min(c.sh, c.h), nw = std::min(c.sw, c.w);
+  for (int q = 0; q < nh * nw; q++) {
+    const int h = q / nw, v = q % nw, k0 = (h + c.ph) % c.sh, l0 = (v + c.pw) % c.sw;
+    const int rows = ceil_div(c.h - h, c.sh), cols = ceil_div(c.w - v, c.sw);
+    Class& k = a.k[a.nclass];
+    k = Class{};
+    k.h0 = h; k.w0 = v;
+    k.g = Gather{yb, s.a, ho, wo, c.n, kp * 2, cols, rows * cols * c.n, 1, 1, (h + c.ph - k0) / c.sh, (v + c.pw - l0) / c.sw, -1,
+                 make_fastdiv(c.n), make_fastdiv(cols)};
+    k.t = Taps{k0 < c.kh ? ceil_div(c.kh - k0, c.sh) : 0, l0 < c.kw ? ceil_div(c.kw - l0, c.sw) : 0, kp / 64, k0, l0, c.sh, c.sw, c.kw};
+    if (k.t.ni == 0 || k.t.nj == 0) k.t.ni = 0, k.t.nj = 1;  // (no tap reaches these pixels: zeros)
+    k.tiles = ceil_div(k.g.M, kBM[s.plan.shape]) * ceil_div(c.cin, kBN[s.plan.shape]);
+    k.first = a.tiles;
+    a.tiles += k.tiles;
+    if (++a.nclass < kClasses && q + 1 < nh * nw) continue;
+    with_shape<1>(s.plan.shape, [&](auto shape) {
+      typedef decltype(shape) S;
+      hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a);
+    });
+    if ((e = launch_check()) != hipSuccess) return e;
+    a.nclass = a.tiles = 0;
+  }
   return join(s, part, dx, a.slice, a.ta, a.tb, st);
 }
 
@@ -597,9 +676,9 @@ hipError_t launch_nvfp_backward_weight(const Conv& c, const NvfpView& dy, const 
   __bf16* const yb = static_cast<__bf16*>(ws);
   __bf16* const xb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
-  hipError_t e = launch_across(codes_of(dy, ho * wo, c.n, 1, c.cout), yb, 8, st);
+  hipError_t e = launch_values(across_task(codes_of(dy, ho * wo, c.n, 1, c.cout), yb, 8),
+                               across_task(codes_of(x, c.h * c.w, c.n, 1, c.cin), xb, 8), st);
   if (e != hipSuccess) return e;
-  if ((e = launch_across(codes_of(x, c.h * c.w, c.n, 1, c.cin), xb, 8, st)) != hipSuccess) return e;
   WeightArgs a{};
   a.dy = yb; a.dy_bytes = s.a; a.rows = c.cout;
   a.x = Shift{xb, s.b, c.h, c.w, c.cin, c.kw, np, c.sh, c.sw, c.ph, c.pw, taps * c.cin, ho * wo * (np / 8), make_fastdiv(c.cin),
@@ -609,7 +688,7 @@ hipError_t launch_nvfp_backward_weight(const Conv& c, const NvfpView& dy, const 
   a.ta = dy.tensor; a.tb = x.tensor;
   a.steps = ceil_div(a.x.pieces, 8);
   a.tiles = ceil_div(c.cout, kBM[s.plan.shape]) * ceil_div(a.x.cols, kBN[s.plan.shape]);
-  with_shape(s.plan.shape, [&](auto shape) {
+  with_shape<2>(s.plan.shape, [&](auto shape) {
     typedef decltype(shape) S;
     hipLaunchKernelGGL(nvfp_weight_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a);
   });
