@@ -351,7 +351,7 @@ struct Class {
   Gather g;
   Taps t;
   int h0, w0;  // its pixels are (r sh + h0, c sw + w0)
-  int first, tiles;  // its tiles among all
+  int tiles;
 };
 constexpr int kClasses = 8;  // of a launch
 
@@ -366,6 +366,10 @@ struct ConvArgs {
   int sh, sw, W, N;   // where a class's rows are in the output
   int nclass;
   bool classes;       // rows go by classes (backward data)
+  // the gathered operand's codes, for the kernel that makes its values itself
+  const uint8_t *codes, *scales;
+  long long codes_bytes, scales_bytes;
+  int rbytes, runs, nPB, nCB;  // bytes and 32-channel runs of a row, blocks along samples and channels
   Class k[kClasses];
 };
 
@@ -373,44 +377,62 @@ struct ConvArgs {
 template <class S>
 __device__ __forceinline__ void store_results(float* strips, const int* rows, v16f (&acc)[S::TM][S::TN], const MmaWave<S>& me,
                                               const Scale& scale, float* out, int cols, int j0) {
-  constexpr int WIDE = S::TN * 32, PITCH = WIDE + 8;  // (rows r and r + 4 are written together: the other half of the banks)
+  constexpr int TJ = S::TN < 2 ? 1 : 2, WIDE = TJ * 32, PITCH = WIDE + 8;  // (rows r and r + 4 are written together: the other half of the banks)
+  static_assert(S::TN % TJ == 0, "strips");
   const int lane = me.lane, wm = me.wave / S::WN, wn = me.wave % S::WN;
   float* const strip = strips + me.wave * 32 * PITCH;
   constexpr int LPR = WIDE / 4, RPI = 64 / LPR;  // lanes of a row, rows of a store
-  const int c = (lane % LPR) * 4, col = j0 + wn * WIDE + c;
+  const int c = (lane % LPR) * 4;
 #pragma unroll
-  for (int i = 0; i < S::TM; i++) {
+  for (int i = 0; i < S::TM; i++)
 #pragma unroll
-    for (int j = 0; j < S::TN; j++)
+    for (int j0t = 0; j0t < S::TN; j0t += TJ) {
+      const int col = j0 + wn * S::TN * 32 + j0t * 32 + c;
 #pragma unroll
-      for (int e = 0; e < 16; e++)
-        strip[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * PITCH + j * 32 + (lane & 31)] = scale(acc[i][j][e]);
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the strip is written (one wave's)
-    asm volatile("" ::: "memory");
+      for (int j = 0; j < TJ; j++)
 #pragma unroll
-    for (int r = 0; r < 32; r += RPI) {
-      const int rr = r + lane / LPR;
-      const int row = rows[(wm * S::TM + i) * 32 + rr];
-      const f4u v = *reinterpret_cast<const f4u*>(strip + rr * PITCH + c);
-      if (row < 0 || col >= cols) continue;
-      float* const to = out + (long long)row * cols + col;
-      if (col + 4 <= cols) {
-        __builtin_nontemporal_store(v, reinterpret_cast<f4u*>(to));
-      } else {
+        for (int e = 0; e < 16; e++)
+          strip[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * PITCH + j * 32 + (lane & 31)] = scale(acc[i][j0t + j][e]);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the strip is written (one wave's)
+      asm volatile("" ::: "memory");
 #pragma unroll
-        for (int e = 0; e < 3; e++)
-          if (col + e < cols) to[e] = v[e];
+      for (int r = 0; r < 32; r += RPI) {
+        const int rr = r + lane / LPR;
+        const int row = rows[(wm * S::TM + i) * 32 + rr];
+        const f4u v = *reinterpret_cast<const f4u*>(strip + rr * PITCH + c);
+        if (row < 0 || col >= cols) continue;
+        float* const to = out + (long long)row * cols + col;
+        if (col + 4 <= cols) {
+          __builtin_nontemporal_store(v, reinterpret_cast<f4u*>(to));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 3; e++)
+            if (col + e < cols) to[e] = v[e];
+        }
       }
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // (and read, before the next one)
+      asm volatile("" ::: "memory");
     }
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // (and read, before the next one)
-    asm volatile("" ::: "memory");
-  }
 }
 
 template <class S>
 constexpr int strips_of() {  // bytes of the strips; the tile's rows are behind them
-  static_assert(S::NW * 32 * (S::TN * 32 + 8) * 4 + S::BM * 4 <= S::LDS, "the strips and the rows take the ring's place");
-  return S::NW * 32 * (S::TN * 32 + 8) * 4;
+  constexpr int n = S::NW * 32 * ((S::TN < 2 ? 1 : 2) * 32 + 8) * 4;
+  static_assert(n + S::BM * 4 <= S::LDS, "the strips and the rows take the ring's place");
+  return n;
+}
+// The output's rows of a tile's rows.
+template <class S>
+__device__ __forceinline__ void fill_rows(const ConvArgs& a, const Class& k, int i0, int* rows) {
+  for (int r = threadIdx.x; r < S::BM; r += S::THREADS) {
+    const int m = i0 + r;
+    int row = m < k.g.M ? m : -1;
+    if (a.classes && row >= 0) {
+      const unsigned px = fdiv((unsigned)m, k.g.dN), n = (unsigned)m - px * k.g.dN.d, pr = fdiv(px, k.g.dW), pc = px - pr * k.g.dW.d;
+      row = (((int)pr * a.sh + k.h0) * a.W + (int)pc * a.sw + k.w0) * a.N + (int)n;
+    }
+    rows[r] = row;
+  }
 }
 template <class S>
 constexpr bool wide_of() {
@@ -427,10 +449,11 @@ __global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_conv_kernel(co
   const MmaWave<S> me;
   const int lane = me.lane, wave = me.wave;
   const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles, at = b - z * a.tiles;
-  int which = 0;
-  while (which + 1 < a.nclass && at >= a.k[which + 1].first) which++;
-  const Class& k = a.k[which];
-  const int tile = at - k.first, tn = (a.cols + S::BN - 1) / S::BN;
+  // the classes of one place side by side: they read the same rows, and every XCD has as many of the long sums
+  const int tile = at / a.nclass;
+  const Class& k = a.k[at - tile * a.nclass];
+  if (tile >= k.tiles) return;
+  const int tn = (a.cols + S::BN - 1) / S::BN;
   const int ti = tile / tn, i0 = ti * S::BM, j0 = (tile - ti * tn) * S::BN;
   const int steps = k.t.ni * k.t.nj * k.t.nc, s0 = (int)((long long)steps * z / a.slices),
             s1 = (int)((long long)steps * (z + 1) / a.slices);
@@ -446,15 +469,200 @@ __global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_conv_kernel(co
   }
   stage_ready<0>();  // the ring is free
   int* const rows = reinterpret_cast<int*>(lds + strips_of<S>());
-  for (int r = threadIdx.x; r < S::BM; r += S::THREADS) {
-    const int m = i0 + r;
-    int row = m < k.g.M ? m : -1;
-    if (a.classes && row >= 0) {
-      const unsigned px = fdiv((unsigned)m, k.g.dN), n = (unsigned)m - px * k.g.dN.d, pr = fdiv(px, k.g.dW), pc = px - pr * k.g.dW.d;
-      row = (((int)pr * a.sh + k.h0) * a.W + (int)pc * a.sw + k.w0) * a.N + (int)n;
+  fill_rows<S>(a, k, i0, rows);
+  __syncthreads();
+  Scale scale{1.0f, 0};
+  if (a.slices == 1) scale = scale_of(a.ta, a.tb);
+  store_results<S>(reinterpret_cast<float*>(lds), rows, acc, me, scale, a.out + (a.slices == 1 ? 0 : z * a.slice), a.cols, j0);
+}
+
+// ---- the same from codes ------------------------------------------------------------------------
+// The gathered operand stays in codes as far as the registers of the wave that
+// multiplies them, a quarter (4 bit) or half of the bytes through L2 and LDS,
+// and no pass over it before. A step is two runs of 32 channels of every row; a
+// lane takes a run of its row (its eight 16-byte pieces of 8 channels are the
+// products' k, which both operands may take in any order) with the run's four
+// block scales in one dword, and makes 8 values with 16 instructions while the
+// other waves multiply. Each wave has all columns, so no value is made twice in
+// a workgroup. The other operand, small, comes as bf16.
+// c5-sized input gradient (160 x 160 x 32 x 128 from 80 x 80 x 32 x 256, stride
+// 2): this kernel against the one above with its pass before.
+template <int F>
+struct CodeRows {
+  static constexpr int RUN = run_bytes_of(F), SLOTS = 2 * RUN / 16;  // 16-byte slots of a row: 2 (4 bit) or 4 (8 bit)
+  static constexpr int ROW = 16 * SLOTS;
+  // a row's slots are permuted so that sixteen rows' reads of one slot lie in different banks
+  __device__ static int swizzle(int row) { return SLOTS == 2 ? (row >> 3) & 1 : (row >> 2) & 3; }
+};
+
+template <int BM_, int BN_, int ST_, int F>
+struct CodeShape : MmaShape<BM_, BN_, 4, 1, ST_> {
+  typedef MmaShape<BM_, BN_, 4, 1, ST_> Base;
+  static constexpr int SCALES = BM_ * CodeRows<F>::ROW, OTHER = SCALES + BM_ * 8;  // offsets in a stage
+  static constexpr int STAGE = OTHER + BN_ * kPiece, LDS = ST_ * STAGE;
+  static constexpr int LC = BM_ * CodeRows<F>::SLOTS / 64 / 4, LS = BM_ * 2 / 64 / 4, LB = Base::LB;  // loads of a wave: codes, scales, others
+};
+
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mma_lds_t)lds, 4, voff, soff, 0, 0);
+}
+
+template <int F, int LC, int LS, int SCALES>
+struct CodeLoader {
+  typedef CodeRows<F> R;
+  __amdgpu_buffer_rsrc_t codes, scales;
+  int coff[LC], ch[LC], cw[LC], soff[LS], sh[LS], sw[LS];
+  int H, W, cpix, spix, dir, nj, nc, i, j, cb, crun[LC], runs, nCB;
+  __device__ void init(const ConvArgs& a, const Gather& g, const Taps& t, int row0, int step0, int wave, int lane) {
+    codes = mma_rsrc(a.codes, a.codes_bytes);
+    scales = mma_rsrc(a.scales, a.scales_bytes);
+    H = g.H; W = g.W; dir = g.dir; nj = t.nj; nc = t.nc;
+    cpix = g.N * a.rbytes; spix = a.nPB * a.nCB; runs = a.runs; nCB = a.nCB;
+    const int tap = step0 / t.nc;
+    cb = step0 - tap * t.nc; i = tap / t.nj; j = tap - i * t.nj;
+    auto place = [&](int m, int& h, int& w, unsigned& n) {
+      const unsigned px = fdiv((unsigned)m, g.dN), r = fdiv(px, g.dW), c = px - r * g.dW.d;
+      n = (unsigned)m - px * g.dN.d;
+      h = (int)r * g.sr + g.r0;
+      w = (int)c * g.sc + g.c0;
+    };
+#pragma unroll
+    for (int k = 0; k < LC; k++) {
+      const int local = (wave + 4 * k) * (64 / R::SLOTS) + lane / R::SLOTS, m = row0 + local;
+      const int slot = (lane % R::SLOTS) ^ R::swizzle(local);
+      unsigned n;
+      place(m, ch[k], cw[k], n);
+      crun[k] = slot * 16 / R::RUN;
+      coff[k] = (int)((unsigned)(ch[k] * g.W + cw[k]) * (unsigned)cpix + n * (unsigned)a.rbytes) + slot * 16;
+      if (m >= g.M) ch[k] = -(1 << 20);
     }
-    rows[r] = row;
+#pragma unroll
+    for (int k = 0; k < LS; k++) {
+      const int m = row0 + (wave + 4 * k) * 32 + (lane >> 1);
+      unsigned n;
+      place(m, sh[k], sw[k], n);
+      soff[k] = (int)((unsigned)(sh[k] * g.W + sw[k]) * (unsigned)spix + (n >> 3) * (unsigned)a.nCB) + (lane & 1) * 4;
+      if (m >= g.M) sh[k] = -(1 << 20);
+    }
   }
+  // (steps are asked for in order)
+  __device__ void issue(uint8_t* lds, int wave, int lane) {
+    const int di = dir * i, dj = dir * j, at = di * W + dj, cmove = at * cpix, smove = at * spix;
+#pragma unroll
+    for (int k = 0; k < LC; k++) {
+      const bool in = (unsigned)(ch[k] + di) < (unsigned)H && (unsigned)(cw[k] + dj) < (unsigned)W && 2 * cb + crun[k] < runs;
+      load_lds16(codes, lds + (wave + 4 * k) * 1024, in ? coff[k] + cmove : kBeyond, cb * 2 * R::RUN);
+    }
+#pragma unroll
+    for (int k = 0; k < LS; k++) {
+      const bool in = (unsigned)(sh[k] + di) < (unsigned)H && (unsigned)(sw[k] + dj) < (unsigned)W && 8 * cb + (lane & 1) * 4 < nCB;
+      load_lds4(scales, lds + SCALES + (wave + 4 * k) * 256, in ? soff[k] + smove : kBeyond, cb * 8);
+    }
+    if (++cb == nc) {
+      cb = 0;
+      if (++j == nj) { j = 0; i++; }
+    }
+  }
+};
+
+// Eight values of piece kk of a run: words `w` of the run's codes, the four scales in `s`.
+template <int F>
+__device__ __forceinline__ bhalf8 piece_values(const uint32_t* w, uint32_t s, int kk) {
+  float v[8];
+  if constexpr (F == 4) {
+    const uint32_t c = w[kk];
+    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1),
+              d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+    v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1]; v[4] = d[0]; v[5] = d[1]; v[6] = e[0]; v[7] = e[1];
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const uint32_t c = w[2 * kk + h];
+      const v2f a = F == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8(c, false) : __builtin_amdgcn_cvt_pk_f32_bf8(c, false),
+                b = F == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8(c, true) : __builtin_amdgcn_cvt_pk_f32_bf8(c, true);
+      v[4 * h] = a[0]; v[4 * h + 1] = a[1]; v[4 * h + 2] = b[0]; v[4 * h + 3] = b[1];
+    }
+  }
+  float f;
+  switch (kk) {  // (a constant where this is called)
+    case 0: f = __builtin_amdgcn_cvt_f32_fp8(s, 0); break;
+    case 1: f = __builtin_amdgcn_cvt_f32_fp8(s, 1); break;
+    case 2: f = __builtin_amdgcn_cvt_f32_fp8(s, 2); break;
+    default: f = __builtin_amdgcn_cvt_f32_fp8(s, 3); break;
+  }
+  bhalf8 o;
+#pragma unroll
+  for (int e = 0; e < 8; e++) o[e] = (__bf16)(v[e] * f);
+  return o;
+}
+
+template <class S, int F>
+__global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  typedef CodeRows<F> R;
+  constexpr int ST = S::ST, TM = S::TM, TN = S::TN, LPS = S::LC + S::LS + S::LB;
+  const MmaWave<S> me;
+  const int lane = me.lane, wave = me.wave;
+  const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles, at = b - z * a.tiles;
+  const int tile = at / a.nclass;
+  const Class& k = a.k[at - tile * a.nclass];
+  if (tile >= k.tiles) return;
+  const int tn = (a.cols + S::BN - 1) / S::BN;
+  const int ti = tile / tn, i0 = ti * S::BM, j0 = (tile - ti * tn) * S::BN;
+  const int steps = k.t.ni * k.t.nj * k.t.nc, s0 = (int)((long long)steps * z / a.slices),
+            n = (int)((long long)steps * (z + 1) / a.slices) - s0;
+  v16f acc[TM][TN];
+  mma_zero<S>(acc);
+  if (n > 0) {
+    CodeLoader<F, S::LC, S::LS, S::SCALES> la;
+    TapLoader<S::LB, 4> lb;
+    la.init(a, k.g, k.t, i0, s0, wave, lane);
+    lb.init(a.b, a.b_bytes, j0, a.cols, a.b_pitch, k.t, s0, wave, lane);
+    auto issue = [&](int slot) {
+      uint8_t* const to = lds + slot * S::STAGE;
+      la.issue(to, wave, lane);
+      lb.issue(0, to + S::OTHER, wave);
+    };
+#pragma unroll
+    for (int s = 0; s < ST - 1; s++)
+      if (s < n) issue(s);
+    const int r = lane & 31, q = lane >> 5, sw = (r >> 1) & 7;
+    int slot = 0, fill = ST - 1;
+    for (int s = 0; s < n; s++) {
+      if (s + ST - 2 < n) stage_ready<(ST - 2) * LPS>();
+      else stage_ready<0>();
+      if (s + ST - 1 < n) issue(fill);
+      const uint8_t* const from = lds + slot * S::STAGE;
+      uint32_t w[TM][R::RUN / 4], sc[TM];
+#pragma unroll
+      for (int i = 0; i < TM; i++) {
+        const int row = (wave * TM + i) * 32 + r;
+#pragma unroll
+        for (int h = 0; h < R::RUN / 16; h++)
+          *reinterpret_cast<uint4*>(&w[i][4 * h]) =
+              *reinterpret_cast<const uint4*>(from + row * R::ROW + (((q * (R::RUN / 16) + h) ^ R::swizzle(row)) << 4));
+        sc[i] = *reinterpret_cast<const uint32_t*>(from + S::SCALES + row * 8 + q * 4);
+      }
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++) {
+        bhalf8 x[TM], y[TN];
+#pragma unroll
+        for (int j = 0; j < TN; j++)
+          y[j] = *reinterpret_cast<const bhalf8*>(from + S::OTHER + (32 * j + r) * kPiece + (((4 * q + kk) ^ sw) << 4));
+#pragma unroll
+        for (int i = 0; i < TM; i++) x[i] = piece_values<F>(w[i], sc[i], kk);
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+          for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+      }
+      slot = slot + 1 == ST ? 0 : slot + 1;
+      fill = fill + 1 == ST ? 0 : fill + 1;
+    }
+  }
+  stage_ready<0>();  // the ring is free
+  int* const rows = reinterpret_cast<int*>(lds + strips_of<S>());
+  fill_rows<S>(a, k, i0, rows);
   __syncthreads();
   Scale scale{1.0f, 0};
   if (a.slices == 1) scale = scale_of(a.ta, a.tb);
@@ -548,15 +756,36 @@ void with_shape(int s, F&& f) {
   }
 }
 
+// The kernel that takes codes: 4- and 8-bit elements whose rows of scales are
+// whole dwords, at most two tiles of columns (a value is made for each), and
+// rows enough for its tall tiles. 0 slices: the other kernel.
+int code_slices(int op, int fmt, long long M, long long cols, int channels, long long steps) {
+  if (op > 1 || (fmt > 1 && fmt != 4) || cols > 256 || ceil_div(channels, 8) % 4 != 0 || M < 4096) return 0;
+  const long long t = (long long)ceil_div(M, 256) * ceil_div(cols, cols <= 64 ? 64 : 128);
+  return (int)std::max(1LL, std::min({512 / std::max(1LL, t), steps / 8, 64LL}));
+}
+template <class F>
+void with_code_shape(int fmt, bool narrow, F&& f) {
+  auto both = [&](auto fm) {
+    constexpr int E = decltype(fm)::value, ST = E == 4 ? 3 : 2;
+    if (narrow) f(CodeShape<256, 64, ST, E>{}, fm);
+    else f(CodeShape<256, 128, ST, E>{}, fm);
+  };
+  if (fmt == 0) both(std::integral_constant<int, 0>{});
+  else if (fmt == 1) both(std::integral_constant<int, 1>{});
+  else both(std::integral_constant<int, 4>{});
+}
+
 struct Sizes {
   long long a, b, part;  // bytes of the operands and the slices
   Plan plan;
+  int code_slices;
 };
 
 // the longest sum of a class of rows
 int class_taps(int k, int stride) { return ceil_div(k, stride); }
 
-Sizes sizes_of(const Conv& c, int op) {
+Sizes sizes_of(const Conv& c, int op, int fa) {
   const long long ho = c.ho(), wo = c.wo(), taps = (long long)c.kh * c.kw;
   Sizes s{};
   long long out;
@@ -565,12 +794,15 @@ Sizes sizes_of(const Conv& c, int op) {
     s.a = (long long)c.h * c.w * c.n * cp * 2;
     s.b = c.cout * taps * cp * 2;
     s.plan = plan_of(op, ho * wo * c.n, c.cout, taps * (cp / 64));
+    s.code_slices = code_slices(op, fa, ho * wo * c.n, c.cout, c.cin, taps * (cp / 64));
     out = ho * wo * c.n * c.cout;
   } else if (op == 1) {
     const long long kp = up(c.cout, 64);
     s.a = ho * wo * c.n * kp * 2;
     s.b = c.cin * taps * kp * 2;
-    s.plan = plan_of(op, (long long)c.h * c.w * c.n, c.cin, (long long)class_taps(c.kh, c.sh) * class_taps(c.kw, c.sw) * (kp / 64));
+    const long long steps = (long long)class_taps(c.kh, c.sh) * class_taps(c.kw, c.sw) * (kp / 64);
+    s.plan = plan_of(op, (long long)c.h * c.w * c.n, c.cin, steps);
+    s.code_slices = code_slices(op, fa, (long long)c.h * c.w * c.n, c.cin, c.cout, steps);
     out = (long long)c.h * c.w * c.n * c.cin;
   } else {
     const long long np = up(c.n, 8);
@@ -579,73 +811,102 @@ Sizes sizes_of(const Conv& c, int op) {
     s.plan = plan_of(op, c.cout, taps * c.cin, (ho * wo * np + 63) / 64);
     out = c.cout * taps * c.cin;
   }
-  s.part = s.plan.slices > 1 ? out * 4 * s.plan.slices : 0;
+  const int slices = std::max(s.plan.slices, s.code_slices);
+  s.part = slices > 1 ? out * 4 * slices : 0;
   return s;
 }
 
 }  // namespace
 
 bool nvfp_gemm_ok(const Conv& c, int op) {
-  const Sizes s = sizes_of(c, op);
+  const Sizes s = sizes_of(c, op, 2);
   return s.a < kBeyond && s.b < kBeyond;
 }
 
-size_t nvfp_gemm_workspace_bytes(const Conv& c, int op) {
-  const Sizes s = sizes_of(c, op);
+size_t nvfp_gemm_workspace_bytes(const Conv& c, int op, int fa) {
+  const Sizes s = sizes_of(c, op, fa);
   return (size_t)(up(s.a, 256) + up(s.b, 256) + s.part);
 }
 
-static hipError_t join(const Sizes& s, const float* part, float* out, long long n, const float* ta, const float* tb, hipStream_t st) {
-  if (s.plan.slices == 1) return hipSuccess;
+static hipError_t join(int slices, const float* part, float* out, long long n, const float* ta, const float* tb, hipStream_t st) {
+  if (slices == 1) return hipSuccess;
   hipLaunchKernelGGL(nvfp_join_kernel, dim3((unsigned)std::min<long long>(ceil_div(n, 256), 4096)), dim3(256), 0, st, part, out, n,
-                     s.plan.slices, ta, tb);
+                     slices, ta, tb);
   return launch_check();
 }
 
+// The gathered operand's codes where their kernel takes them.
+static bool use_codes(ConvArgs& a, const Sizes& s, const Codes& t) {
+  if (s.code_slices == 0 || ((uintptr_t)t.scales & 3u)) return false;
+  a.codes = t.codes; a.scales = t.scales;
+  const long long pixels = (long long)t.A * t.B;
+  a.codes_bytes = pixels * t.P * t.rbytes; a.scales_bytes = pixels * t.nPB * t.nCB;
+  a.rbytes = t.rbytes; a.runs = ceil_div(t.C, 32); a.nPB = t.nPB; a.nCB = t.nCB;
+  return true;
+}
+
+template <int OP>
+static hipError_t launch_tiles(const ConvArgs& a, const Sizes& s, int fmt, hipStream_t st) {
+  const dim3 grid((unsigned)(a.tiles * a.slices));
+  if (a.codes)
+    with_code_shape(fmt, a.cols <= 64, [&](auto shape, auto f) {
+      hipLaunchKernelGGL((nvfp_codes_kernel<decltype(shape), decltype(f)::value>), grid, dim3(256), 0, st, a);
+    });
+  else
+    with_shape<OP>(s.plan.shape, [&](auto shape) {
+      typedef decltype(shape) S;
+      hipLaunchKernelGGL(nvfp_conv_kernel<S>, grid, dim3(S::THREADS), 0, st, a);
+    });
+  return launch_check();
+}
+static int tiles_for(const ConvArgs& a, const Sizes& s, int M) {
+  if (a.codes) return ceil_div(M, 256) * ceil_div(a.cols, a.cols <= 64 ? 64 : 128);
+  return ceil_div(M, kBM[s.plan.shape]) * ceil_div(a.cols, kBN[s.plan.shape]);
+}
+
 hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView& w, float* y, void* ws, hipStream_t st) {
-  const Sizes s = sizes_of(c, 0);
+  const Sizes s = sizes_of(c, 0, x.fmt);
   const int cp = (int)up(c.cin, 64), taps = c.kh * c.kw, ho = c.ho(), wo = c.wo();
   __bf16* const xb = static_cast<__bf16*>(ws);
   __bf16* const wb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
-  hipError_t e = launch_values(rows_task(codes_of(x, c.h * c.w, c.n, 1, c.cin), xb),
-                               rows_task(codes_of(w, 1, c.cout, taps, c.cin), wb), st);
-  if (e != hipSuccess) return e;
   ConvArgs a{};
+  const Codes xc = codes_of(x, c.h * c.w, c.n, 1, c.cin);
+  const bool codes = use_codes(a, s, xc);
+  hipError_t e = launch_values(rows_task(codes_of(w, 1, c.cout, taps, c.cin), wb), codes ? Task{} : rows_task(xc, xb), st);
+  if (e != hipSuccess) return e;
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * cp * 2; a.cols = c.cout;
-  a.slices = s.plan.slices; a.slice = (long long)ho * wo * c.n * c.cout;
+  a.slices = codes ? s.code_slices : s.plan.slices; a.slice = (long long)ho * wo * c.n * c.cout;
   a.out = a.slices > 1 ? part : y;
   a.ta = x.tensor; a.tb = w.tensor;
   a.nclass = 1;
   Class& k = a.k[0];
   k.g = Gather{xb, s.a, c.h, c.w, c.n, cp * 2, wo, ho * wo * c.n, c.sh, c.sw, -c.ph, -c.pw, 1, make_fastdiv(c.n), make_fastdiv(wo)};
   k.t = Taps{c.kh, c.kw, cp / 64, 0, 0, 1, 1, c.kw};
-  a.tiles = ceil_div(k.g.M, kBM[s.plan.shape]) * ceil_div(c.cout, kBN[s.plan.shape]);
-  with_shape<0>(s.plan.shape, [&](auto shape) {
-    typedef decltype(shape) S;
-    hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a);
-  });
-  if ((e = launch_check()) != hipSuccess) return e;
-  return join(s, part, y, a.slice, a.ta, a.tb, st);
+  k.tiles = a.tiles = tiles_for(a, s, k.g.M);
+  if ((e = launch_tiles<0>(a, s, x.fmt, st)) != hipSuccess) return e;
+  return join(a.slices, part, y, a.slice, a.ta, a.tb, st);
 }
 
 hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const NvfpView& w, float* dx, void* ws, hipStream_t st) {
-  const Sizes s = sizes_of(c, 1);
+  const Sizes s = sizes_of(c, 1, dy.fmt);
   const int kp = (int)up(c.cout, 64), taps = c.kh * c.kw, ho = c.ho(), wo = c.wo();
   __bf16* const yb = static_cast<__bf16*>(ws);
   __bf16* const wb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
-  hipError_t e = launch_values(rows_task(codes_of(dy, ho * wo, c.n, 1, c.cout), yb),
-                               across_task(codes_of(w, 1, c.cout, taps, c.cin), wb, 64), st);
-  if (e != hipSuccess) return e;
   ConvArgs a{};
+  const Codes yc = codes_of(dy, ho * wo, c.n, 1, c.cout);
+  const bool codes = use_codes(a, s, yc);
+  hipError_t e = launch_values(across_task(codes_of(w, 1, c.cout, taps, c.cin), wb, 64), codes ? Task{} : rows_task(yc, yb), st);
+  if (e != hipSuccess) return e;
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * kp * 2; a.cols = c.cin;
-  a.slices = s.plan.slices; a.slice = (long long)c.h * c.w * c.n * c.cin;
+  a.slices = codes ? s.code_slices : s.plan.slices; a.slice = (long long)c.h * c.w * c.n * c.cin;
   a.out = a.slices > 1 ? part : dx;
   a.ta = dy.tensor; a.tb = w.tensor;
   a.sh = c.sh; a.sw = c.sw; a.W = c.w; a.N = c.n;
   a.classes = c.sh > 1 || c.sw > 1;
   const int nh = std::min(c.sh, c.h), nw = std::min(c.sw, c.w);
+  int most = 0;
   for (int q = 0; q < nh * nw; q++) {
     const int h = q / nw, v = q % nw, k0 = (h + c.ph) % c.sh, l0 = (v + c.pw) % c.sw;
     const int rows = ceil_div(c.h - h, c.sh), cols = ceil_div(c.w - v, c.sw);
@@ -656,22 +917,18 @@ hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const Nv
                  make_fastdiv(c.n), make_fastdiv(cols)};
     k.t = Taps{k0 < c.kh ? ceil_div(c.kh - k0, c.sh) : 0, l0 < c.kw ? ceil_div(c.kw - l0, c.sw) : 0, kp / 64, k0, l0, c.sh, c.sw, c.kw};
     if (k.t.ni == 0 || k.t.nj == 0) k.t.ni = 0, k.t.nj = 1;  // (no tap reaches these pixels: zeros)
-    k.tiles = ceil_div(k.g.M, kBM[s.plan.shape]) * ceil_div(c.cin, kBN[s.plan.shape]);
-    k.first = a.tiles;
-    a.tiles += k.tiles;
+    k.tiles = tiles_for(a, s, k.g.M);
+    most = std::max(most, k.tiles);
     if (++a.nclass < kClasses && q + 1 < nh * nw) continue;
-    with_shape<1>(s.plan.shape, [&](auto shape) {
-      typedef decltype(shape) S;
-      hipLaunchKernelGGL(nvfp_conv_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a);
-    });
-    if ((e = launch_check()) != hipSuccess) return e;
-    a.nclass = a.tiles = 0;
+    a.tiles = most * a.nclass;
+    if ((e = launch_tiles<1>(a, s, dy.fmt, st)) != hipSuccess) return e;
+    a.nclass = most = 0;
   }
-  return join(s, part, dx, a.slice, a.ta, a.tb, st);
+  return join(a.slices, part, dx, a.slice, a.ta, a.tb, st);
 }
 
 hipError_t launch_nvfp_backward_weight(const Conv& c, const NvfpView& dy, const NvfpView& x, float* dw, void* ws, hipStream_t st) {
-  const Sizes s = sizes_of(c, 2);
+  const Sizes s = sizes_of(c, 2, dy.fmt);
   const int np = (int)up(c.n, 8), taps = c.kh * c.kw, ho = c.ho(), wo = c.wo();
   __bf16* const yb = static_cast<__bf16*>(ws);
   __bf16* const xb = reinterpret_cast<__bf16*>(static_cast<char*>(ws) + up(s.a, 256));
@@ -693,7 +950,7 @@ hipError_t launch_nvfp_backward_weight(const Conv& c, const NvfpView& dy, const 
     hipLaunchKernelGGL(nvfp_weight_kernel<S>, dim3((unsigned)(a.tiles * a.slices)), dim3(S::THREADS), 0, st, a);
   });
   if ((e = launch_check()) != hipSuccess) return e;
-  return join(s, part, dw, a.slice, a.ta, a.tb, st);
+  return join(a.slices, part, dw, a.slice, a.ta, a.tb, st);
 }
 
 }  // namespace mq

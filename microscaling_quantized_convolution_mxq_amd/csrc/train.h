@@ -28,7 +28,7 @@ struct NvfpView {
 };
 // whether the products' 16-bit operands stay within 32-bit offsets; op 0 forward, 1 backward data, 2 backward weight
 bool nvfp_gemm_ok(const Conv& c, int op);
-size_t nvfp_gemm_workspace_bytes(const Conv& c, int op);
+size_t nvfp_gemm_workspace_bytes(const Conv& c, int op, int fa);  // fa: format of the call's first operand
 hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView& w, float* y, void* ws, hipStream_t st);
 hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const NvfpView& w, float* dx, void* ws, hipStream_t st);
 hipError_t launch_nvfp_backward_weight(const Conv& c, const NvfpView& dy, const NvfpView& x, float* dw, void* ws, hipStream_t st);

@@ -70,11 +70,11 @@ int check_nvfp(const mq_nvfp& t, mq_role role, int32_t d0, int32_t d1, int32_t d
   return MQ_OK;
 }
 
-int check_product(const mq_conv* cv, int op, const float* out, const void* ws, size_t ws_bytes) {
+int check_product(const mq_conv* cv, int op, int fa, const float* out, const void* ws, size_t ws_bytes) {
   if (!nvfp_gemm_ok(to_conv(cv), op)) return MQ_ERR_SHAPE;
   if (!out) return MQ_ERR_NULL;
   if (!aligned4(out)) return MQ_ERR_ALIGN;
-  if (!ws || ws_bytes < nvfp_gemm_workspace_bytes(to_conv(cv), op)) return MQ_ERR_WORKSPACE;
+  if (!ws || ws_bytes < nvfp_gemm_workspace_bytes(to_conv(cv), op, fa)) return MQ_ERR_WORKSPACE;
   return aligned16(ws) ? MQ_OK : MQ_ERR_ALIGN;
 }
 
@@ -174,7 +174,7 @@ int mqconv_layer_norm_backward_mx(const mq_layer_norm* ln, const float* dy, cons
 
 size_t mqconv_nvfp_gemm_workspace_bytes(const mq_conv* cv, int op, mq_elem fa, mq_elem fb) {
   if (!conv_ok(cv) || op < 0 || op > 2 || !fmt_ok(fa) || !fmt_ok(fb) || !nvfp_gemm_ok(to_conv(cv), op)) return 0;
-  return nvfp_gemm_workspace_bytes(to_conv(cv), op);
+  return nvfp_gemm_workspace_bytes(to_conv(cv), op, fa);
 }
 
 int mqconv_nvfp_forward(const mq_conv* cv, mq_nvfp xq, mq_nvfp wq, float* y, void* ws, size_t ws_bytes, void* stream) {
@@ -184,7 +184,7 @@ int mqconv_nvfp_forward(const mq_conv* cv, mq_nvfp xq, mq_nvfp wq, float* y, voi
   int e = check_nvfp(xq, MQ_ROLE_ACT, cv->h, cv->w, cv->n, cv->cin, &x);
   if (e != MQ_OK) return e;
   if ((e = check_nvfp(wq, MQ_ROLE_WEIGHT, cv->cout, cv->kh, cv->kw, cv->cin, &w)) != MQ_OK) return e;
-  if ((e = check_product(cv, 0, y, ws, ws_bytes)) != MQ_OK) return e;
+  if ((e = check_product(cv, 0, x.fmt, y, ws, ws_bytes)) != MQ_OK) return e;
   return hip_status(launch_nvfp_forward(to_conv(cv), x, w, y, ws, (hipStream_t)stream));
 }
 
@@ -197,7 +197,7 @@ int mqconv_nvfp_backward_data(const mq_conv* cv, mq_nvfp dyq, mq_nvfp wq, float*
   int e = check_nvfp(dyq, MQ_ROLE_GRAD, c.ho(), c.wo(), c.n, c.cout, &dy);
   if (e != MQ_OK) return e;
   if ((e = check_nvfp(wq, MQ_ROLE_WEIGHT, c.cout, c.kh, c.kw, c.cin, &w)) != MQ_OK) return e;
-  if ((e = check_product(cv, 1, dx, ws, ws_bytes)) != MQ_OK) return e;
+  if ((e = check_product(cv, 1, dy.fmt, dx, ws, ws_bytes)) != MQ_OK) return e;
   return hip_status(launch_nvfp_backward_data(c, dy, w, dx, ws, (hipStream_t)stream));
 }
 
@@ -210,7 +210,7 @@ int mqconv_nvfp_backward_weight(const mq_conv* cv, mq_nvfp dyq, mq_nvfp xq, floa
   int e = check_nvfp(dyq, MQ_ROLE_GRAD, c.ho(), c.wo(), c.n, c.cout, &dy);
   if (e != MQ_OK) return e;
   if ((e = check_nvfp(xq, MQ_ROLE_ACT, c.h, c.w, c.n, c.cin, &x)) != MQ_OK) return e;
-  if ((e = check_product(cv, 2, dw, ws, ws_bytes)) != MQ_OK) return e;
+  if ((e = check_product(cv, 2, dy.fmt, dw, ws, ws_bytes)) != MQ_OK) return e;
   return hip_status(launch_nvfp_backward_weight(c, dy, x, dw, ws, (hipStream_t)stream));
 }
 

@@ -34,6 +34,13 @@ CONVS = [
     (3, 24, 9, 9, 40, 2, 1, 8, 5, 0, 0), (64, 72, 6, 5, 136, 3, 3, 1, 1, 1, 1), (128, 64, 4, 4, 32, 3, 3, 2, 1, 1, 1),
     (12, 20, 1, 40, 30, 1, 3, 1, 1, 0, 1), (16, 8, 60, 60, 64, 3, 3, 1, 1, 1, 1),
 ]
+# rows enough for the kernel that reads the codes itself: one and two tiles of columns, ragged ones, channels that end inside a
+# run and inside a block, strides (and pixels that no tap reaches), samples that end inside a block, sums in slices, a linear layer
+CODES = [
+    (16, 64, 16, 16, 64, 3, 3, 1, 1, 1, 1), (5, 32, 30, 30, 100, 3, 3, 1, 1, 1, 1), (20, 96, 33, 31, 160, 3, 3, 2, 2, 1, 1),
+    (64, 250, 9, 9, 64, 3, 3, 1, 1, 1, 1), (4100, 320, 1, 1, 70, 1, 1, 1, 1, 0, 0), (7, 58, 40, 39, 30, 5, 3, 1, 2, 2, 0),
+    (9, 27, 60, 61, 32, 1, 1, 2, 2, 0, 0), (33, 128, 23, 24, 224, 2, 2, 3, 1, 1, 0),
+]
 OPS = ("forward", "data", "weight")
 
 
@@ -114,6 +121,14 @@ def test_products_of_four_bit_codes(s):
         _close(s, op, host(_call(s, op, a[0], b[0])), a[1], b[1], "e2m1")
 
 
+@pytest.mark.parametrize("s", CODES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("fmts", [(4, 4, 4), (0, 4, 1), (1, 2, 0)])
+def test_products_from_codes(s, fmts):
+    for op, (a, b) in enumerate(_operands(s, *fmts, seed=200 + sum(s))):
+        if op < 2:
+            _close(s, op, host(_call(s, op, a[0], b[0])), a[1], b[1], str(fmts))
+
+
 @pytest.mark.parametrize("s", [LINEAR[2], LINEAR[5], LINEAR[13], CONVS[2], CONVS[5], CONVS[10]], ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("fmts", [(0, 0, 1), (1, 2, 3), (2, 3, 0), (3, 4, 2), (4, 1, 4), (4, 0, 1)])
 def test_products_of_every_format(s, fmts):
@@ -155,7 +170,7 @@ def test_scales_of_any_size(s):
             _close(s, op, host(_call(s, op, a[0], b[0])), a[1], b[1], f"{sx} {sw}")
 
 
-@pytest.mark.parametrize("s", [LINEAR[4], LINEAR[13], CONVS[2], CONVS[10]], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("s", [LINEAR[4], LINEAR[13], CONVS[2], CONVS[10], CODES[1], CODES[5]], ids=lambda s: "x".join(map(str, s)))
 def test_nan_blocks_reach_their_outputs_alone_and_zeros_give_zeros(s):
     x, w, dy = _inputs(s, 6)
     W, DY = _quantized(w, 1, 4), _quantized(dy, 2, 4)
@@ -179,7 +194,7 @@ def test_nan_blocks_reach_their_outputs_alone_and_zeros_give_zeros(s):
     assert not host(_call(s, 0, Z[0], W[0])).any() and not host(_call(s, 2, DY[0], Z[0])).any()
 
 
-@pytest.mark.parametrize("s", [LINEAR[2], LINEAR[5], LINEAR[13], CONVS[4], CONVS[2]], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("s", [LINEAR[2], LINEAR[5], LINEAR[13], CONVS[4], CONVS[2], CODES[1], CODES[3]], ids=lambda s: "x".join(map(str, s)))
 def test_repeats_strange_addresses_another_stream_and_guards(s):
     for op, (a, b) in enumerate(_operands(s, 4, 4, 4, 77)):
         a, b = a[0], b[0]
@@ -199,7 +214,7 @@ def test_repeats_strange_addresses_another_stream_and_guards(s):
         assert torch.equal(view, ref.reshape(-1)) and (big[:3] == 7).all() and (big[3 + ref.numel():] == 7).all()
 
 
-@pytest.mark.parametrize("s", [LINEAR[2], LINEAR[13], CONVS[2]], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("s", [LINEAR[2], LINEAR[13], CONVS[2], CODES[3]], ids=lambda s: "x".join(map(str, s)))
 def test_graph_replays_are_the_eager_results(s):
     first, second = _operands(s, 4, 4, 4, 41), _operands(s, 4, 4, 4, 42)
     used = [[_clone(t[0]) for t in pair] for pair in first]
