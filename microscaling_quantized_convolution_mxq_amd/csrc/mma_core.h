@@ -50,6 +50,14 @@ __device__ __forceinline__ void stage_ready() {
   asm volatile("" ::: "memory");
 }
 
+// The same for LDS accesses alone: loads stay under way.
+__device__ __forceinline__ void lds_ready() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // A workgroup's tile: BM x BN outputs by WM x WN waves, a ring of ST stages. NG
 // groups of waves each take a part of the steps in a ring of their own, and
 // group 0 adds their sums: with few tiles, a tile's loads and products come from

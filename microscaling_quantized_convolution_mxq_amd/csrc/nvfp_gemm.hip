@@ -24,8 +24,8 @@
 
 #include <algorithm>
 
-#include "block_common.h"
 #include "mma_core.h"
+#include "mx_rows.h"
 #include "train.h"
 
 namespace mq {
@@ -82,10 +82,12 @@ Codes codes_of(const NvfpView& t, int A, int P, int B, int C) {
   return Codes{t.codes, t.scales, t.fmt, A, P, B, C, (int)row_bytes(t.fmt, C), ceil_div(P, 8), ceil_div(C, 8)};
 }
 
-// Channels 8 ch .. 8 ch + 7 of row (ab, p) as bf16; zeros past C.
+typedef unsigned short bits8 __attribute__((ext_vector_type(8)));  // eight 16-bit values
+
+// Channels 8 ch .. 8 ch + 7 of row (ab, p) as bf16, or as f16 (which holds 4-bit elements times their scales too, 6 bits from
+// 2^-10 to 2688); zeros past C.
 template <int F>
-__device__ __forceinline__ bhalf8 values8(const Codes& t, long long row, int ab, int p, int ch) {
-  bhalf8 o;
+__device__ __forceinline__ bits8 values8(const Codes& t, bool half, long long row, int ab, int p, int ch) {
   float v[8];
   const int c0 = 8 * ch;
   if (c0 < t.C) {
@@ -97,9 +99,16 @@ __device__ __forceinline__ bhalf8 values8(const Codes& t, long long row, int ab,
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] = 0.0f;
   }
+  if (half) {
+    half8 o;
+#pragma unroll
+    for (int i = 0; i < 8; i++) o[i] = (_Float16)v[i];
+    return __builtin_bit_cast(bits8, o);
+  }
+  bhalf8 o;
 #pragma unroll
   for (int i = 0; i < 8; i++) o[i] = (__bf16)v[i];
-  return o;
+  return __builtin_bit_cast(bits8, o);
 }
 
 // f(the format as a constant); the format is the same for a whole workgroup
@@ -114,13 +123,13 @@ __device__ __forceinline__ void by_format(int fmt, L&& f) {
   }
 }
 
-// An operand as bf16, either
+// An operand as 16-bit values, either
 //   out[row][Cp], Cp a multiple of 64: 8 channels a thread, or
 //   out[c][ab][Pp], Pp a multiple of 8: tiles of 64 channels x 64 of the (ab, p).
 struct Task {
   Codes t;
   __bf16* out;
-  bool across;
+  bool across, half;     // half: f16 instead of bf16
   int groups;            // workgroups
   int n;                 // pieces of 8 channels
   FastDiv pieces, dP, dB;
@@ -134,24 +143,22 @@ __device__ __forceinline__ void make_rows(const Task& a, int group) {
   if (i >= (unsigned)a.n) return;
   const unsigned row = fdiv(i, a.pieces), ch = i - row * a.pieces.d;
   const unsigned q = fdiv(row, a.dB), b = row - q * a.dB.d, aa = fdiv(q, a.dP), p = q - aa * a.dP.d;
-  *reinterpret_cast<bhalf8*>(a.out + (long long)i * 8) = values8<F>(a.t, row, (int)(aa * a.dB.d + b), (int)p, (int)ch);
+  *reinterpret_cast<bits8*>(a.out + (long long)i * 8) = values8<F>(a.t, a.half, row, (int)(aa * a.dB.d + b), (int)p, (int)ch);
 }
 
 constexpr int kAcross = 66;  // a column of the tile (eight threads of one slot write 8 channels each, 264 dwords apart: eight banks)
 template <int F>
-__device__ __forceinline__ void make_across(const Task& a, int group, __bf16* tile) {
+__device__ __forceinline__ void make_across(const Task& a, int group, unsigned short* tile) {
   const int ct = group / a.tiles, s0 = (group - ct * a.tiles) * 64, c0 = ct * 64;
 #pragma unroll
   for (int i = threadIdx.x; i < 512; i += 256) {
     const int ch = i & 7, slot = i >> 3, s = s0 + slot;
-    bhalf8 v;
-#pragma unroll
-    for (int e = 0; e < 8; e++) v[e] = (__bf16)0.0f;
+    bits8 v = {0, 0, 0, 0, 0, 0, 0, 0};
     if (s < a.S) {
       const unsigned ab = fdiv((unsigned)s, a.dPp), p = (unsigned)s - ab * a.dPp.d;
       if ((int)p < a.t.P) {
         const unsigned aa = fdiv(ab, a.dB), b = ab - aa * a.dB.d;
-        v = values8<F>(a.t, ((long long)aa * a.t.P + p) * a.dB.d + b, (int)ab, (int)p, (c0 >> 3) + ch);
+        v = values8<F>(a.t, a.half, ((long long)aa * a.t.P + p) * a.dB.d + b, (int)ab, (int)p, (c0 >> 3) + ch);
       }
     }
 #pragma unroll
@@ -169,7 +176,7 @@ __device__ __forceinline__ void make_across(const Task& a, int group, __bf16* ti
 
 // Both operands in one launch.
 __global__ __launch_bounds__(256) void nvfp_values_kernel(const Task a, const Task b) {
-  __shared__ __attribute__((aligned(16))) __bf16 tile[64 * kAcross];
+  __shared__ __attribute__((aligned(16))) unsigned short tile[64 * kAcross];
   const bool first = (int)blockIdx.x < a.groups;
   const Task& t = first ? a : b;
   const int group = first ? (int)blockIdx.x : (int)blockIdx.x - a.groups;
@@ -374,10 +381,10 @@ struct ConvArgs {
 };
 
 // A wave's results through LDS, 32 rows at a time, to whole pieces of rows: `rows` has the tile's rows in the output (-1: none).
-template <class S>
+template <class S, int MOST = 2>
 __device__ __forceinline__ void store_results(float* strips, const int* rows, v16f (&acc)[S::TM][S::TN], const MmaWave<S>& me,
                                               const Scale& scale, float* out, int cols, int j0) {
-  constexpr int TJ = S::TN < 2 ? 1 : 2, WIDE = TJ * 32, PITCH = WIDE + 8;  // (rows r and r + 4 are written together: the other half of the banks)
+  constexpr int TJ = S::TN < MOST ? S::TN : MOST, WIDE = TJ * 32, PITCH = WIDE + 8;  // (rows r and r + 4 are written together: the other half of the banks)
   static_assert(S::TN % TJ == 0, "strips");
   const int lane = me.lane, wm = me.wave / S::WN, wn = me.wave % S::WN;
   float* const strip = strips + me.wave * 32 * PITCH;
@@ -565,9 +572,23 @@ struct CodeLoader {
   }
 };
 
-// Eight values of piece kk of a run: words `w` of the run's codes, the four scales in `s`.
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+
+// Eight values of piece kk of a run: words `w` of the run's codes, the four
+// scales in `s`. As f16, 4-bit elements take 4 conversions and 4 packed
+// products; as bf16, whose products have no packed form, twice as many.
 template <int F>
-__device__ __forceinline__ bhalf8 piece_values(const uint32_t* w, uint32_t s, int kk) {
+__device__ __forceinline__ half8 piece_values(const uint32_t* w, uint32_t s, int kk, half8) {
+  static_assert(F == 4, "4-bit elements");
+  const uint32_t c = w[kk];
+  const half2v two = kk < 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s, 1.0f, false) : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s, 1.0f, true);
+  const half2v f = {two[kk & 1], two[kk & 1]};
+  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 0) * f, b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 1) * f,
+               d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 2) * f, e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 3) * f;
+  return half8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+}
+template <int F>
+__device__ __forceinline__ bhalf8 piece_values(const uint32_t* w, uint32_t s, int kk, bhalf8) {
   float v[8];
   if constexpr (F == 4) {
     const uint32_t c = w[kk];
@@ -596,37 +617,84 @@ __device__ __forceinline__ bhalf8 piece_values(const uint32_t* w, uint32_t s, in
   return o;
 }
 
-template <class S, int F>
+// Tiles t of a launch for a workgroup that takes several: each XCD has a contiguous range of them.
+struct TileWalk {
+  int at, end, step;
+  __device__ explicit TileWalk(int total) {
+    const int x = blockIdx.x & 7, q = total >> 3, r = total & 7;
+    at = x * q + min(x, r);
+    end = at + q + (x < r ? 1 : 0);
+    at += blockIdx.x >> 3;
+    step = ((int)gridDim.x + 7 - x) >> 3;
+  }
+};
+
+// Workgroups stay and walk over the tiles: one for each left the chip half
+// empty, as sums are short (a workgroup of four waves lived 20 us, and a place
+// waited as long for the next). The first loads of a tile are under way while
+// the results of the one before are stored, from the end of the ring.
+__device__ __forceinline__ v16f multiply(half8 x, half8 y, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, c, 0, 0, 0); }
+__device__ __forceinline__ v16f multiply(bhalf8 x, bhalf8 y, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0); }
+
+template <class S, int F, class V>
 __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   typedef CodeRows<F> R;
   constexpr int ST = S::ST, TM = S::TM, TN = S::TN, LPS = S::LC + S::LS + S::LB;
+  constexpr int STRIPS = 4 * 32 * 40 * 4, KEPT = STRIPS + S::BM * 4;  // strips of 32 columns, and the tile's rows
+  constexpr int FREE = (S::LDS - KEPT) / S::STAGE, PRE = FREE < ST - 1 ? FREE : ST - 1;
+  static_assert(PRE >= 1, "a stage beside the strips");
+  float* const strips = reinterpret_cast<float*>(lds + S::LDS - KEPT);
+  int* const rows = reinterpret_cast<int*>(lds + S::LDS - S::BM * 4);
   const MmaWave<S> me;
   const int lane = me.lane, wave = me.wave;
-  const int b = xcd_tile(blockIdx.x, gridDim.x), z = b / a.tiles, at = b - z * a.tiles;
-  const int tile = at / a.nclass;
-  const Class& k = a.k[at - tile * a.nclass];
-  if (tile >= k.tiles) return;
+  const int r = lane & 31, q = lane >> 5, sw = (r >> 1) & 7;
   const int tn = (a.cols + S::BN - 1) / S::BN;
-  const int ti = tile / tn, i0 = ti * S::BM, j0 = (tile - ti * tn) * S::BN;
-  const int steps = k.t.ni * k.t.nj * k.t.nc, s0 = (int)((long long)steps * z / a.slices),
-            n = (int)((long long)steps * (z + 1) / a.slices) - s0;
-  v16f acc[TM][TN];
-  mma_zero<S>(acc);
-  if (n > 0) {
-    CodeLoader<F, S::LC, S::LS, S::SCALES> la;
-    TapLoader<S::LB, 4> lb;
-    la.init(a, k.g, k.t, i0, s0, wave, lane);
-    lb.init(a.b, a.b_bytes, j0, a.cols, a.b_pitch, k.t, s0, wave, lane);
-    auto issue = [&](int slot) {
-      uint8_t* const to = lds + slot * S::STAGE;
-      la.issue(to, wave, lane);
-      lb.issue(0, to + S::OTHER, wave);
-    };
+  Scale scale{1.0f, 0};
+  if (a.slices == 1) scale = scale_of(a.ta, a.tb);
+
+  TileWalk walk(a.tiles * a.slices);
+  CodeLoader<F, S::LC, S::LS, S::SCALES> la;
+  TapLoader<S::LB, 4> lb;
+  int which = 0, i0 = 0, j0 = 0, z = 0, n = 0;
+  auto issue = [&](int slot) {
+    uint8_t* const to = lds + slot * S::STAGE;
+    la.issue(to, wave, lane);
+    lb.issue(0, to + S::OTHER, wave);
+  };
+  // the next tile and its first loads; false: there is none
+  auto next = [&]() {
+    for (; walk.at < walk.end; walk.at += walk.step) {
+      z = walk.at / a.tiles;
+      const int at = walk.at - z * a.tiles, tile = at / a.nclass;
+      // (turned from place to place, or a workgroup whose step is a multiple of their number would always meet the same class)
+      which = (at + tile + (tile >> 4)) % a.nclass;
+      const Class& k = a.k[which];
+      if (tile >= k.tiles) continue;
+      const int ti = tile / tn, steps = k.t.ni * k.t.nj * k.t.nc, s0 = (int)((long long)steps * z / a.slices);
+      i0 = ti * S::BM;
+      j0 = (tile - ti * tn) * S::BN;
+      n = (int)((long long)steps * (z + 1) / a.slices) - s0;
+      if (n > 0) {
+        la.init(a, k.g, k.t, i0, s0, wave, lane);
+        lb.init(a.b, a.b_bytes, j0, a.cols, a.b_pitch, k.t, s0, wave, lane);
 #pragma unroll
-    for (int s = 0; s < ST - 1; s++)
+        for (int s = 0; s < PRE; s++)
+          if (s < n) issue(s);
+      }
+      walk.at += walk.step;
+      return true;
+    }
+    return false;
+  };
+
+  bool more = next();
+  while (more) {
+    v16f acc[TM][TN];
+    mma_zero<S>(acc);
+#pragma unroll
+    for (int s = PRE; s < ST - 1; s++)
       if (s < n) issue(s);
-    const int r = lane & 31, q = lane >> 5, sw = (r >> 1) & 7;
     int slot = 0, fill = ST - 1;
     for (int s = 0; s < n; s++) {
       if (s + ST - 2 < n) stage_ready<(ST - 2) * LPS>();
@@ -645,28 +713,29 @@ __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
       }
 #pragma unroll
       for (int kk = 0; kk < 4; kk++) {
-        bhalf8 x[TM], y[TN];
+        V x[TM], y[TN];
 #pragma unroll
         for (int j = 0; j < TN; j++)
-          y[j] = *reinterpret_cast<const bhalf8*>(from + S::OTHER + (32 * j + r) * kPiece + (((4 * q + kk) ^ sw) << 4));
+          y[j] = *reinterpret_cast<const V*>(from + S::OTHER + (32 * j + r) * kPiece + (((4 * q + kk) ^ sw) << 4));
 #pragma unroll
-        for (int i = 0; i < TM; i++) x[i] = piece_values<F>(w[i], sc[i], kk);
+        for (int i = 0; i < TM; i++) x[i] = piece_values<F>(w[i], sc[i], kk, V{});
 #pragma unroll
         for (int i = 0; i < TM; i++)
 #pragma unroll
-          for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < TN; j++) acc[i][j] = multiply(x[i], y[j], acc[i][j]);
       }
       slot = slot + 1 == ST ? 0 : slot + 1;
       fill = fill + 1 == ST ? 0 : fill + 1;
     }
+    stage_ready<0>();  // the ring is free
+    fill_rows<S>(a, a.k[which], i0, rows);
+    float* const out = a.out + (a.slices == 1 ? 0 : z * a.slice);
+    const int c0 = j0;
+    more = next();
+    lds_ready();  // the rows are known
+    store_results<S, 1>(strips, rows, acc, me, scale, out, a.cols, c0);
+    if (PRE < ST - 1) lds_ready();  // (the strips are read: loads may go there)
   }
-  stage_ready<0>();  // the ring is free
-  int* const rows = reinterpret_cast<int*>(lds + strips_of<S>());
-  fill_rows<S>(a, k, i0, rows);
-  __syncthreads();
-  Scale scale{1.0f, 0};
-  if (a.slices == 1) scale = scale_of(a.ta, a.tb);
-  store_results<S>(reinterpret_cast<float*>(lds), rows, acc, me, scale, a.out + (a.slices == 1 ? 0 : z * a.slice), a.cols, j0);
 }
 
 struct WeightArgs {
@@ -765,15 +834,16 @@ int code_slices(int op, int fmt, long long M, long long cols, int channels, long
   return (int)std::max(1LL, std::min({512 / std::max(1LL, t), steps / 8, 64LL}));
 }
 template <class F>
-void with_code_shape(int fmt, bool narrow, F&& f) {
-  auto both = [&](auto fm) {
+void with_code_shape(int fmt, bool half, bool narrow, F&& f) {
+  auto both = [&](auto fm, auto v) {
     constexpr int E = decltype(fm)::value, ST = E == 4 ? 3 : 2;
-    if (narrow) f(CodeShape<256, 64, ST, E>{}, fm);
-    else f(CodeShape<256, 128, ST, E>{}, fm);
+    if (narrow) f(CodeShape<256, 64, ST, E>{}, fm, v);
+    else f(CodeShape<256, 128, ST, E>{}, fm, v);
   };
-  if (fmt == 0) both(std::integral_constant<int, 0>{});
-  else if (fmt == 1) both(std::integral_constant<int, 1>{});
-  else both(std::integral_constant<int, 4>{});
+  if (fmt == 0) both(std::integral_constant<int, 0>{}, bhalf8{});
+  else if (fmt == 1) both(std::integral_constant<int, 1>{}, bhalf8{});
+  else if (half) both(std::integral_constant<int, 4>{}, half8{});
+  else both(std::integral_constant<int, 4>{}, bhalf8{});
 }
 
 struct Sizes {
@@ -846,11 +916,13 @@ static bool use_codes(ConvArgs& a, const Sizes& s, const Codes& t) {
 }
 
 template <int OP>
-static hipError_t launch_tiles(const ConvArgs& a, const Sizes& s, int fmt, hipStream_t st) {
+static hipError_t launch_tiles(const ConvArgs& a, const Sizes& s, int fmt, bool half, hipStream_t st) {
   const dim3 grid((unsigned)(a.tiles * a.slices));
   if (a.codes)
-    with_code_shape(fmt, a.cols <= 64, [&](auto shape, auto f) {
-      hipLaunchKernelGGL((nvfp_codes_kernel<decltype(shape), decltype(f)::value>), grid, dim3(256), 0, st, a);
+    with_code_shape(fmt, half, a.cols <= 64, [&](auto shape, auto f, auto v) {
+      const auto kern = nvfp_codes_kernel<decltype(shape), decltype(f)::value, decltype(v)>;
+      static const int resident = resident_groups(reinterpret_cast<const void*>(kern), 256) / 8 * 8;
+      hipLaunchKernelGGL(kern, dim3((unsigned)std::min(a.tiles * a.slices, std::max(8, resident))), dim3(256), 0, st, a);
     });
   else
     with_shape<OP>(s.plan.shape, [&](auto shape) {
@@ -873,7 +945,10 @@ hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView&
   ConvArgs a{};
   const Codes xc = codes_of(x, c.h * c.w, c.n, 1, c.cin);
   const bool codes = use_codes(a, s, xc);
-  hipError_t e = launch_values(rows_task(codes_of(w, 1, c.cout, taps, c.cin), wb), codes ? Task{} : rows_task(xc, xb), st);
+  const bool half = codes && x.fmt == 4 && w.fmt == 4;
+  Task wt = rows_task(codes_of(w, 1, c.cout, taps, c.cin), wb);
+  wt.half = half;
+  hipError_t e = launch_values(wt, codes ? Task{} : rows_task(xc, xb), st);
   if (e != hipSuccess) return e;
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * cp * 2; a.cols = c.cout;
   a.slices = codes ? s.code_slices : s.plan.slices; a.slice = (long long)ho * wo * c.n * c.cout;
@@ -884,7 +959,7 @@ hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView&
   k.g = Gather{xb, s.a, c.h, c.w, c.n, cp * 2, wo, ho * wo * c.n, c.sh, c.sw, -c.ph, -c.pw, 1, make_fastdiv(c.n), make_fastdiv(wo)};
   k.t = Taps{c.kh, c.kw, cp / 64, 0, 0, 1, 1, c.kw};
   k.tiles = a.tiles = tiles_for(a, s, k.g.M);
-  if ((e = launch_tiles<0>(a, s, x.fmt, st)) != hipSuccess) return e;
+  if ((e = launch_tiles<0>(a, s, x.fmt, half, st)) != hipSuccess) return e;
   return join(a.slices, part, y, a.slice, a.ta, a.tb, st);
 }
 
@@ -897,7 +972,10 @@ hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const Nv
   ConvArgs a{};
   const Codes yc = codes_of(dy, ho * wo, c.n, 1, c.cout);
   const bool codes = use_codes(a, s, yc);
-  hipError_t e = launch_values(across_task(codes_of(w, 1, c.cout, taps, c.cin), wb, 64), codes ? Task{} : rows_task(yc, yb), st);
+  const bool half = codes && dy.fmt == 4 && w.fmt == 4;
+  Task wt = across_task(codes_of(w, 1, c.cout, taps, c.cin), wb, 64);
+  wt.half = half;
+  hipError_t e = launch_values(wt, codes ? Task{} : rows_task(yc, yb), st);
   if (e != hipSuccess) return e;
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * kp * 2; a.cols = c.cin;
   a.slices = codes ? s.code_slices : s.plan.slices; a.slice = (long long)c.h * c.w * c.n * c.cin;
@@ -921,7 +999,7 @@ hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const Nv
     most = std::max(most, k.tiles);
     if (++a.nclass < kClasses && q + 1 < nh * nw) continue;
     a.tiles = most * a.nclass;
-    if ((e = launch_tiles<1>(a, s, dy.fmt, st)) != hipSuccess) return e;
+    if ((e = launch_tiles<1>(a, s, dy.fmt, half, st)) != hipSuccess) return e;
     a.nclass = most = 0;
   }
   return join(a.slices, part, dx, a.slice, a.ta, a.tb, st);
