@@ -35,12 +35,11 @@ namespace {
 typedef float v2f __attribute__((ext_vector_type(2)));
 
 // ---- values of codes ----------------------------------------------------------------------------
-// Eight neighbouring codes (4, 6 or 8 bytes at p) as floats.
+// Eight neighbouring codes, 32, 48 or 64 bits in two words, as floats.
 template <int F>
-__device__ __forceinline__ void decode8(const uint8_t* p, float (&v)[8]) {
+__device__ __forceinline__ void decode8_words(uint32_t lo, uint32_t hi, float (&v)[8]) {
   if constexpr (Fmt<F>::bits == 8) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    const uint32_t u[2] = {w.x, w.y};
+    const uint32_t u[2] = {lo, hi};
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       v2f a, b;
@@ -54,8 +53,7 @@ __device__ __forceinline__ void decode8(const uint8_t* p, float (&v)[8]) {
       v[4 * i] = a[0]; v[4 * i + 1] = a[1]; v[4 * i + 2] = b[0]; v[4 * i + 3] = b[1];
     }
   } else if constexpr (Fmt<F>::bits == 6) {
-    const uint16_t* const h = reinterpret_cast<const uint16_t*>(p);
-    const uint64_t w = (uint64_t)h[0] | (uint64_t)h[1] << 16 | (uint64_t)h[2] << 32;
+    const uint64_t w = (uint64_t)lo | (uint64_t)hi << 32;
     // magnitude bits as the top of an fp32's: its exponent is off by 127 - bias, subnormals included
     constexpr float up = __builtin_bit_cast(float, (uint32_t)(254 - Fmt<F>::bias) << 23);
 #pragma unroll
@@ -64,10 +62,22 @@ __device__ __forceinline__ void decode8(const uint8_t* p, float (&v)[8]) {
       v[i] = __uint_as_float((c & 31u) << (23 - Fmt<F>::M) | (c & 32u) << 26) * up;
     }
   } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1),
-              c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 1),
+              c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 3);
     v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1]; v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
+  }
+}
+// The same from memory.
+template <int F>
+__device__ __forceinline__ void decode8(const uint8_t* p, float (&v)[8]) {
+  if constexpr (Fmt<F>::bits == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    decode8_words<F>(w.x, w.y, v);
+  } else if constexpr (Fmt<F>::bits == 6) {
+    const uint16_t* const h = reinterpret_cast<const uint16_t*>(p);
+    decode8_words<F>((uint32_t)h[0] | (uint32_t)h[1] << 16, h[2], v);
+  } else {
+    decode8_words<F>(*reinterpret_cast<const uint32_t*>(p), 0, v);
   }
 }
 
@@ -113,7 +123,7 @@ __device__ __forceinline__ bits8 values8(const Codes& t, bool half, long long ro
 
 // f(the format as a constant); the format is the same for a whole workgroup
 template <class L>
-__device__ __forceinline__ void by_format(int fmt, L&& f) {
+__host__ __device__ __forceinline__ void by_format(int fmt, L&& f) {
   switch (fmt) {
     case 0: f(std::integral_constant<int, 0>{}); break;
     case 1: f(std::integral_constant<int, 1>{}); break;
@@ -738,6 +748,115 @@ __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
   }
 }
 
+// ---- a linear layer for a few rows --------------------------------------------------------------
+// Y[n][co] for up to 8 samples, bound by reading W's codes once: no values are
+// written, no matrix units (a tile of 64 rows would be empty). A lane takes the
+// same run of 32 channels of R rows of W and of every sample; the products of
+// the codes' own values (exact in fp32) are summed over a block's 8 channels and
+// then take the two block scales, so a scale costs an eighth of a product. The
+// four rows lie in one block of 8 along Cout, so they share the scales, and all
+// samples lie in one along N. Waves of a workgroup share the channels between
+// them where these are many.
+// 4096 x 4096 E2M1 at one sample: 5.1 us on the device (8.9 MB of codes and
+// scales, 1.75 TB/s: one round of loads, so their latency) against 12.7 through
+// the tiles, whose values of W alone are 33.5 MB written and read. A call with its
+// host part is 9.2 us at 1 and 2 samples, 9.6 at 4 and 14.6 at 8, through the
+// tiles 25 us at any of them.
+// Operands of two formats take it at one sample only: to decode the second by a
+// switch in the loop over samples needs more registers than there are.
+constexpr int kRowR = 4;
+
+// A run's 32 codes in registers.
+template <int F>
+struct Run {
+  static constexpr int WORDS = run_bytes_of(F) / 4;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 2) *reinterpret_cast<uint2*>(w + i) = *reinterpret_cast<const uint2*>(p + 4 * i);
+  }
+  // the values of block b's eight codes
+  __device__ __forceinline__ void values(int b, float (&v)[8]) const {
+    if constexpr (Fmt<F>::bits == 8) decode8_words<F>(w[2 * b], w[2 * b + 1], v);
+    else if constexpr (Fmt<F>::bits == 4) decode8_words<F>(w[b], 0, v);
+    else if (b & 1) decode8_words<F>(w[3 * (b / 2) + 1] >> 16 | w[3 * (b / 2) + 2] << 16, w[3 * (b / 2) + 2] >> 16, v);
+    else decode8_words<F>(w[3 * (b / 2)], w[3 * (b / 2) + 1] & 0xffffu, v);
+  }
+};
+
+// SAME: both operands have the format FW (else x's is looked up, and M is 1).
+template <int FW, bool SAME, int M>
+__global__ __launch_bounds__(256, M == 8 ? 2 : 4) void nvfp_few_rows_kernel(const Codes x, const Codes w, const float* ta, const float* tb,
+                                                                float* y, int N, int cols, int along) {
+  __shared__ float sums[4][M][kRowR];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave % along, co0 = (blockIdx.x * (4 / along) + wave / along) * kRowR;
+  const int runs = (w.C + 31) / 32;
+  float acc[M][kRowR];
+#pragma unroll
+  for (int m = 0; m < M; m++)
+#pragma unroll
+    for (int r = 0; r < kRowR; r++) acc[m][r] = 0;
+  for (int run = part * 64 + lane; run < runs && co0 < cols; run += 64 * along) {
+    Run<FW> wr[kRowR], xr[SAME ? M : 1];
+#pragma unroll
+    for (int r = 0; r < kRowR; r++) wr[r].load(w.codes + (long long)min(co0 + r, cols - 1) * w.rbytes + run * run_bytes_of(FW));
+    if constexpr (SAME)
+#pragma unroll
+      for (int m = 0; m < M; m++) xr[m].load(x.codes + (long long)min(m, N - 1) * x.rbytes + run * run_bytes_of(FW));
+    float s[4];
+#pragma unroll
+    for (int b = 0; b < 4; b++) {  // the run's blocks (the last run may have fewer)
+      const bool in = 4 * run + b < w.nCB;
+      const int at = in ? 4 * run + b : 0;
+      s[b] = __builtin_amdgcn_cvt_f32_fp8(w.scales[(long long)(co0 >> 3) * w.nCB + at], 0) *
+             __builtin_amdgcn_cvt_f32_fp8(x.scales[at], 0);
+      s[b] = in ? s[b] : 0.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < 4; b++) {
+      float v[kRowR][8];
+#pragma unroll
+      for (int r = 0; r < kRowR; r++) wr[r].values(b, v[r]);
+#pragma unroll
+      for (int m = 0; m < M; m++) {
+        float u[8];
+        if constexpr (SAME) {
+          xr[m].values(b, u);
+        } else {
+          by_format(x.fmt, [&](auto f) {
+            constexpr int F = decltype(f)::value;
+            decode8<F>(x.codes + (long long)min(m, N - 1) * x.rbytes + run * run_bytes_of(F) + b * Fmt<F>::bits, u);
+          });
+        }
+#pragma unroll
+        for (int r = 0; r < kRowR; r++) {
+          float d = u[0] * v[r][0];
+#pragma unroll
+          for (int e = 1; e < 8; e++) d = __builtin_fmaf(u[e], v[r][e], d);
+          acc[m][r] = __builtin_fmaf(d, s[b], acc[m][r]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; m++)
+#pragma unroll
+    for (int r = 0; r < kRowR; r++) {
+#pragma unroll
+      for (int off = 1; off < 64; off *= 2) acc[m][r] += __shfl_xor(acc[m][r], off);
+      if (lane == 0) sums[wave][m][r] = acc[m][r];
+    }
+  __syncthreads();
+  if (part != 0 || lane >= M * kRowR) return;
+  const int m = lane / kRowR, r = lane % kRowR;
+  if (m >= N || co0 + r >= cols) return;
+  float s = sums[wave][m][r];
+  for (int k = 1; k < along; k++) s += sums[wave + k][m][r];
+  const Scale scale = scale_of(ta, tb);
+  y[(long long)m * cols + co0 + r] = scale(s);
+}
+
 struct WeightArgs {
   const __bf16* dy;
   long long dy_bytes;
@@ -936,7 +1055,31 @@ static int tiles_for(const ConvArgs& a, const Sizes& s, int M) {
   return ceil_div(M, kBM[s.plan.shape]) * ceil_div(a.cols, kBN[s.plan.shape]);
 }
 
+// Whether the kernel for a few rows takes it: a linear layer.
+static bool few_rows(const Conv& c, bool same) {
+  return c.n <= (same ? 8 : 1) && c.h == 1 && c.w == 1 && c.kh == 1 && c.kw == 1;
+}
+
+static hipError_t launch_few_rows(const Conv& c, const NvfpView& x, const NvfpView& w, float* y, hipStream_t st) {
+  const Codes xc = codes_of(x, 1, c.n, 1, c.cin), wc = codes_of(w, 1, c.cout, 1, c.cin);
+  const int pieces = ceil_div(c.cin, 2048), along = pieces >= 4 ? 4 : (pieces >= 2 ? 2 : 1);
+  const dim3 grid((unsigned)ceil_div(c.cout, kRowR * (4 / along)));
+  by_format(w.fmt, [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    const auto go = [&](auto kern) {
+      hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, xc, wc, x.tensor, w.tensor, y, c.n, c.cout, along);
+    };
+    if (x.fmt != w.fmt) go(nvfp_few_rows_kernel<F, false, 1>);
+    else if (c.n == 1) go(nvfp_few_rows_kernel<F, true, 1>);
+    else if (c.n == 2) go(nvfp_few_rows_kernel<F, true, 2>);
+    else if (c.n <= 4) go(nvfp_few_rows_kernel<F, true, 4>);
+    else go(nvfp_few_rows_kernel<F, true, 8>);
+  });
+  return launch_check();
+}
+
 hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView& w, float* y, void* ws, hipStream_t st) {
+  if (few_rows(c, x.fmt == w.fmt)) return launch_few_rows(c, x, w, y, st);
   const Sizes s = sizes_of(c, 0, x.fmt);
   const int cp = (int)up(c.cin, 64), taps = c.kh * c.kw, ho = c.ho(), wo = c.wo();
   __bf16* const xb = static_cast<__bf16*>(ws);

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 from typing import Optional, Sequence, Tuple
 
 import microscaling_quantized_convolution_mxq_amd as _mq
@@ -187,41 +188,53 @@ class NvfpTensor:
 
     def c_struct(self, what: str = "NvfpTensor") -> mq_nvfp:
         """The C view; tensor buffers are checked against the sizes the layout needs."""
-        d = _int32(what, *self.dims)
-        return mq_nvfp(_mq._buf(self.codes, _mq.mqconv_codes_bytes(self.role, self.fmt, *d), "uint8", what + ".codes"),
-                       _mq._buf(self.scales, _mq.mqconv_nvfp_scales_bytes(self.role, *d), "uint8", what + ".scales"),
-                       _mq._f32(self.tensor_scale, 1, what + ".tensor_scale"), self.fmt, self.role, *d)
+        d = tuple(self.dims)
+        nc, ns = _sizes(self.role, self.fmt, d)
+        return mq_nvfp(_mq._buf(self.codes, nc, "uint8", what), _mq._buf(self.scales, ns, "uint8", what),
+                       _mq._buf(self.tensor_scale, 4, "float32", what), self.fmt, self.role, *d)
 
 
-def _conv32(shape) -> _mq.mq_conv:
-    t = shape.as_tuple() if hasattr(shape, "as_tuple") else tuple(shape)
-    return _mq.mq_conv(*_int32("shape", *t))
+@functools.lru_cache(maxsize=1024)
+def _sizes(role: int, fmt: int, dims):
+    """Bytes of codes and block scales of a two-level tensor."""
+    d = _int32("NvfpTensor", *dims)
+    return _mq.mqconv_codes_bytes(role, fmt, *d), _mq.mqconv_nvfp_scales_bytes(role, *d)
+
+
+@functools.lru_cache(maxsize=1024)
+def _geometry(t):
+    """The C descriptor of a convolution (read by the calls, never written), and the values of x, w and y."""
+    return _mq.mq_conv(*_int32("shape", *t)), _mq._nx(t), _mq._nw(t), _mq._ny(t)
+
+
+def _conv(shape):
+    return _geometry(shape.as_tuple() if hasattr(shape, "as_tuple") else tuple(shape))
 
 
 def mqconv_nvfp_gemm_workspace_bytes(shape, op: int, fa: int, fb: int) -> int:
-    return _lib().mqconv_nvfp_gemm_workspace_bytes(ctypes.byref(_conv32(shape)), op, fa, fb)
+    return _lib().mqconv_nvfp_gemm_workspace_bytes(ctypes.byref(_conv(shape)[0]), op, fa, fb)
 
 
 def mqconv_nvfp_forward(shape, xq: NvfpTensor, wq: NvfpTensor, y, ws=None, stream=None) -> None:
-    c = _conv32(shape)
+    c, _, _, ny = _conv(shape)
     p, n = _mq._ws(ws)
-    _mq._check(_lib().mqconv_nvfp_forward(ctypes.byref(c), xq.c_struct("xq"), wq.c_struct("wq"),
-                                          _floats(y, _mq._ny(shape), "y"), p, n, _mq._stream(stream)), "mqconv_nvfp_forward")
+    _mq._check(_lib().mqconv_nvfp_forward(ctypes.byref(c), xq.c_struct("xq"), wq.c_struct("wq"), _floats(y, ny, "y"), p, n,
+                                          _mq._stream(stream)), "mqconv_nvfp_forward")
 
 
 def mqconv_nvfp_backward_data(shape, dyq: NvfpTensor, wq: NvfpTensor, dx, ws=None, stream=None) -> None:
-    c = _conv32(shape)
+    c, nx, _, _ = _conv(shape)
     p, n = _mq._ws(ws)
     _mq._check(_lib().mqconv_nvfp_backward_data(ctypes.byref(c), dyq.c_struct("dyq"), wq.c_struct("wq"),
-                                                _floats(dx, _mq._nx(shape), "dx"), p, n, _mq._stream(stream)),
+                                                _floats(dx, nx, "dx"), p, n, _mq._stream(stream)),
                "mqconv_nvfp_backward_data")
 
 
 def mqconv_nvfp_backward_weight(shape, dyq: NvfpTensor, xq: NvfpTensor, dw, ws=None, stream=None) -> None:
-    c = _conv32(shape)
+    c, _, nw, _ = _conv(shape)
     p, n = _mq._ws(ws)
     _mq._check(_lib().mqconv_nvfp_backward_weight(ctypes.byref(c), dyq.c_struct("dyq"), xq.c_struct("xq"),
-                                                  _floats(dw, _mq._nw(shape), "dw"), p, n, _mq._stream(stream)),
+                                                  _floats(dw, nw, "dw"), p, n, _mq._stream(stream)),
                "mqconv_nvfp_backward_weight")
 
 
