@@ -894,14 +894,31 @@ __global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_weight_kernel(
   store_results<S>(reinterpret_cast<float*>(lds), rows, acc, me, scale, a.out + (a.slices == 1 ? 0 : z * a.slice), a.x.cols, j0);
 }
 
-// The slices' sums, added in order (fp64), times the tensors' scales.
-__global__ __launch_bounds__(256) void nvfp_join_kernel(const float* part, float* out, long long n, int slices, const float* ta,
-                                                        const float* tb) {
+// The slices' sums, added in order (fp64), times the tensors' scales: bound by
+// the slices' bytes, with four of a thread's loads under way.
+template <class V>
+__global__ __launch_bounds__(256) void nvfp_join_kernel(const V* part, V* out, long long n, int slices, const float* ta, const float* tb) {
+  constexpr int PER = sizeof(V) / 4;
   const Scale scale = scale_of(ta, tb);
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    double s = 0;
-    for (int z = 0; z < slices; z++) s += part[z * n + i];
-    out[i] = scale((float)s);
+    double s[PER] = {};
+    auto add = [&](const V& v) {
+#pragma unroll
+      for (int e = 0; e < PER; e++) s[e] += reinterpret_cast<const float*>(&v)[e];
+    };
+    int z = 0;
+    for (; z + 4 <= slices; z += 4) {
+      V v[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) v[k] = part[(z + k) * n + i];
+#pragma unroll
+      for (int k = 0; k < 4; k++) add(v[k]);
+    }
+    for (; z < slices; z++) add(part[z * n + i]);
+    V o;
+#pragma unroll
+    for (int e = 0; e < PER; e++) reinterpret_cast<float*>(&o)[e] = scale((float)s[e]);
+    out[i] = o;
   }
 }
 
@@ -1019,8 +1036,13 @@ size_t nvfp_gemm_workspace_bytes(const Conv& c, int op, int fa) {
 
 static hipError_t join(int slices, const float* part, float* out, long long n, const float* ta, const float* tb, hipStream_t st) {
   if (slices == 1) return hipSuccess;
-  hipLaunchKernelGGL(nvfp_join_kernel, dim3((unsigned)std::min<long long>(ceil_div(n, 256), 4096)), dim3(256), 0, st, part, out, n,
-                     slices, ta, tb);
+  const auto go = [&](auto kern, auto v, long long count) {
+    typedef decltype(v) V;
+    hipLaunchKernelGGL(kern, dim3((unsigned)std::min<long long>(ceil_div(count, 256), 4096)), dim3(256), 0, st,
+                       reinterpret_cast<const V*>(part), reinterpret_cast<V*>(out), count, slices, ta, tb);
+  };
+  if (n % 2 == 0 && (uintptr_t)out % 8 == 0) go(nvfp_join_kernel<float2>, float2{}, n / 2);
+  else go(nvfp_join_kernel<float>, 0.0f, n);
   return launch_check();
 }
 
