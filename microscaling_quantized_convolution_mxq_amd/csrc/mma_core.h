@@ -69,12 +69,13 @@ struct MmaShape {
   static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;  // a wave's 32 x 32 products
   static constexpr int STAGE = (BM + BN) * kPiece, LDS = ST * STAGE * NG;
   static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;     // loads of a wave and step
-  static_assert(LA >= 1 && LB >= 1 && TM >= 1 && TN >= 1 && NW % 2 == 0, "tile");
+  static_assert(LA >= 1 && LB >= 1 && TM >= 1 && TN >= 1, "tile");
   static_assert(NG == 1 || BM * BN * 4 * (NG - 1) <= LDS, "the groups' sums fit the rings");
 };
 
-// What a lane loads: load j of wave w covers rows 8 (w + NW j) ..+8, the lane
-// row + lane / 8; with an even number of waves its chunk is the same in all.
+// What a lane loads: load j of wave w covers the eight rows from 8 (w + NW j)
+// on, the lane row + lane / 8, and of that the chunk of eight-row block w + NW j;
+// with an even number of waves the chunk is the same in all loads.
 __device__ __forceinline__ int lane_chunk(int wave, int lane) { return (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7); }
 template <int NW>
 __device__ __forceinline__ int lane_row(int wave, int lane, int j) {
@@ -91,7 +92,7 @@ struct RowLoader {
 #pragma unroll
     for (int j = 0; j < L; j++) {
       const int r = row0 + lane_row<NW>(wave, lane, j);
-      off[j] = r < rows ? r * pitch + lane_chunk(wave, lane) * 16 : kBeyond;
+      off[j] = r < rows ? r * pitch + lane_chunk(wave + NW * j, lane) * 16 : kBeyond;
     }
   }
   __device__ void issue(int step, uint8_t* lds, int wave) const {

@@ -242,6 +242,7 @@ struct Taps {
 
 template <int L, int NW>
 struct GatherLoader {
+  static_assert(NW % 2 == 0, "one chunk a lane");
   __amdgpu_buffer_rsrc_t rsrc;
   int off[L], h[L], w[L];
   int H, W, pix, dir, nj, nc, i, j, cb;
@@ -298,6 +299,7 @@ struct TapLoader {
 // dY' [co][pixel][Np]: rows of `pieces` 16-byte pieces, which need not end with a step
 template <int L, int NW>
 struct EndLoader {
+  static_assert(NW % 2 == 0, "one chunk a lane");
   RowLoader<L, NW> rows;
   int pieces, chunk;
   __device__ void init(const void* p, long long bytes, int row0, int n, int count, int wave, int lane) {
@@ -323,6 +325,7 @@ struct Shift {
 };
 template <int L, int NW>
 struct ShiftLoader {
+  static_assert(NW % 2 == 0, "one chunk a lane");
   __amdgpu_buffer_rsrc_t rsrc;
   int off[L], h[L], w[L], chunk;
   const Shift* s;
