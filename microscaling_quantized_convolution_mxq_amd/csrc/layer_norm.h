@@ -21,13 +21,19 @@ struct LnArgs {
   float *dgamma, *dbeta;
   int R, C, parts;
   float eps;
+  double inv;                      // 1 / C
 };
 
 hipError_t launch_layer_norm_rows(const LnArgs& a, hipStream_t st);
 // dx or the rows' parameters, and `part` where it is given
 hipError_t launch_layer_norm_grad_rows(const LnArgs& a, hipStream_t st);
 hipError_t launch_layer_norm_columns(const LnArgs& a, hipStream_t st);
-// the MX forms' second pass: every value again from its row's parameters
+// the MX forms in one pass, for rows of C channels that one wave holds; the gradient's sets `parts` to the rows it leaves, at
+// most as many as it is given
+bool layer_norm_mx_one_pass(int C);
+hipError_t launch_layer_norm_mx(const LnArgs& a, int N, const MxOutView& out, hipStream_t st);
+hipError_t launch_layer_norm_grad_mx(LnArgs& a, int N, const MxOutView& out, hipStream_t st);
+// their second pass for other rows: every value again from its row's parameters
 hipError_t launch_layer_norm_mx_rows(const LnArgs& a, int N, const MxOutView& out, hipStream_t st);
 hipError_t launch_layer_norm_grad_mx_rows(const LnArgs& a, int N, const MxOutView& out, hipStream_t st);
 

@@ -20,7 +20,7 @@
 // every sum (they stay in the caches, being one row a workgroup).
 #include <algorithm>
 
-#include "layer_norm.h"
+#include "layer_norm_rows.h"
 #include "mx_rows.h"
 #include "norm.h"
 
@@ -30,106 +30,12 @@ namespace {
 
 constexpr int kWide = 8192;      // most channels of a row held in registers, forward
 constexpr int kWideGrad = 4096;  // and backward, which holds two tensors and the columns' sums
-constexpr int kParts = 1024;     // most rows of column sums
-
-typedef float quad_t[4];
-
-// Channel of quad q of thread t of the row's T threads.
-template <int T>
-__device__ __forceinline__ int chan(int q, int t) {
-  return (q * T + t) * 4;
-}
-
-// FULL: C is a multiple of four, so a quad is in the row or outside; loads then stand under no condition.
-template <int T, int Q, bool FULL>
-__device__ __forceinline__ void load_row(const float* row, int C, int t, quad_t (&v)[Q]) {
-#pragma unroll
-  for (int q = 0; q < Q; q++) {
-    const int c = chan<T>(q, t);
-    if (FULL) load_run<4, true>(row + (c < C ? c : 0), 4, v[q]);
-    else load_run<4, false>(row + c, C - c, v[q]);
-  }
-}
-template <int T, int Q, bool FULL>
-__device__ __forceinline__ void store_row(float* row, int C, int t, const quad_t (&v)[Q]) {
-#pragma unroll
-  for (int q = 0; q < Q; q++) {
-    const int c = chan<T>(q, t);
-    store_run<4, FULL>(row + c, C - c, v[q]);
-  }
-}
-// whether value i of quad q exists
-template <int T, bool FULL>
-__device__ __forceinline__ bool has(int q, int i, int t, int C) {
-  return FULL ? chan<T>(q, t) < C : chan<T>(q, t) + i < C;
-}
-
-template <int T, int Q, bool FULL>
-__device__ __forceinline__ void load_param(const float* p, int C, int t, float other, quad_t (&v)[Q]) {
-  if (p) {
-    load_row<T, Q, FULL>(p, C, t, v);
-  } else {
-#pragma unroll
-    for (int q = 0; q < Q; q++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) v[q][i] = other;
-  }
-}
-
-template <int CTRL>
-__device__ __forceinline__ double add_dpp(double a) {
-  const long long b = __double_as_longlong(a);
-  const int lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, false);
-  const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xF, 0xF, false);
-  return a + __longlong_as_double(((long long)hi << 32) | (unsigned)lo);
-}
-__device__ __forceinline__ double lane_of(double a, int lane) {
-  const long long b = __double_as_longlong(a);
-  return __longlong_as_double(((long long)__builtin_amdgcn_readlane((int)(b >> 32), lane) << 32) |
-                              (unsigned)__builtin_amdgcn_readlane((int)b, lane));
-}
-// Sum over aligned groups of T lanes, on every lane of the group: at each step
-// a lane adds the sum of the other half of its group (DPP within 16 lanes).
-template <int T>
-__device__ __forceinline__ double group_sum(double a) {
-  if constexpr (T >= 2) a = add_dpp<0xB1>(a);   // lane ^ 1
-  if constexpr (T >= 4) a = add_dpp<0x4E>(a);   // lane ^ 2
-  if constexpr (T >= 8) a = add_dpp<0x141>(a);  // 7 - lane within 8
-  if constexpr (T >= 16) a = add_dpp<0x140>(a); // 15 - lane within 16
-  if constexpr (T >= 32) a += __shfl_xor(a, 16);
-  if constexpr (T >= 64) a = lane_of(a, 0) + lane_of(a, 32);
-  return a;
-}
-
-// Sums of K values over a row's T threads, on all of them. Where these are
-// several waves (a whole workgroup) each leaves its part in LDS; `phase`
-// alternates between calls, so one barrier a call is enough: a wave that
-// writes a phase's slots again has passed the barrier of the other phase, which
-// every wave reaches only after its reads of this one.
-template <int T, int K>
-__device__ __forceinline__ void row_sums(double (&s)[K], int phase) {
-#pragma unroll
-  for (int k = 0; k < K; k++) s[k] = group_sum<(T < 64 ? T : 64)>(s[k]);
-  if constexpr (T > 64) {
-    constexpr int W = T / 64;
-    __shared__ double red[2][W][K];
-    const int w = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0)
-#pragma unroll
-      for (int k = 0; k < K; k++) red[phase][w][k] = s[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; k++) {
-      s[k] = red[phase][0][k];
-#pragma unroll
-      for (int i = 1; i < W; i++) s[k] += red[phase][i][k];
-    }
-  }
-}
-
-__device__ __forceinline__ float rstd_of(double sq, int C, float eps) {
-  return (float)(1.0 / sqrt(sq / C + (double)eps));
-}
+// Most workgroups of the gradient's pass, each of which leaves a row of column
+// sums: two a compute unit, one for rows of more than 1024 channels, whose
+// workgroups have more threads and more loads under way. Each more costs its row
+// (512 x 16 x 4096: 77.8 us with 256, 84.0 with 512, 95.3 with 1024; 20 x 20
+// x 128 x 256: 47.1, 36.5 and 39.4).
+constexpr int kParts = 512, kPartsWide = 256;
 
 template <int T>
 constexpr int threads_of() {
@@ -170,7 +76,7 @@ __global__ __launch_bounds__(threads_of<T>()) void ln_kernel(const LnArgs a) {
       if (ADD) load_row<T, Q, FULL>(a.add + (long long)rn * a.C, a.C, t, more);
     }
     row_sums<T, 1>(s, 0);
-    const double mean = s[0] / a.C;
+    const double mean = s[0] * a.inv;
     s[0] = 0;
 #pragma unroll
     for (int q = 0; q < Q; q++)
@@ -180,7 +86,7 @@ __global__ __launch_bounds__(threads_of<T>()) void ln_kernel(const LnArgs a) {
         s[0] = __builtin_fma(d, d, s[0]);
       }
     row_sums<T, 1>(s, 1);
-    const float m = (float)mean, rs = rstd_of(s[0], a.C, a.eps);
+    const float m = (float)mean, rs = rstd_of(s[0], a);
     if (t == 0) {
       if (a.mean) a.mean[r] = m;
       if (a.rstd) a.rstd[r] = rs;
@@ -215,7 +121,7 @@ __global__ __launch_bounds__(1024) void ln_long_kernel(const LnArgs a) {
     }
     // (a thread reads back what it wrote itself; without a sum the addends are added again)
     row_sums<1024, 1>(s, 0);
-    const double mean = s[0] / a.C;
+    const double mean = s[0] * a.inv;
     const float* from = ADD && a.sum ? a.sum + at : x;
     const float* more = ADD && !a.sum ? a.add + at : nullptr;
     s[0] = 0;
@@ -224,7 +130,7 @@ __global__ __launch_bounds__(1024) void ln_long_kernel(const LnArgs a) {
       s[0] = __builtin_fma(d, d, s[0]);
     }
     row_sums<1024, 1>(s, 1);
-    const float m = (float)mean, rs = rstd_of(s[0], a.C, a.eps);
+    const float m = (float)mean, rs = rstd_of(s[0], a);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[r] = m;
       if (a.rstd) a.rstd[r] = rs;
@@ -281,7 +187,7 @@ __global__ __launch_bounds__(threads_of<T>()) void ln_grad_kernel(const LnArgs a
       }
     if (r + step < a.R) load(r + step);
     row_sums<T, 2>(s, phase);
-    const float k1 = (float)(s[0] / a.C), k2 = (float)(s[1] / a.C);
+    const float k1 = (float)(s[0] * a.inv), k2 = (float)(s[1] * a.inv);
     if (a.out) {
 #pragma unroll
       for (int q = 0; q < Q; q++)
@@ -294,44 +200,12 @@ __global__ __launch_bounds__(threads_of<T>()) void ln_grad_kernel(const LnArgs a
     }
   }
   if (!a.part) return;
-  // the workgroup's row of column sums: groups of a wave by lanes, waves in turn through LDS
-  if constexpr (T < 64) {
-#pragma unroll
-    for (int off = T; off < 64; off *= 2)
-#pragma unroll
-      for (int q = 0; q < Q; q++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          sb[q][i] += __shfl_xor(sb[q][i], off);
-          sg[q][i] += __shfl_xor(sg[q][i], off);
-        }
-  }
   if constexpr (T <= 64) {
-    __shared__ double2 cols[B / 64 - 1][T * Q * 4];
-    const int w = threadIdx.x >> 6;
-    if (w > 0 && (threadIdx.x & 63) < T)
-#pragma unroll
-      for (int q = 0; q < Q; q++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) cols[w - 1][chan<T>(q, t) + i] = make_double2(sb[q][i], sg[q][i]);
-    __syncthreads();
-    if (threadIdx.x >= T) return;
-#pragma unroll
-    for (int q = 0; q < Q; q++)
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        for (int k = 0; k < B / 64 - 1; k++) {
-          const double2 o = cols[k][chan<T>(q, t) + i];
-          sb[q][i] += o.x;
-          sg[q][i] += o.y;
-        }
+    __shared__ double2 cols[(B / 64 - 1) * T * Q * 4];
+    leave_columns<T, Q, B>(a, cols, t, sb, sg);
+  } else {
+    leave_columns<T, Q, B>(a, nullptr, t, sb, sg);
   }
-  float2* const to = a.part + (long long)blockIdx.x * a.C;
-#pragma unroll
-  for (int q = 0; q < Q; q++)
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (chan<T>(q, t) + i < a.C) to[chan<T>(q, t) + i] = make_float2((float)sb[q][i], (float)sg[q][i]);
 }
 
 template <bool ADD>
@@ -346,7 +220,7 @@ __global__ __launch_bounds__(1024) void ln_grad_long_kernel(const LnArgs a) {
       s[1] += (double)g * (double)ln_hat(a.x[at + c], mean, rs);
     }
     row_sums<1024, 2>(s, phase);
-    const float k1 = (float)(s[0] / a.C), k2 = (float)(s[1] / a.C);
+    const float k1 = (float)(s[0] * a.inv), k2 = (float)(s[1] * a.inv);
     if (a.out) {
       for (int c = threadIdx.x; c < a.C; c += 1024) {
         const float g = a.gamma ? a.dy[at + c] * a.gamma[c] : a.dy[at + c];
@@ -441,7 +315,7 @@ hipError_t launch_backward_rows(const LnArgs& a, hipStream_t st) {
 // of column sums.
 static int grad_parts(int R, int C) {
   if (C > kWideGrad) return std::min(R, 64);
-  return std::min(ceil_div(R, rows_of_group(C)), kParts);
+  return std::min(ceil_div(R, rows_of_group(C)), C > 1024 ? kPartsWide : kParts);
 }
 
 size_t layer_norm_workspace_bytes(const LnShape& s, int op) {
@@ -490,8 +364,9 @@ hipError_t launch_layer_norm(const LnShape& s, const float* x, const float* resi
   LnArgs a{};
   a.x = x; a.add = residual; a.gamma = gamma; a.beta = beta;
   a.sum = sum; a.out = y; a.mean = mean; a.rstd = rstd;
-  a.R = s.P * s.N; a.C = s.C; a.eps = s.eps;
+  a.R = s.P * s.N; a.C = s.C; a.eps = s.eps; a.inv = 1.0 / s.C;
   if (!yq.codes) return launch_layer_norm_rows(a, st);
+  if (layer_norm_mx_one_pass(s.C)) return launch_layer_norm_mx(a, s.N, yq, st);
   // the second pass reads the statistics that the first one leaves
   float* const kept = static_cast<float*>(ws);
   if (!a.mean) a.mean = kept;
@@ -509,12 +384,18 @@ hipError_t launch_layer_norm_backward(const LnShape& s, const float* dy, const f
   LnArgs a{};
   a.x = x; a.dy = dy; a.add = dskip; a.gamma = gamma;
   a.mean_in = mean; a.rstd_in = rstd; a.out = dx; a.dgamma = dgamma; a.dbeta = dbeta;
-  a.R = s.P * s.N; a.C = s.C; a.eps = s.eps;
+  a.R = s.P * s.N; a.C = s.C; a.eps = s.eps; a.inv = 1.0 / s.C;
   a.parts = grad_parts(a.R, a.C);
   a.row = static_cast<LnRow*>(ws);
   if (dgamma || dbeta)
     a.part = reinterpret_cast<float2*>(static_cast<char*>(ws) + ((size_t)a.R * 8 + 15) / 16 * 16);
-  hipError_t e = launch_layer_norm_grad_rows(a, st);
+  hipError_t e;
+  if (dxq.codes && layer_norm_mx_one_pass(s.C)) {
+    e = launch_layer_norm_grad_mx(a, s.N, dxq, st);
+    if (e == hipSuccess && a.part) e = launch_layer_norm_columns(a, st);
+    return e;
+  }
+  e = launch_layer_norm_grad_rows(a, st);
   if (e == hipSuccess && dxq.codes) e = launch_layer_norm_grad_mx_rows(a, s.N, dxq, st);
   if (e == hipSuccess && a.part) e = launch_layer_norm_columns(a, st);
   return e;

@@ -159,7 +159,16 @@ def test_gradient_against_differences(shape):
     assert abs((f(1e-4) - f(-1e-4)) / 2e-4 - sum(t.sum() for t in terms)) <= 1e-4 * sum(np.abs(t).sum() for t in terms)
 
 
-MX_SHAPES = [(1, 1, 1, 1), (1, 1, 300, 64), (5, 3, 33, 45), (19, 23, 5, 90), (20, 20, 32, 64), (7, 6, 40, 320), (3, 2, 2, 31),
+def _columns_close(shape, dy, x, mean, rstd, dgamma, dbeta):
+    """dgamma and dbeta against 64-bit sums: 3 e sum |dy xh| + e |dgamma| and e sum |dy| + e |dbeta|, with 2 e of every term's xh."""
+    dy, x = host(dy).astype(np.float64).reshape(-1, shape[3]), host(x).astype(np.float64).reshape(-1, shape[3])
+    xh = (x - host(mean).astype(np.float64).reshape(-1, 1)) * host(rstd).astype(np.float64).reshape(-1, 1)
+    for got, terms, k in ((dgamma, dy * xh, 3), (dbeta, dy, 1)):
+        total = terms.sum(axis=0)
+        assert (np.abs(host(got) - total) <= k * E * np.abs(terms).sum(axis=0) + E * np.abs(total) + TINY).all()
+
+
+MX_SHAPES = [(6, 7, 3, 36), (3, 5, 20, 128), (4, 3, 70, 132), (9, 2, 64, 256), (50, 41, 1, 100), (1, 1, 1, 1), (1, 1, 300, 64), (5, 3, 33, 45), (19, 23, 5, 90), (20, 20, 32, 64), (7, 6, 40, 320), (3, 2, 2, 31),
              (2, 3, 37, 1000), (40, 24, 16, 64), (2, 1, 35, 2048), (1, 2, 33, 4100), (1, 3, 3, 9008), (1, 1, 2, 20000)]
 
 
@@ -186,7 +195,8 @@ def test_mx_results_are_the_quantized_fp32_results(shape, fmt):
         s = total if extra else x
         dx, dg, db = _backward(shape, dy, s, gamma, mean, rstd, dskip=skip if extra else None)
         t, dg2, db2 = _backward(shape, dy, s, gamma, mean, rstd, mx=(fmt, bp), dskip=skip if extra else None, fill=0)
-        assert torch.equal(dg, dg2) and torch.equal(db, db2)
+        # (the two forms share the rows between workgroups in their own ways: both within the bound of 64-bit sums)
+        _columns_close(shape, dy, s, mean, rstd, dg2, db2)
         ref = mq.MxTensor.empty(mq.ROLE_GRAD, fmt, bp, shape)
         mq.mqconv_quantize(dx, ref)
         _same_codes(t, ref, f"dx {shape}")
@@ -361,7 +371,7 @@ def test_repeats_bit_for_bit_and_injected_failures():
             _same_codes(got[0], ref[0], f"workspace of {fill}")
             assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
     try:
-        for c, ref, launches in zip(calls, refs, (2, 4)):
+        for c, ref, launches in zip(calls, refs, (1, 3)):
             for k in range(1, launches + 2):
                 mq.mqconv_inject_launch_failure(k)
                 if k <= launches:
