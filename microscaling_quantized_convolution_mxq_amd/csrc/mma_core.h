@@ -274,9 +274,8 @@ __device__ __forceinline__ void mma_loop(uint8_t* ring, LA& la, LB& lb, int step
   }
 }
 
-// The same for one wave a SIMD with large tiles of its own (128 x 64 and more):
-// LDS hands 128 bytes a clock to a compute unit, which four waves of 64 x 64
-// need for their operands alone, and waves of 128 x 64 need three quarters of.
+// The same for one wave a SIMD with large tiles of its own (128 x 64 and more),
+// which read each operand fewer times.
 // With no second wave to fill in, the operands of the next 16 values of k are
 // read while the present ones are multiplied, over the barrier too: it stands
 // before the last products of a step, and what they read is in registers. n is

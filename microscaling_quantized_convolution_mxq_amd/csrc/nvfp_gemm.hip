@@ -147,13 +147,22 @@ struct Task {
   FastDiv dPp;
 };
 
+constexpr int kPieces = 2;  // of a thread, their loads together (8192 x 4096 and 4096 x 4096, 127 MB: 31.8 us, 37.1 with one)
 template <int F>
 __device__ __forceinline__ void make_rows(const Task& a, int group) {
-  const unsigned i = group * 256u + threadIdx.x;
-  if (i >= (unsigned)a.n) return;
-  const unsigned row = fdiv(i, a.pieces), ch = i - row * a.pieces.d;
-  const unsigned q = fdiv(row, a.dB), b = row - q * a.dB.d, aa = fdiv(q, a.dP), p = q - aa * a.dP.d;
-  *reinterpret_cast<bits8*>(a.out + (long long)i * 8) = values8<F>(a.t, a.half, row, (int)(aa * a.dB.d + b), (int)p, (int)ch);
+  bits8 v[kPieces];
+  long long to[kPieces];
+#pragma unroll
+  for (int u = 0; u < kPieces; u++) {
+    const unsigned i = (unsigned)(group * kPieces + u) * 256u + threadIdx.x, j = min(i, (unsigned)a.n - 1);
+    const unsigned row = fdiv(j, a.pieces), ch = j - row * a.pieces.d;
+    const unsigned q = fdiv(row, a.dB), b = row - q * a.dB.d, aa = fdiv(q, a.dP), p = q - aa * a.dP.d;
+    to[u] = i < (unsigned)a.n ? (long long)i * 8 : -1;
+    v[u] = values8<F>(a.t, a.half, row, (int)(aa * a.dB.d + b), (int)p, (int)ch);
+  }
+#pragma unroll
+  for (int u = 0; u < kPieces; u++)
+    if (to[u] >= 0) *reinterpret_cast<bits8*>(a.out + to[u]) = v[u];
 }
 
 constexpr int kAcross = 66;  // a column of the tile (eight threads of one slot write 8 channels each, 264 dwords apart: eight banks)
@@ -204,7 +213,7 @@ Task rows_task(const Codes& t, __bf16* out) {
   Task a{};
   a.t = t; a.out = out;
   a.n = (int)((long long)t.A * t.P * t.B * (cp / 8));
-  a.groups = ceil_div(a.n, 256);
+  a.groups = ceil_div(a.n, 256 * kPieces);
   a.pieces = make_fastdiv(cp / 8); a.dP = make_fastdiv(t.P); a.dB = make_fastdiv(t.B);
   return a;
 }
@@ -505,8 +514,15 @@ __global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_conv_kernel(co
 // block scales in one dword, and makes 8 values with 16 instructions while the
 // other waves multiply. Each wave has all columns, so no value is made twice in
 // a workgroup. The other operand, small, comes as bf16.
-// c5-sized input gradient (160 x 160 x 32 x 128 from 80 x 80 x 32 x 256, stride
-// 2): this kernel against the one above with its pass before.
+// The input gradient of 3 x 3, stride 2 (160 x 160 x 32 x 128 from 80 x 80 x 32 x
+// 256, E2M1): 160 us with the weights' pass, 750 TFLOP/s, 288 by the kernel above
+// with its pass over both. Its products alone are 84 us at the rate of a large
+// matrix product, loads and stores without products 89: at two waves a SIMD
+// (registers for the sums) they overlap by half. Fewer rows or stages a
+// workgroup, and so more of these, change it by no more than 3 us.
+// 3 x 3 on 80 x 80 x 16 x 64 to 64 channels: 21 us with the weights' pass (25.6 by
+// the kernel above), of which 10 remain with one step of the nine; with tiles of
+// 128 rows the same.
 template <int F>
 struct CodeRows {
   static constexpr int RUN = run_bytes_of(F), SLOTS = 2 * RUN / 16;  // 16-byte slots of a row: 2 (4 bit) or 4 (8 bit)
@@ -871,8 +887,13 @@ struct WeightArgs {
   long long slice;
 };
 
+// dW: the sums run over output pixels and samples, so both operands come with
+// those contiguous (X' moved by a tap's pixels, as whole pieces of 8 samples).
+// Bound by the loop: 62 us for 60 GFLOP (975 TFLOP/s) at 3 x 3 x 256 to 256
+// channels on 20 x 20 x 128, of it about 7 for the slices' 33 MB; the operands'
+// pass before is 17 us (65 MB) and the join behind 8.
 template <class S>
-__global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_weight_kernel(const WeightArgs a) {
+__global__ __launch_bounds__(S::THREADS, 2) void nvfp_weight_kernel(const WeightArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const MmaWave<S> me;
   const int lane = me.lane, wave = me.wave;
@@ -886,8 +907,7 @@ __global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_weight_kernel(
   ShiftLoader<S::LB, S::NW> lb;
   la.init(a.dy, a.dy_bytes, i0, a.rows, a.x.pieces, wave, lane);
   lb.init(a.x, j0, wave, lane);
-  if constexpr (wide_of<S>()) mma_loop_wide<Bf16, S>(lds, la, lb, s0, s1 - s0, me, acc);
-  else mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, s1 - s0, me, acc);
+  mma_loop<Bf16, S>(lds, la, lb, s0, s1 - s0, s1 - s0, me, acc);
   stage_ready<0>();
   int* const rows = reinterpret_cast<int*>(lds + strips_of<S>());
   for (int r = threadIdx.x; r < S::BM; r += S::THREADS) rows[r] = i0 + r < a.rows ? i0 + r : -1;
@@ -927,25 +947,29 @@ __global__ __launch_bounds__(256) void nvfp_join_kernel(const V* part, V* out, l
 
 // ---- plans --------------------------------------------------------------------------------------
 typedef MmaShape<256, 256, 2, 2, 2> Big;
-typedef MmaShape<256, 128, 2, 2, 3> Wide;
 typedef MmaShape<128, 128, 2, 2, 2> Mid;
 typedef MmaShape<256, 64, 4, 1, 2> Tall;
 typedef MmaShape<64, 64, 2, 2, 3> Small;
-enum { kBig, kWide, kMid, kTall, kSmall };
+enum { kBig, kMid, kTall, kSmall };
 
-// Tiles by the output's extents, and slices along k where these tiles do not fill the chip.
+// Tiles by the output's extents, and slices along k where these tiles do not
+// fill the chip. Large ones read less and multiply at a better rate, as long as
+// there are tiles for most compute units:
+//   8192 x 4096 x 4096: 240 us (1145 TFLOP/s) in tiles of 256 x 256, 286 of 128 x 128;
+//   dW of 3 x 3 x 256 from 20 x 20 x 128 x 256 (256 x 2304, sums of 51200): 62 us
+//   in tiles of 128 x 128 by 14 slices, 129 of 64 x 64; 256 x 128 the same as 128 x 128;
+//   3 x 3 on 80 x 80 x 16 x 64 to 64 channels: 19.2 us in tiles of 256 x 64, 22.4 of 64 x 64.
 struct Plan {
   int shape, slices;
 };
-const int kBM[5] = {256, 256, 128, 256, 64}, kBN[5] = {256, 128, 128, 64, 64};
+const int kBM[4] = {256, 128, 256, 64}, kBN[4] = {256, 128, 64, 64};
 Plan plan_of(int op, long long M, long long N, long long steps) {
   auto tiles = [&](int s) { return (long long)ceil_div(M, kBM[s]) * ceil_div(N, kBN[s]); };
   Plan p{kSmall, 1};
   if (op < 2 && N > 128 && M > 128 && tiles(kBig) >= 200) p.shape = kBig;
-  else if (M > 128 && N > 64 && steps >= 32 && tiles(kWide) * (steps / 16) >= 200) p.shape = kWide;
   else if (N <= 64 && M >= 256 && tiles(kTall) >= 200) p.shape = kTall;
   else if (N > 64 && M > 64 && tiles(kMid) * std::max(1LL, steps / 8) >= 256) p.shape = kMid;
-  const long long t = tiles(p.shape), want = (p.shape == kWide ? 256 : 512) / std::max(1LL, t);
+  const long long want = 512 / std::max(1LL, tiles(p.shape));
   // slices of eight steps at least, and no more sums than operands' bytes by far
   if (want >= 2) p.slices = (int)std::max(1LL, std::min({want, steps / 8, 64LL}));
   return p;
@@ -957,7 +981,6 @@ void with_shape(int s, F&& f) {
     case kBig:
       if constexpr (OP < 2) f(Big{});  // (the weight gradient's loader leaves no registers for it)
       break;
-    case kWide: f(Wide{}); break;
     case kMid: f(Mid{}); break;
     case kTall: f(Tall{}); break;
     default: f(Small{}); break;
@@ -966,7 +989,8 @@ void with_shape(int s, F&& f) {
 
 // The kernel that takes codes: 4- and 8-bit elements whose rows of scales are
 // whole dwords, at most two tiles of columns (a value is made for each), and
-// rows enough for its tall tiles. 0 slices: the other kernel.
+// rows enough for its tall tiles (figures of both kernels are at this one). 0
+// slices: the other kernel.
 int code_slices(int op, int fmt, long long M, long long cols, int channels, long long steps) {
   if (op > 1 || (fmt > 1 && fmt != 4) || cols > 256 || ceil_div(channels, 8) % 4 != 0 || M < 4096) return 0;
   const long long t = (long long)ceil_div(M, 256) * ceil_div(cols, cols <= 64 ? 64 : 128);
