@@ -389,24 +389,15 @@ __global__ __launch_bounds__(256) void join_kernel(const Group g) {
 // ---- plans --------------------------------------------------------------------------------------
 // A matrix's tiles and slices are chosen by its own extents alone, so its
 // result does not depend on what else a call holds.
-// Small matrices: A's products have few tiles and long sums, so each of their
-// tiles is a wave's, four times over along k (a call of 27 layers up to 256 x
-// 1152: A 9.7 us, against 13.6 in tiles of 64 x 64 by two groups of four waves;
-// A^2 7.4 against 8.6). B X has tiles enough: 10.5 us in tiles of 64 x 64, 11.2
-// in smaller ones, of which 4 are writing X twice over.
-template <int KIND>
-struct SmallOf {
-  typedef MmaShape<64, 64, 2, 2, 3> type;
-};
-template <>
-struct SmallOf<kGram> {
-  typedef MmaShape<32, 32, 1, 1, 3, 4> type;
-};
-template <>
-struct SmallOf<kPoly> {
-  typedef MmaShape<32, 32, 1, 1, 2, 4> type;
-};
 typedef MmaShape<256, 128, 2, 2, 3> Wide;
+typedef MmaShape<64, 64, 2, 2, 3> Mid;
+// Of small matrices A and A^2 have few tiles and long sums, so each tile is a
+// wave's, four times over along k.
+template <int KIND>
+struct NarrowOf {
+  typedef MmaShape<32, 32, 1, 1, KIND == kGram ? 3 : 2, 4> type;
+};
+enum { kWide, kMid, kNarrow };
 
 int tiles(int n, int b) { return (n + b - 1) / b; }
 
@@ -420,41 +411,60 @@ int tiles_of(const Mat& m) {
   return n;
 }
 
+// Measured, us a product with its join, at n wide tiles times steps of 32 and t mid tiles:
+//             A                        A^2                      B X
+//             n     t   wide mid  nar  n     t   wide mid  nar  n     wide  mid
+// 256 x 1152  108   10       16.2  9.6     10       8.2  7.0
+// 512 x 2048  384   36  25.6 24.4 12.9  96    36  52.0 11.3  9.0  512   33.1  13.4
+// 768 x 768   288   78       12.2 14.4  288   78       15.1 12.5
+// 1024 x 1024 640  136  26.4 14.9 23.6  640  136  27.9 15.9 19.7  1024  27.6  16.6
+// 1536 x 1536 2016 300  32.2      52.0  2016 300  34.8      42.6  3456  39.6  36.4
+// 2048 x 4096 9216 528  69.1     184.0  4608 528  48.6      89.7  16384 102.1 147.9
+// Wide tiles pay with steps enough over all of them: few leave the chip empty,
+// or spend their gain on joining slices; mid tiles with one for every third
+// compute unit and more.
 struct Plan {
-  bool wide;
-  int tiles, slices;
+  int size, tiles, slices;
 };
 template <int KIND>
 Plan plan_of(const Mat& m) {
   const int steps = (KIND == kGram ? m.np : m.mp) / 32;
-  Plan p{};
-  p.wide = m.mp >= (KIND == kPoly ? 1536 : 512);
-  if (p.wide) {
+  Plan p{kWide, tiles_of<KIND, Wide>(m), 1};
+  if ((long long)p.tiles * steps >= (KIND <= kPoly ? 1000 : 4096)) {
     // one workgroup a compute unit; slices of 16 steps at least
-    p.tiles = tiles_of<KIND, Wide>(m);
     p.slices = std::max(1, std::min({256 / p.tiles, steps / 16, 32}));
-  } else {
-    p.tiles = tiles_of<KIND, typename SmallOf<KIND>::type>(m);
-    p.slices = std::max(1, std::min({256 / p.tiles, steps / 48, 32}));
+    return p;
+  }
+  p = Plan{kMid, tiles_of<KIND, Mid>(m), 1};
+  if (KIND <= kPoly && p.tiles < 100) {
+    p = Plan{kNarrow, tiles_of<KIND, typename NarrowOf<KIND>::type>(m), 1};
+    if (KIND == kGram) p.slices = std::max(1, std::min({256 / p.tiles, steps / 48, 32}));
   }
   return p;
 }
+template <int KIND, class F>
+auto with_size(int size, F&& f) {
+  if (size == kWide) return f(Wide{});
+  if constexpr (KIND <= kPoly)
+    if (size == kNarrow) return f(typename NarrowOf<KIND>::type{});
+  return f(Mid{});
+}
 template <int KIND>
 long long part_of(const Mat& m) {  // float4 of its slices
-  typedef typename SmallOf<KIND>::type S;
   const Plan p = plan_of<KIND>(m);
-  return p.slices == 1 ? 0 : (long long)p.tiles * p.slices * (p.wide ? Wide::BM * Wide::BN : S::BM * S::BN) / 4;
+  const int tile = with_size<KIND>(p.size, [](auto s) { return decltype(s)::BM * decltype(s)::BN; });
+  return p.slices == 1 ? 0 : (long long)p.tiles * p.slices * tile / 4;
 }
 long long part_size(const Mat& m) { return std::max({part_of<kGram>(m), part_of<kPoly>(m), part_of<kApply>(m)}); }
 
 template <int KIND, class S>
-hipError_t launch_class(Group& g, bool wide, hipStream_t st) {
+hipError_t launch_size(Group& g, int size, hipStream_t st) {
   int total = 0, join = 0, joins[kUpdateGroup];
   for (int i = 0; i < g.count; i++) {
     const Plan p = plan_of<KIND>(g.m[i]);
-    const bool in = p.wide == wide;
+    const bool in = p.size == size;
     g.start[i] = total;
-    g.tiles[i] = std::max(1, p.tiles);
+    g.tiles[i] = p.tiles;
     g.slices[i] = p.slices;
     total += in ? p.tiles * p.slices : 0;
     joins[i] = join;
@@ -464,18 +474,23 @@ hipError_t launch_class(Group& g, bool wide, hipStream_t st) {
   g.start[g.count] = total;
   hipLaunchKernelGGL((newton_kernel<KIND, S>), dim3((unsigned)total), dim3(S::THREADS), 0, st, g);
   const hipError_t e = launch_check();
-  if (e != hipSuccess || join == 0) return e;
-  std::copy(joins, joins + g.count, g.start);
-  g.start[g.count] = join;
-  hipLaunchKernelGGL((join_kernel<KIND, S>), dim3((unsigned)join), dim3(256), 0, st, g);
-  return launch_check();
+  if constexpr (S::BM == Wide::BM || (KIND == kGram && S::BM != Mid::BM)) {  // (the others take no slices)
+    if (e != hipSuccess || join == 0) return e;
+    std::copy(joins, joins + g.count, g.start);
+    g.start[g.count] = join;
+    hipLaunchKernelGGL((join_kernel<KIND, S>), dim3((unsigned)join), dim3(256), 0, st, g);
+    return launch_check();
+  }
+  return e;
 }
 
 template <int KIND>
 hipError_t launch_product(Group& g, hipStream_t st) {
-  const hipError_t e = launch_class<KIND, Wide>(g, true, st);
-  if (e != hipSuccess) return e;
-  return launch_class<KIND, typename SmallOf<KIND>::type>(g, false, st);
+  for (int size = kWide; size <= (KIND <= kPoly ? kNarrow : kMid); size++) {
+    const hipError_t e = with_size<KIND>(size, [&](auto s) { return launch_size<KIND, decltype(s)>(g, size, st); });
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 Mat make_mat(int rows, int cols) {

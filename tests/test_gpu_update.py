@@ -119,7 +119,7 @@ def test_five_steps_of_every_shape_in_one_call(kind):
         np.testing.assert_array_equal(_run(nt, [g], fill=0)[0], x)
 
 
-@pytest.mark.parametrize("shape", [(1024, 1024), (1100, 2050), (1536, 640), (48, 7000), (6400, 300)], ids=str)
+@pytest.mark.parametrize("shape", [(1024, 1024), (1100, 2050), (1536, 640), (1550, 2600), (1800, 1800), (48, 7000), (6400, 300)], ids=str)
 def test_large_matrices(shape):
     nt = mq.mq_newton()
     args = (5, nt.a, nt.b, nt.c, nt.eps)
