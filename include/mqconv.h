@@ -340,8 +340,8 @@ int mqconv_naive_backward_weight(const mq_conv* cv, const float* dy, const float
  * tensor_scale: one fp32 on the device. ws: mqconv_nvfp_workspace_bytes()
  * bytes of device scratch (partial maxima).
  * The GEMMs of the path take E8M0 block scales (what gfx950's block-scaled
- * MFMA applies per 32 K-elements); this format is quantized and measured
- * (error against the E8M0 format at equal element bits), not multiplied.
+ * MFMA applies per 32 K-elements); the products of this format are in
+ * mqconv_train.h.
  * --------------------------------------------------------------------------- */
 size_t mqconv_nvfp_scales_bytes(mq_role role, int32_t d0, int32_t d1, int32_t d2, int32_t d3);
 size_t mqconv_nvfp_workspace_bytes(void);
