@@ -385,3 +385,23 @@ def test_repeats_bit_for_bit_and_injected_failures():
                     assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
     finally:
         mq.mqconv_inject_launch_failure(0)
+
+
+@pytest.mark.parametrize("shape", [(6, 7, 3, 36), (3, 2, 33, 64), (9, 2, 64, 256), (4, 3, 5, 320)], ids=str)
+@pytest.mark.parametrize("bp", [1, 32])
+def test_mx_results_of_non_finite_rows(shape, bp):
+    """A row with a NaN or an infinity is NaN in the fp32 form; the MX form is what the quantizer makes of that."""
+    x, dy, skip, gamma, beta = _inputs(shape, 71)
+    x[0, 0, 0, -1], x[-1, -1, -1, 0], x[1, 1, 1, 5] = np.nan, np.inf, -np.inf
+    x, dy, gamma, beta = dev(x), dev(dy), dev(gamma), dev(beta)
+    y, mean, rstd = _forward(shape, x, gamma, beta)
+    for fmt in (0, 1, 2, 4):
+        t, _, _ = _forward(shape, x, gamma, beta, mx=(fmt, bp))
+        ref = mq.MxTensor.empty(mq.ROLE_ACT, fmt, bp, shape)
+        mq.mqconv_quantize(y, ref)
+        _same_codes(t, ref, f"y {shape}")
+        dx, _, _ = _backward(shape, dy, x, gamma, mean, rstd)
+        t, _, _ = _backward(shape, dy, x, gamma, mean, rstd, mx=(fmt, bp), sums=False)
+        ref = mq.MxTensor.empty(mq.ROLE_GRAD, fmt, bp, shape)
+        mq.mqconv_quantize(dx, ref)
+        _same_codes(t, ref, f"dx {shape}")

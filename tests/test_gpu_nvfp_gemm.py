@@ -283,3 +283,17 @@ def test_injected_failures_then_recovery():
         finally:
             mq.mqconv_inject_launch_failure(0)
         assert failed >= 2
+
+
+@pytest.mark.parametrize("fmts", [(4, 4), (0, 0), (1, 1), (2, 2), (3, 3), (0, 4), (2, 1)], ids=str)
+def test_few_rows_of_many_channels(fmts):
+    """Channels shared by 1, 2 and 4 waves, and more than those hold at once; single rows of two formats."""
+    for n, cin, cout in ((1, 2048, 9), (1, 2049, 70), (2, 4100, 33), (3, 7000, 8), (8, 9000, 50), (5, 20000, 5), (1, 40009, 3)):
+        if n > 1 and fmts[0] != fmts[1] and cin > 5000:
+            continue
+        s = (n, cin, 1, 1, cout, 1, 1, 1, 1, 0, 0)
+        x, w, _ = _inputs(s, 90 + n)
+        X, W = _quantized(x, mq.ROLE_ACT, fmts[0]), _quantized(w, mq.ROLE_WEIGHT, fmts[1])
+        first = _call(s, 0, X[0], W[0])
+        _close(s, 0, host(first), X[1], W[1], str(fmts))
+        assert torch.equal(_call(s, 0, X[0], W[0], fill=0), first)

@@ -135,3 +135,33 @@ def test_a_captured_step_replays_to_the_eager_results():
         for i, (got, want) in enumerate(zip(state(b), ref)):
             assert torch.equal(got, want), f"replay {k}: tensor {i}"
         eager.forward(X)  # the program's own work between the replays
+
+
+def test_two_blocks_on_two_streams_at_once():
+    n, size, c = 64, 10, 64
+    x, dy = _inputs(n, size, c)
+    X, DY = dev(x), dev(dy)
+
+    def steps(b):
+        for _ in range(3):
+            b.forward(X)
+            b.backward(X, DY)
+            b.step()
+
+    def state(b):
+        return (b.y, b.dx, b.dw, b.w, b.momentum, b.gamma, b.beta)
+
+    alone = [two_level_block.Block(n, size, c, seed=k) for k in (1, 2)]
+    for b in alone:
+        steps(b)
+    torch.cuda.synchronize()
+    both = [two_level_block.Block(n, size, c, seed=k) for k in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    for b, s in zip(both, streams):
+        with torch.cuda.stream(s):
+            steps(b)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        for i, (want, got) in enumerate(zip(state(a), state(b))):
+            assert torch.equal(got, want), f"tensor {i}"
