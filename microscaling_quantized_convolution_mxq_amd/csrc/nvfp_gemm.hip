@@ -233,6 +233,10 @@ hipError_t launch_values(const Task& a, const Task& b, hipStream_t st) {
 }
 
 // ---- products -----------------------------------------------------------------------------------
+// A value that all lanes share, in a scalar register (quotients are computed in
+// vector ones, and a load's address from those is a loop over its values).
+__device__ __forceinline__ int shared(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // Rows of an image of pixels, each the channels (64 cb) of a pixel's sample, moved by the taps of a step. Output row (r, c, n)
 // starts at pixel (r sr + r0, c sc + c0), and tap (i, j) is at (+-i, +-j) from there.
 struct Gather {
@@ -293,11 +297,11 @@ struct TapLoader {
   __device__ void init(const void* p, long long bytes, int row0, int n, int pitch, const Taps& taps, int step0, int wave, int lane) {
     rows.init(p, bytes, row0, n, pitch, wave, lane);
     t = taps;
-    const int tap = step0 / t.nc;
-    cb = step0 - tap * t.nc; i = tap / t.nj; j = tap - i * t.nj;
+    const int tap = shared(step0 / t.nc);
+    cb = step0 - tap * t.nc; i = shared(tap / t.nj); j = tap - i * t.nj;
   }
   __device__ void issue(int, uint8_t* lds, int wave) {
-    rows.issue(((t.k0 + t.si * i) * t.KW + t.l0 + t.sj * j) * t.nc + cb, lds, wave);
+    rows.issue(shared(((t.k0 + t.si * i) * t.KW + t.l0 + t.sj * j) * t.nc + cb), lds, wave);
     if (++cb == t.nc) {
       cb = 0;
       if (++j == t.nj) { j = 0; i++; }
@@ -514,15 +518,16 @@ __global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_conv_kernel(co
 // block scales in one dword, and makes 8 values with 16 instructions while the
 // other waves multiply. Each wave has all columns, so no value is made twice in
 // a workgroup. The other operand, small, comes as bf16.
+// Codes are read from LDS as vectors: for a struct the compiler waits until
+// every load is done, those of later steps too.
 // The input gradient of 3 x 3, stride 2 (160 x 160 x 32 x 128 from 80 x 80 x 32 x
-// 256, E2M1): 160 us with the weights' pass, 750 TFLOP/s, 288 by the kernel above
-// with its pass over both. Its products alone are 84 us at the rate of a large
-// matrix product, loads and stores without products 89: at two waves a SIMD
-// (registers for the sums) they overlap by half. Fewer rows or stages a
-// workgroup, and so more of these, change it by no more than 3 us.
-// 3 x 3 on 80 x 80 x 16 x 64 to 64 channels: 21 us with the weights' pass (25.6 by
-// the kernel above), of which 10 remain with one step of the nine; with tiles of
-// 128 rows the same.
+// 256, E2M1): 147 to 160 us with the clock, 288 by the kernel above with its pass
+// over both. Its products alone are 84 us at the rate of a large matrix product,
+// its stores 79 at a copy's: at two waves a SIMD (registers for the sums) they
+// overlap by half.
+// 3 x 3 on 80 x 80 x 16 x 64 to 64 channels: 18.7 us (19.2 and a pass of 6.4 by the
+// kernel above, here 4.0), of which 10 remain with one step of the nine; with
+// tiles of 128 rows the same.
 template <int F>
 struct CodeRows {
   static constexpr int RUN = run_bytes_of(F), SLOTS = 2 * RUN / 16;  // 16-byte slots of a row: 2 (4 bit) or 4 (8 bit)
@@ -550,12 +555,10 @@ struct CodeLoader {
   int coff[LC], ch[LC], cw[LC], soff[LS], sh[LS], sw[LS];
   int H, W, cpix, spix, dir, nj, nc, i, j, cb, crun[LC], runs, nCB;
   __device__ void init(const ConvArgs& a, const Gather& g, const Taps& t, int row0, int step0, int wave, int lane) {
-    codes = mma_rsrc(a.codes, a.codes_bytes);
-    scales = mma_rsrc(a.scales, a.scales_bytes);
     H = g.H; W = g.W; dir = g.dir; nj = t.nj; nc = t.nc;
     cpix = g.N * a.rbytes; spix = a.nPB * a.nCB; runs = a.runs; nCB = a.nCB;
-    const int tap = step0 / t.nc;
-    cb = step0 - tap * t.nc; i = tap / t.nj; j = tap - i * t.nj;
+    const int tap = shared(step0 / t.nc);
+    cb = step0 - tap * t.nc; i = shared(tap / t.nj); j = tap - i * t.nj;
     auto place = [&](int m, int& h, int& w, unsigned& n) {
       const unsigned px = fdiv((unsigned)m, g.dN), r = fdiv(px, g.dW), c = px - r * g.dW.d;
       n = (unsigned)m - px * g.dN.d;
@@ -587,12 +590,12 @@ struct CodeLoader {
 #pragma unroll
     for (int k = 0; k < LC; k++) {
       const bool in = (unsigned)(ch[k] + di) < (unsigned)H && (unsigned)(cw[k] + dj) < (unsigned)W && 2 * cb + crun[k] < runs;
-      load_lds16(codes, lds + (wave + 4 * k) * 1024, in ? coff[k] + cmove : kBeyond, cb * 2 * R::RUN);
+      load_lds16(codes, lds + (wave + 4 * k) * 1024, in ? coff[k] + cmove : kBeyond, shared(cb * 2 * R::RUN));
     }
 #pragma unroll
     for (int k = 0; k < LS; k++) {
       const bool in = (unsigned)(sh[k] + di) < (unsigned)H && (unsigned)(sw[k] + dj) < (unsigned)W && 8 * cb + (lane & 1) * 4 < nCB;
-      load_lds4(scales, lds + SCALES + (wave + 4 * k) * 256, in ? soff[k] + smove : kBeyond, cb * 8);
+      load_lds4(scales, lds + SCALES + (wave + 4 * k) * 256, in ? soff[k] + smove : kBeyond, shared(cb * 8));
     }
     if (++cb == nc) {
       cb = 0;
@@ -602,6 +605,7 @@ struct CodeLoader {
 };
 
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Eight values of piece kk of a run: words `w` of the run's codes, the four
 // scales in `s`. As f16, 4-bit elements take 4 conversions and 4 packed
@@ -673,6 +677,8 @@ __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
   constexpr int STRIPS = 4 * 32 * 40 * 4, KEPT = STRIPS + S::BM * 4;  // strips of 32 columns, and the tile's rows
   constexpr int FREE = (S::LDS - KEPT) / S::STAGE, PRE = FREE < ST - 1 ? FREE : ST - 1;
   static_assert(PRE >= 1, "a stage beside the strips");
+  constexpr int STORES = TM * TN * 4;  // of a wave with a whole tile
+  int held = 0;  // steps of the present tile whose loads stand before such stores
   float* const strips = reinterpret_cast<float*>(lds + S::LDS - KEPT);
   int* const rows = reinterpret_cast<int*>(lds + S::LDS - S::BM * 4);
   const MmaWave<S> me;
@@ -684,29 +690,34 @@ __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
 
   TileWalk walk(a.tiles * a.slices);
   CodeLoader<F, S::LC, S::LS, S::SCALES> la;
-  TapLoader<S::LB, 4> lb;
+  RowLoader<S::LB, 4> lb;
+  int first = 0, down = 0, right = 0;  // the other operand's row of a step: (first + i down + j right) nc + cb
   int which = 0, i0 = 0, j0 = 0, z = 0, n = 0;
+  const __amdgpu_buffer_rsrc_t codes = mma_rsrc(a.codes, a.codes_bytes), scales = mma_rsrc(a.scales, a.scales_bytes),
+                               other = mma_rsrc(a.b, a.b_bytes);
   auto issue = [&](int slot) {
-    uint8_t* const to = lds + slot * S::STAGE;
+    uint8_t* const to = lds + shared(slot * S::STAGE);
+    la.codes = codes; la.scales = scales; lb.rsrc = other;  // (the same for all tiles)
+    lb.issue(shared((first + la.i * down + la.j * right) * la.nc + la.cb), to + S::OTHER, wave);
     la.issue(to, wave, lane);
-    lb.issue(0, to + S::OTHER, wave);
   };
   // the next tile and its first loads; false: there is none
   auto next = [&]() {
     for (; walk.at < walk.end; walk.at += walk.step) {
-      z = walk.at / a.tiles;
-      const int at = walk.at - z * a.tiles, tile = at / a.nclass;
+      z = shared(walk.at / a.tiles);
+      const int at = walk.at - z * a.tiles, tile = shared(at / a.nclass);
       // (turned from place to place, or a workgroup whose step is a multiple of their number would always meet the same class)
-      which = (at + tile + (tile >> 4)) % a.nclass;
+      which = shared((at + tile + (tile >> 4)) % a.nclass);
       const Class& k = a.k[which];
       if (tile >= k.tiles) continue;
-      const int ti = tile / tn, steps = k.t.ni * k.t.nj * k.t.nc, s0 = (int)((long long)steps * z / a.slices);
+      const int ti = shared(tile / tn), steps = k.t.ni * k.t.nj * k.t.nc, s0 = shared((int)((long long)steps * z / a.slices));
       i0 = ti * S::BM;
       j0 = (tile - ti * tn) * S::BN;
-      n = (int)((long long)steps * (z + 1) / a.slices) - s0;
+      n = shared((int)((long long)steps * (z + 1) / a.slices)) - s0;
       if (n > 0) {
         la.init(a, k.g, k.t, i0, s0, wave, lane);
-        lb.init(a.b, a.b_bytes, j0, a.cols, a.b_pitch, k.t, s0, wave, lane);
+        lb.init(a.b, a.b_bytes, j0, a.cols, a.b_pitch, wave, lane);
+        first = k.t.k0 * k.t.KW + k.t.l0; down = k.t.si * k.t.KW; right = k.t.sj;
 #pragma unroll
         for (int s = 0; s < PRE; s++)
           if (s < n) issue(s);
@@ -726,8 +737,9 @@ __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
       if (s < n) issue(s);
     int slot = 0, fill = ST - 1;
     for (int s = 0; s < n; s++) {
-      if (s + ST - 2 < n) stage_ready<(ST - 2) * LPS>();
-      else stage_ready<0>();
+      if (s + ST - 2 >= n) stage_ready<0>();
+      else if (s < held) stage_ready<(ST - 2) * LPS + STORES>();
+      else stage_ready<(ST - 2) * LPS>();
       if (s + ST - 1 < n) issue(fill);
       const uint8_t* const from = lds + slot * S::STAGE;
       uint32_t w[TM][R::RUN / 4], sc[TM];
@@ -736,8 +748,8 @@ __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
         const int row = (wave * TM + i) * 32 + r;
 #pragma unroll
         for (int h = 0; h < R::RUN / 16; h++)
-          *reinterpret_cast<uint4*>(&w[i][4 * h]) =
-              *reinterpret_cast<const uint4*>(from + row * R::ROW + (((q * (R::RUN / 16) + h) ^ R::swizzle(row)) << 4));
+          *reinterpret_cast<u32x4*>(&w[i][4 * h]) =
+              *reinterpret_cast<const u32x4*>(from + row * R::ROW + (((q * (R::RUN / 16) + h) ^ R::swizzle(row)) << 4));
         sc[i] = *reinterpret_cast<const uint32_t*>(from + S::SCALES + row * 8 + q * 4);
       }
 #pragma unroll
@@ -760,6 +772,9 @@ __global__ __launch_bounds__(256, 2) void nvfp_codes_kernel(const ConvArgs a) {
     fill_rows<S>(a, a.k[which], i0, rows);
     float* const out = a.out + (a.slices == 1 ? 0 : z * a.slice);
     const int c0 = j0;
+    // Where every lane stores, every wave does so STORES times, and the stages asked for before that are waited for with the
+    // stores under way.
+    held = i0 + S::BM <= a.k[which].g.M && j0 + S::BN <= a.cols ? PRE : 0;
     more = next();
     lds_ready();  // the rows are known
     store_results<S, 1>(strips, rows, acc, me, scale, out, a.cols, c0);

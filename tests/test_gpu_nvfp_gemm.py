@@ -41,6 +41,8 @@ CODES = [
     (64, 250, 9, 9, 64, 3, 3, 1, 1, 1, 1), (4100, 320, 1, 1, 70, 1, 1, 1, 1, 0, 0), (7, 58, 40, 39, 30, 5, 3, 1, 2, 2, 0),
     (9, 27, 60, 61, 32, 1, 1, 2, 2, 0, 0), (33, 128, 23, 24, 224, 2, 2, 3, 1, 1, 0),
 ]
+# more tiles than the chip holds workgroups, which then take several: whole tiles, and a last one that is not
+MANY_TILES = [(64, 32, 64, 64, 96, 3, 3, 1, 1, 1, 1), (65, 96, 63, 65, 32, 3, 3, 1, 1, 1, 1), (64, 32, 64, 64, 64, 1, 1, 1, 1, 0, 0)]
 OPS = ("forward", "data", "weight")
 
 
@@ -121,7 +123,7 @@ def test_products_of_four_bit_codes(s):
         _close(s, op, host(_call(s, op, a[0], b[0])), a[1], b[1], "e2m1")
 
 
-@pytest.mark.parametrize("s", CODES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("s", CODES + MANY_TILES, ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("fmts", [(4, 4, 4), (0, 4, 1), (1, 2, 0)])
 def test_products_from_codes(s, fmts):
     for op, (a, b) in enumerate(_operands(s, *fmts, seed=200 + sum(s))):
