@@ -224,15 +224,17 @@ __device__ __forceinline__ void finish(const Group& g, const Mat& m, const Last&
   if (r0 >= mp || c0 >= (KIND <= kPoly ? mp : np)) return;  // (whole waves)
   if constexpr (KIND == kLast) {
     const int col = c0 + (lane & 31), row = r0 + (lane >> 5);
-    const long long pitch = last.tall ? 1 : m.cols, at = last.tall ? (long long)col * m.cols + row : (long long)row * m.cols + col;
+    const long long down = last.tall ? 1 : m.cols, right = last.tall ? m.cols : 1;
     float old[16];
+    if (g.update) {  // (all under way together, so none under a condition: places past the end read the last one)
 #pragma unroll
-    for (int e = 0; e < 16; e++) old[e] = g.update && row + 2 * e < last.real_m && col < last.real_n ? m.out[at + 2 * e * pitch] : 0.0f;
+      for (int e = 0; e < 16; e++) old[e] = m.out[min(row + 2 * e, last.real_m - 1) * down + min(col, last.real_n - 1) * right];
+    }
 #pragma unroll
     for (int e = 0; e < 16; e++) {
       const float o = strip[(lane & 31) * kStrip + (lane >> 5) + 2 * e] * (2.0f / kUp / kUp);
       if (row + 2 * e < last.real_m && col < last.real_n)
-        m.out[at + 2 * e * pitch] = g.update ? __builtin_fmaf(last.step, o, old[e] * last.keep) : o;
+        m.out[(row + 2 * e) * down + col * right] = g.update ? __builtin_fmaf(last.step, o, old[e] * last.keep) : o;
     }
   } else {
     const int c = (lane & 3) * 8;
