@@ -149,7 +149,7 @@ typedef struct {
 } mq_muon;
 
 /* The weights of one call: 1 .. MQ_UPDATE_GROUP_MAX matrices, which share
- * every launch. Arrays are HOST arrays, read during the call only. */
+ * launches. Arrays are HOST arrays, read during the call only. */
 #define MQ_UPDATE_GROUP_MAX 32
 
 /* Workspace (device bytes, 16-byte aligned) of the calls below for these
