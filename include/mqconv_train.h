@@ -85,7 +85,7 @@ int mqconv_layer_norm_backward_mx(const mq_layer_norm* ln, const float* dy, cons
  * with the scale byte 0x7F (NaN) makes every output that it is part of NaN. */
 typedef struct {
   const void* codes;           /* device, 16-byte aligned: the packed layout of the role */
-  const uint8_t* block_scales; /* device: E4M3 bytes (mqconv_nvfp_scales_bytes) */
+  const uint8_t* block_scales; /* device: E4M3 bytes (mqconv_nvfp_scales_bytes); between dwords some calls copy them */
   const float* tensor_scale;   /* device, 4-byte aligned: one value */
   mq_elem fmt;
   mq_role role;

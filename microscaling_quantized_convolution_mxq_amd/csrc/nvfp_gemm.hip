@@ -1088,14 +1088,30 @@ static hipError_t join(int slices, const float* part, float* out, long long n, c
   return launch_check();
 }
 
-// The gathered operand's codes where their kernel takes them.
-static bool use_codes(ConvArgs& a, const Sizes& s, const Codes& t) {
-  if (s.code_slices == 0 || ((uintptr_t)t.scales & 3u)) return false;
+// Bytes at any address to whole dwords.
+__global__ __launch_bounds__(256) void nvfp_align_kernel(const uint8_t* from, uint32_t* to, int n) {
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+    const uint8_t* const p = from + 4 * (long long)i;
+    to[i] = (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16 | (uint32_t)p[3] << 24;
+  }
+}
+
+// The gathered operand's codes where their kernel takes them, a rule on sizes and formats alone, so that no result depends on
+// an address: scales that start between dwords are copied first, to `spare`, the place of the 16-bit values that this kernel
+// does without (16 bytes for each scale's at least; rows of scales are whole dwords).
+static hipError_t use_codes(ConvArgs& a, const Sizes& s, const Codes& t, void* spare, hipStream_t st, bool& codes) {
+  codes = s.code_slices != 0;
+  if (!codes) return hipSuccess;
   a.codes = t.codes; a.scales = t.scales;
   const long long pixels = (long long)t.A * t.B;
   a.codes_bytes = pixels * t.P * t.rbytes; a.scales_bytes = pixels * t.nPB * t.nCB;
   a.rbytes = t.rbytes; a.runs = ceil_div(t.C, 32); a.nPB = t.nPB; a.nCB = t.nCB;
-  return true;
+  if (((uintptr_t)t.scales & 3u) == 0) return hipSuccess;
+  a.scales = static_cast<const uint8_t*>(spare);
+  const int n = (int)(a.scales_bytes / 4);
+  hipLaunchKernelGGL(nvfp_align_kernel, dim3((unsigned)std::min(ceil_div(n, 256), 2048)), dim3(256), 0, st, t.scales,
+                     static_cast<uint32_t*>(spare), n);
+  return launch_check();
 }
 
 template <int OP>
@@ -1151,11 +1167,13 @@ hipError_t launch_nvfp_forward(const Conv& c, const NvfpView& x, const NvfpView&
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
   ConvArgs a{};
   const Codes xc = codes_of(x, c.h * c.w, c.n, 1, c.cin);
-  const bool codes = use_codes(a, s, xc);
+  bool codes;
+  hipError_t e = use_codes(a, s, xc, xb, st, codes);
+  if (e != hipSuccess) return e;
   const bool half = codes && x.fmt == 4 && w.fmt == 4;
   Task wt = rows_task(codes_of(w, 1, c.cout, taps, c.cin), wb);
   wt.half = half;
-  hipError_t e = launch_values(wt, codes ? Task{} : rows_task(xc, xb), st);
+  e = launch_values(wt, codes ? Task{} : rows_task(xc, xb), st);
   if (e != hipSuccess) return e;
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * cp * 2; a.cols = c.cout;
   a.slices = codes ? s.code_slices : s.plan.slices; a.slice = (long long)ho * wo * c.n * c.cout;
@@ -1178,11 +1196,13 @@ hipError_t launch_nvfp_backward_data(const Conv& c, const NvfpView& dy, const Nv
   float* const part = reinterpret_cast<float*>(static_cast<char*>(ws) + up(s.a, 256) + up(s.b, 256));
   ConvArgs a{};
   const Codes yc = codes_of(dy, ho * wo, c.n, 1, c.cout);
-  const bool codes = use_codes(a, s, yc);
+  bool codes;
+  hipError_t e = use_codes(a, s, yc, yb, st, codes);
+  if (e != hipSuccess) return e;
   const bool half = codes && dy.fmt == 4 && w.fmt == 4;
   Task wt = across_task(codes_of(w, 1, c.cout, taps, c.cin), wb, 64);
   wt.half = half;
-  hipError_t e = launch_values(wt, codes ? Task{} : rows_task(yc, yb), st);
+  e = launch_values(wt, codes ? Task{} : rows_task(yc, yb), st);
   if (e != hipSuccess) return e;
   a.b = wb; a.b_bytes = s.b; a.b_pitch = taps * kp * 2; a.cols = c.cin;
   a.slices = codes ? s.code_slices : s.plan.slices; a.slice = (long long)c.h * c.w * c.n * c.cin;

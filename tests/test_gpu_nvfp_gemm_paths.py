@@ -13,10 +13,11 @@ import pytest
 import torch
 
 import microscaling_quantized_convolution_mxq_amd as mq
-from gpu_common import host, say
-from test_gpu_nvfp_gemm import CODES, E, LINEAR, OPS, _call, _inputs, _quantized, _reference, _sum_extent
+from gpu_common import host, say, workspace
+from test_gpu_nvfp_gemm import CODES, E, LINEAR, MANY_TILES, OPS, _call, _inputs, _operands, _quantized, _reference, _sum_extent
 
 pytestmark = pytest.mark.gpu
+FNS = (mq.mqconv_nvfp_forward, mq.mqconv_nvfp_backward_data, mq.mqconv_nvfp_backward_weight)
 
 
 def _product64(s, op, a, b):
@@ -119,3 +120,53 @@ def test_nan_blocks_of_every_format(s, fx, fw):
         total = np.asarray(_reference(s, op, np.abs(a[1]), np.abs(b[1]))).reshape(got.shape)
         tol = ((2.0 ** -22 + E) * _sum_extent(s, op) / 16 + 64 * E) * total + 5 * E * np.abs(ref) + 2.0 ** -149
         assert (np.abs(got.astype(np.float64) - ref) <= tol)[clean].all(), label
+
+
+def _moved(t, offset):
+    """The same operand with its block scales `offset` bytes from an aligned address, NaN bytes around them."""
+    big = torch.full((t.scales.numel() + 32,), 0x7F, dtype=torch.uint8, device="cuda")
+    view = big[16 + offset:16 + offset + t.scales.numel()]
+    view.copy_(t.scales)
+    return mq.NvfpTensor(t.codes, view, t.tensor_scale, t.fmt, t.role, t.dims)
+
+
+@pytest.mark.parametrize("s", [CODES[0], CODES[1], CODES[3], CODES[4], CODES[5], MANY_TILES[1], LINEAR[2], LINEAR[13]],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("fmts", [(4, 4, 4), (0, 4, 1), (2, 3, 2)])
+def test_results_do_not_depend_on_the_address_of_scales(s, fmts):
+    for op, (a, b) in enumerate(_operands(s, *fmts, seed=500 + sum(s))):
+        a, b = a[0], b[0]
+        ref = _call(s, op, a, b)
+        for k, m in ((1, 0), (2, 3), (3, 1)):
+            say(f"{OPS[op]} {s} {fmts}: scales at {k} and {m}")
+            for fill in (0xFF, 0):
+                assert torch.equal(_call(s, op, _moved(a, k), _moved(b, m), fill=fill), ref)
+
+
+def test_captured_calls_with_scales_at_odd_addresses():
+    s = CODES[1]
+    first, second = (_operands(s, 4, 4, 4, seed) for seed in (61, 62))
+    for op in range(2):
+        used = [_moved(t[0], 1 + op) for t in first[op]]
+        used = [mq.NvfpTensor(t.codes.clone(), t.scales, t.tensor_scale.clone(), t.fmt, t.role, t.dims) for t in used]
+        ws = workspace(mq.mqconv_nvfp_gemm_workspace_bytes(s, op, 4, 4))
+        refs = [_call(s, op, p[op][0][0], p[op][1][0]) for p in (first, second)]
+        out = torch.empty_like(refs[0])
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.stream(stream):
+            FNS[op](s, *used, out, ws)
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=stream):
+                FNS[op](s, *used, out, ws)
+        for k in (1, 0, 0, 1):
+            for t, new in zip(used, (first, second)[k][op]):
+                for name in ("codes", "scales", "tensor_scale"):
+                    getattr(t, name).copy_(getattr(new[0], name))
+            out.fill_(float("nan"))
+            ws.fill_(0xFF)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, refs[k])
+            FNS[op](s, *used, out, ws)
