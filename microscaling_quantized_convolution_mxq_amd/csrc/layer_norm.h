@@ -14,7 +14,7 @@ struct LnArgs {
   const float *x, *add;            // add: residual (forward) or the skip path's gradient (backward); may be null
   const float *dy, *gamma, *beta;  // gamma, beta may be null
   const float *mean_in, *rstd_in;  // backward
-  float *sum, *mean, *rstd;        // forward: x + add, and the statistics (may be null)
+  float *sum, *mean, *rstd;        // forward: x + add (given exactly where add is), and the statistics (may be null)
   float* out;                      // y or dx; null: the rows' parameters instead (rows: mean, rstd or `row`)
   LnRow* row;                      // backward without dx
   float2* part;                    // backward: sums of dy and dy xh of each workgroup's rows [parts][C]

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(threads_of<T>()) void ln_kernel(const LnArgs a) {
         v[q][i] = ADD ? next[q][i] + more[q][i] : next[q][i];
         s[0] += has<T, FULL>(q, i, t, a.C) ? (double)v[q][i] : 0.0;
       }
-    if (ADD && a.sum) store_row<T, Q, FULL>(a.sum + at, a.C, t, v);
+    if (ADD) store_row<T, Q, FULL>(a.sum + at, a.C, t, v);
     if (rn != r) {
       load_row<T, Q, FULL>(a.x + (long long)rn * a.C, a.C, t, next);
       if (ADD) load_row<T, Q, FULL>(a.add + (long long)rn * a.C, a.C, t, more);
@@ -118,17 +118,15 @@ __global__ __launch_bounds__(1024) void ln_long_kernel(const LnArgs a) {
     double s[1] = {0};
     for (int c = threadIdx.x; c < a.C; c += 1024) {
       const float v = ADD ? x[c] + a.add[at + c] : x[c];
-      if (ADD && a.sum) a.sum[at + c] = v;
+      if (ADD) a.sum[at + c] = v;
       s[0] += v;
     }
-    // (a thread reads back what it wrote itself; without a sum the addends are added again)
     row_sums<1024, 1>(s, 0);
     const double mean = s[0] * a.inv;
-    const float* from = ADD && a.sum ? a.sum + at : x;
-    const float* more = ADD && !a.sum ? a.add + at : nullptr;
+    const float* from = ADD ? a.sum + at : x;  // (a thread reads back what it wrote itself)
     s[0] = 0;
     for (int c = threadIdx.x; c < a.C; c += 1024) {
-      const double d = (double)(more ? from[c] + more[c] : from[c]) - mean;
+      const double d = (double)from[c] - mean;
       s[0] = __builtin_fma(d, d, s[0]);
     }
     row_sums<1024, 1>(s, 1);
@@ -139,8 +137,7 @@ __global__ __launch_bounds__(1024) void ln_long_kernel(const LnArgs a) {
     }
     if (a.out)
       for (int c = threadIdx.x; c < a.C; c += 1024)
-        a.out[at + c] = ln_value(more ? from[c] + more[c] : from[c], m, rs, a.gamma ? a.gamma[c] : 1.0f,
-                                 a.beta ? a.beta[c] : 0.0f);
+        a.out[at + c] = ln_value(from[c], m, rs, a.gamma ? a.gamma[c] : 1.0f, a.beta ? a.beta[c] : 0.0f);
   }
 }
 

@@ -204,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void ln_mx_kernel(const LnArgs a, const T
         if constexpr (ADD) v[k][0][e] += more[k][0][e];
         s[0] += has<T, true>(0, e, t, a.C) ? (double)v[k][0][e] : 0.0;
       }
-      if (ADD && a.sum && row_ok) store_row<T, 1, true>(a.sum + row * a.C, a.C, t, v[k]);
+      if (ADD && row_ok) store_row<T, 1, true>(a.sum + row * a.C, a.C, t, v[k]);
       row_sums<T, 1>(s, 0);
       const double mean = s[0] * a.inv;
       s[0] = 0;

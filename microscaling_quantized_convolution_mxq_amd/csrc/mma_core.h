@@ -340,21 +340,6 @@ __device__ __forceinline__ void mma_loop_wide(uint8_t* lds, LA& la, LB& lb, int 
   if constexpr (LOW) mma_add<S>(acc, low);
 }
 
-// f(row, column, quad): the four values of rows row .. row + 3 in one column, of a wave's results.
-template <class S, class F>
-__device__ __forceinline__ void mma_results(const v16f (&acc)[S::TM][S::TN], int wave, int lane, F&& f) {
-  const int wm = wave / S::WN, wn = wave % S::WN;
-#pragma unroll
-  for (int i = 0; i < S::TM; i++)
-#pragma unroll
-    for (int j = 0; j < S::TN; j++, __builtin_amdgcn_sched_barrier(0))  // (a few results in registers at a time)
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const float v[4] = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
-        f((wm * S::TM + i) * 32 + 8 * e + 4 * (lane >> 5), (wn * S::TN + j) * 32 + (lane & 31), v);
-      }
-}
-
 // Workgroups go to the eight XCDs in turn; this gives each XCD a contiguous
 // range of the n tiles, which share operand rows in its L2.
 __device__ __forceinline__ int xcd_tile(int b, int n) {

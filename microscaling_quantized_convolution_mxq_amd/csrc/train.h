@@ -12,7 +12,7 @@ struct LnShape {
   float eps;
 };
 size_t layer_norm_workspace_bytes(const LnShape& s, int op);
-// exactly one of y and yq (yq.codes) is given; residual, sum, mean, rstd may be null (sum is given where yq and residual are)
+// exactly one of y and yq (yq.codes) is given; residual, mean, rstd may be null; sum is given exactly where residual is
 hipError_t launch_layer_norm(const LnShape& s, const float* x, const float* residual, const float* gamma,
                              const float* beta, float* sum, float* y, const MxOutView& yq, float* mean, float* rstd,
                              void* ws, hipStream_t st);
