@@ -38,8 +38,10 @@ extern "C" {
  *   dbeta[c] = sum dy;  dgamma[c] = sum dy * xh        (over H, W, N)
  * dskip: the gradient that reaches s on the skip path, or NULL. dx is the
  * gradient of x and of residual. dgamma, dbeta may be NULL. All sums are fp64;
- * a workgroup's share of dgamma and dbeta is kept in fp32. A row that holds a
- * NaN or an infinity is NaN; other rows are not touched by it. */
+ * a workgroup's share of dgamma and dbeta is kept in fp32. y is made of mean
+ * and rstd as they are kept, rounded to fp32; they and x - mean have to stay in
+ * fp32's normal range. A row that holds a NaN or an infinity is NaN; other rows
+ * are not touched by it. */
 typedef struct {
   int32_t h, w, n, c; /* all >= 1 */
   float eps;          /* finite, >= 0, else MQ_ERR_UNSUPPORTED */
@@ -82,7 +84,8 @@ int mqconv_layer_norm_backward_mx(const mq_layer_norm* ln, const float* dy, cons
  * sums along either of their sides. An element's value is value(q) * B * T;
  * value(q) * B is exact in 16 bits, products are exact, sums fp32 (products
  * below 2^-26 of a sum may be lost in it), and T T' is applied to them. A block
- * with the scale byte 0x7F (NaN) makes every output that it is part of NaN. */
+ * with the scale byte 0x7F (NaN) makes every output that it is part of NaN;
+ * outputs that pair its values with zero padding alone are left open. */
 typedef struct {
   const void* codes;           /* device, 16-byte aligned: the packed layout of the role */
   const uint8_t* block_scales; /* device: E4M3 bytes (mqconv_nvfp_scales_bytes); between dwords some calls copy them */
@@ -119,8 +122,9 @@ int mqconv_nvfp_backward_weight(const mq_conv* cv, mq_nvfp dyq, mq_nvfp xq, floa
  * so a singular value x becomes p(x) = a x + b x^3 + c x^5, step after step,
  * and the singular vectors stay: a few steps bring every singular value near
  * 1 that is not far below the largest. |U|_F and the products' sums are held
- * in 32 bits or more; every factor of a product in two f16 parts, 22 bits or
- * more, so results have the accuracy of fp32 products.
+ * in 32 bits or more; every factor of a product in two f16 parts, off by 2^-22
+ * of itself or by 2^-40 (2^-39 for the factor of a step, a I + b S + c S^2),
+ * whichever is more, so results have the accuracy of fp32 products.
  * Parts of U whose share of |U|_F is below 2^-40 may be lost; a NaN or an
  * infinity in U makes its whole result NaN; U = 0 gives 0 (NaN with eps = 0,
  * as the formula does). */

@@ -19,7 +19,8 @@
 // The gradient of 512 x 16 x 4096: 78 us for 403 MB (5.1 TB/s, a copy's rate); 7 x 9
 // x 3 x 45 with a residual: 3.3 us, latency.
 // Rows of more channels than a workgroup's registers hold are read once for
-// every sum (they stay in the caches, being one row a workgroup).
+// every sum, from the caches after the first time (one row a workgroup); their
+// gradient's column sums are a pass of its own over dy and x.
 #include <algorithm>
 
 #include "layer_norm_rows.h"
@@ -30,13 +31,20 @@ namespace mq {
 
 namespace {
 
-constexpr int kWide = 8192;      // most channels of a row held in registers, forward
-constexpr int kWideGrad = 4096;  // and backward, which holds two tensors and the columns' sums
+// Most channels of a row held in registers: forward, 512 threads of 16 values;
+// backward, which holds two tensors and the columns' sums (32 registers of eight
+// values), 512 of 8. Whole calls with rows held and with rows read again: forward of
+// 256 x 16 x 8192 50.7 and 105.6 us; gradient of 512 x 16 x 4096 78.7 and 269, of
+// 512 x 16 x 2048 43.3 and 170. Above these: forward of 512 x 16 x 12288 330 us
+// (805 MB), gradient of 256 x 16 x 8192 239 (403 MB).
+constexpr int kWide = 8192;
+constexpr int kWideGrad = 4096;
 // Most workgroups of the gradient's pass, each of which leaves a row of column
 // sums: two a compute unit, one for rows of more than 1024 channels, whose
-// workgroups have more threads and more loads under way. Each more costs its row
-// (512 x 16 x 4096: 77.8 us with 256, 84.0 with 512, 95.3 with 1024; 20 x 20
-// x 128 x 256: 47.1, 36.5 and 39.4).
+// workgroups have more threads and more loads under way. Each more costs its row.
+// Whole calls: 512 x 16 x 4096 with 128, 256, 512 and 1024 workgroups 99.7, 79.0,
+// 83.8 and 93.3 us; with 256, 512 and 1024, 512 x 16 x 1024 32.5, 26.7 and 28.8,
+// 20 x 20 x 128 x 256 with a skip path 54.9, 43.8 and 48.5, to E5M2 63.0, 44.4 and 46.7.
 constexpr int kParts = 512, kPartsWide = 256;
 
 template <int T>

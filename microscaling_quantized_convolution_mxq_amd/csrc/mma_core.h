@@ -6,8 +6,9 @@
 // read in steps of 128 bytes of every row:
 //   Bf16:   64 values;
 //   Split:  32 values as 32 f16 high parts, then their 32 low parts:
-//           a = ah + al with ah = f16(a), al = f16(a - ah), 22 bits or more,
-//           a b = ah bh + ah bl + al bh (al bl, below 2^-22 of it, is left out).
+//           a = ah + al with ah = f16(a), al = f16(a - ah), off by at most 2^-22
+//           of a, or by 2^-25 where that is more (f16's smallest values are 2^-24
+//           apart), a b = ah bh + ah bl + al bh (al bl, below 2^-22 of it, is left out).
 // A step of a tile is [row][8] chunks of 16 bytes in LDS, written by loads that
 // go to LDS directly. Chunk c of row r is in slot c ^ ((r >> 1) & 7): a row is
 // half of the 64 banks, so the sixteen rows that an operand read touches at one

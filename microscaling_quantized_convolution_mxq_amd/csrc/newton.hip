@@ -3,19 +3,21 @@
 // for a number of steps, with U the gradient or the momentum that the first
 // pass updates. X is m x n with m <= n (the transpose of a tall matrix).
 //
-// The result has fp32's accuracy: every product's factors are f16 pairs (22
-// bits, mma_core.h), summed in fp32 by the f16 matrix units, which at three
+// The result has fp32's accuracy: every product's factors are f16 pairs
+// (mma_core.h), summed in fp32 by the f16 matrix units, which at three
 // products for one are five times as fast as the fp32 ones. Values are stored
-// times a power of two that keeps them within f16's range and their low parts
-// above its subnormals: the steps are refused unless |X| and |A| stay below 2
-// and |B| below 4 (the polynomial's range, checked on the host), so X and A
-// are stored times 2^15 and B times 2^14.
+// times the largest power of two that keeps them within f16's range: the steps
+// are refused unless |X| and |A| stay below 2 and |B| below 4 (the polynomial's
+// range, checked on the host), so X and A are stored times 2^15 and B times
+// 2^14. A stored value is off by 2^-22 of itself, or, as low parts may be f16
+// subnormals, by 2^-40 (B: 2^-39): more than that for entries below 2^-18 (2^-17),
+// which are about one in a hundred of X0 at 2048 x 4096.
 // A and A^2 are symmetric: tiles on and above the diagonal are computed, and
 // written on both sides. X is kept in both orientations ([m][n] for A, [n][m]
 // for the product with B), since an operand's rows run along k.
 // The matrices of a call share the launches of a product, one for each size of
 // tile that it needs (a network's layers are small).
-// 2048 x 4096, 5 steps: 1070 us, 845 TFLOP/s of f16 products with everything; 27
+// 2048 x 4096, 5 steps: 1090 us, 830 TFLOP/s of f16 products with everything; 27
 // layers of 16 x 27 to 256 x 1152: 149 us, 17 kernels of 7 to 11 us one after the
 // other, which launches and the first loads and last stores take.
 #include <math.h>

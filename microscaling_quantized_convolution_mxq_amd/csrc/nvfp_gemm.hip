@@ -521,10 +521,11 @@ __global__ __launch_bounds__(S::THREADS, waves_of<S>()) void nvfp_conv_kernel(co
 // Codes are read from LDS as vectors: for a struct the compiler waits until
 // every load is done, those of later steps too.
 // The input gradient of 3 x 3, stride 2 (160 x 160 x 32 x 128 from 80 x 80 x 32 x
-// 256, E2M1): 147 to 160 us with the clock, 288 by the kernel above with its pass
-// over both. Its products alone are 84 us at the rate of a large matrix product,
-// its stores 79 at a copy's: at two waves a SIMD (registers for the sums) they
-// overlap by half.
+// 256, E2M1): 149 us once the clock has settled (140 at the least, 190 to 207 for
+// some milliseconds after the first calls), 288 by the kernel above with its pass over
+// both; a call with the weights' pass 154, of E5M2 by E4M3 168. Its products alone
+// are 84 us at the rate of a large matrix product, its stores 79 at a copy's: at two
+// waves a SIMD (registers for the sums) they overlap by half.
 // 3 x 3 on 80 x 80 x 16 x 64 to 64 channels: 18.7 us (19.2 and a pass of 6.4 by the
 // kernel above, here 4.0), of which 10 remain with one step of the nine; with
 // tiles of 128 rows the same.

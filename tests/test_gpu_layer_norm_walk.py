@@ -71,3 +71,13 @@ def test_mx_tiles_of_several_turns(shape, fmt):
         ref = mq.MxTensor.empty(mq.ROLE_GRAD, fmt, bp, shape)
         mq.mqconv_quantize(dx, ref)
         _same_codes(t, ref, f"dx {shape}")
+
+
+@pytest.mark.parametrize("shape", [(7, 9, 3, 45), (1, 3, 5, 1024), (1, 1, 3, 20000)], ids=str)
+@pytest.mark.parametrize("size", [1e37, 1e-36])
+def test_values_near_the_ends_of_the_range(shape, size):
+    """x - mean up to 1e38 and rstd of 1e-37; 1e-36 and 1e36, with eps = 0: the ends of what fp32's normal range allows."""
+    x, _, _, gamma, beta = _inputs(shape, 15)
+    x = (x * np.float32(size)).astype(np.float32)
+    got = _forward(shape, dev(x), dev(gamma), dev(beta), eps=0.0)
+    _check_forward(x, gamma, beta, got, eps=0.0)
