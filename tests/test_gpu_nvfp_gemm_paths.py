@@ -14,7 +14,7 @@ import torch
 
 import microscaling_quantized_convolution_mxq_amd as mq
 from gpu_common import host, say, workspace
-from test_gpu_nvfp_gemm import CODES, E, LINEAR, MANY_TILES, OPS, _call, _inputs, _operands, _quantized, _reference, _sum_extent
+from test_gpu_nvfp_gemm import CODES, E, LINEAR, MANY_TILES, OPS, _call, _close, _inputs, _operands, _quantized, _reference, _sum_extent
 
 pytestmark = pytest.mark.gpu
 FNS = (mq.mqconv_nvfp_forward, mq.mqconv_nvfp_backward_data, mq.mqconv_nvfp_backward_weight)
@@ -78,6 +78,30 @@ def test_largest_tiles_of_several_taps(s, op, fa, fb):
     x, w, dy = _inputs(s, 400 + sum(s))
     a = _quantized(x, mq.ROLE_ACT, fa) if op == 0 else _quantized(dy, mq.ROLE_GRAD, fa)
     _check(s, op, a, _quantized(w, mq.ROLE_WEIGHT, fb), f"{fa} by {fb}")
+
+
+# Sums in slices together with classes of rows: four classes of 1 to 4 taps, nine of them (two launches), some that no tap
+# reaches; the largest tiles in slices; all from codes and from 16-bit values
+SLICED = [((8, 64, 25, 27, 512, 3, 3, 2, 2, 1, 1), 1), ((8, 64, 26, 25, 320, 5, 5, 3, 3, 2, 1), 1),
+          ((8, 64, 26, 25, 1024, 2, 2, 3, 3, 1, 1), 1), ((9, 130, 22, 23, 600, 3, 2, 8, 1, 0, 1), 1),
+          ((32, 256, 40, 40, 256, 3, 3, 1, 1, 1, 1), 0)]
+
+
+@pytest.mark.parametrize("s,op", SLICED, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else OPS[v])
+@pytest.mark.parametrize("fa,fb", [(4, 4), (0, 1), (2, 4)])
+def test_slices_of_classes_and_of_large_tiles(s, op, fa, fb):
+    x, w, dy = _inputs(s, 600 + sum(s))
+    a = _quantized(x, mq.ROLE_ACT, fa) if op == 0 else _quantized(dy, mq.ROLE_GRAD, fa)
+    _check(s, op, a, _quantized(w, mq.ROLE_WEIGHT, fb), f"{fa} by {fb}")
+
+
+@pytest.mark.parametrize("n,cin,cout", [(20, 40, 52000), (300, 64, 51300), (3, 5, 60001)])
+def test_weight_gradient_of_many_outputs(n, cin, cout):
+    """Tall tiles: few columns of dW and tens of thousands of rows."""
+    s = (n, cin, 1, 1, cout, 1, 1, 1, 1, 0, 0)
+    x, _, dy = _inputs(s, n)
+    a, b = _quantized(dy, mq.ROLE_GRAD, 4), _quantized(x, mq.ROLE_ACT, 1)
+    _close(s, 2, host(_call(s, 2, a[0], b[0])), a[1], b[1], "tall")
 
 
 @pytest.mark.parametrize("s", [LINEAR[2], LINEAR[5], LINEAR[13], CODES[1], CODES[5]], ids=lambda s: "x".join(map(str, s)))
