@@ -194,3 +194,24 @@ def test_captured_calls_with_scales_at_odd_addresses():
             torch.cuda.synchronize()
             assert torch.equal(out, refs[k])
             FNS[op](s, *used, out, ws)
+
+
+def test_injected_failures_with_scales_at_odd_addresses():
+    """The launches: the scales' copy, the weights' values, the product, and, of the forward, the join of its slices."""
+    s = CODES[3]
+    for op, (a, b) in enumerate(_operands(s, 4, 4, 4, 63)[:2]):
+        ref, moved = _call(s, op, a[0], b[0]), _moved(a[0], 3)
+        try:
+            launches = 4 - op
+            for k in range(1, launches + 2):
+                mq.mqconv_inject_launch_failure(k)
+                if k <= launches:
+                    with pytest.raises(mq.MqConvError) as e:
+                        _call(s, op, moved, b[0])
+                    assert e.value.status == -7
+                else:
+                    got = _call(s, op, moved, b[0])
+                    mq.mqconv_inject_launch_failure(0)
+                    assert torch.equal(got, ref)
+        finally:
+            mq.mqconv_inject_launch_failure(0)
